@@ -8,7 +8,9 @@ use; a missing library is an error, never a fallback.
 from .binding import (GEMM_EINVAL, GEMM_ELAUNCH, GEMM_MAX_K, GEMM_OK, GemmError, gemm_nt,
                       gemm_nt_f16, gemm_nt_f16_strerror, gemm_nt_f16_tile,
                       gemm_nt_f16_tile_coord)
+from .moe import MoeLayer
+from .w4 import W4Weight, dequantize_w4, gemm_nt_w4, quantize_w4
 
 __all__ = ["gemm_nt", "gemm_nt_f16", "gemm_nt_f16_strerror", "gemm_nt_f16_tile",
            "gemm_nt_f16_tile_coord", "GemmError", "GEMM_OK", "GEMM_EINVAL", "GEMM_ELAUNCH",
-           "GEMM_MAX_K"]
+           "GEMM_MAX_K", "W4Weight", "quantize_w4", "dequantize_w4", "gemm_nt_w4", "MoeLayer"]

@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in ``include/gemm_nt_f16.h``.
+"""Python binding of the C ABI in ``include/gemm_nt_f16.h``,
+``include/gemm_nt_w4.h`` and ``include/moe_nt.h``.
 
 Argument marshalling only: every step of the GEMM runs in the HIP kernels of
 ``libgemm18.so``.  PyTorch supplies device memory and the current stream.
@@ -20,12 +21,26 @@ GEMM_MAX_K = 4194303
 GEMM_FP8_E4M3 = 0
 GEMM_FP8_E5M2 = 1
 
-# Every symbol the header declares.
+GEMM_T_F16 = 0
+GEMM_T_BF16 = 1
+MOE_RENORMALIZE = 1
+
+# Every symbol the headers declare.
 EXPORTS = ("gemm_nt_f16", "gemm_nt_f16_strerror", "gemm_nt_f16_tile", "gemm_nt_f16_tile_coord",
            "gemm_nt_bf16", "gemm_nt_f16_ex", "gemm_nt_f16_ws", "gemm_nt_f16_ws_size", "gemm_nt_f16_ws_tile",
            "gemm_nt_f16_ws_items", "gemm_nt_fp8", "gemm_nt_fp8_cs", "gemm_nt_fp8_tile",
            "gemm_nt_f16_kernel", "gemm_nt_f16_ws_noalloc", "gemm_nt_f16_acc16",
-           "gemm_nt_f16_acc16_kernel")
+           "gemm_nt_f16_acc16_kernel", "gemm_w4_packed_bytes", "gemm_w4_quantize",
+           "gemm_w4_dequantize", "gemm_nt_w4", "gemm_nt_w4_ws_size", "moe_nt_route",
+           "moe_nt_experts", "moe_nt_layer", "moe_nt_ws_size")
+
+
+class moe_nt_weights(ctypes.Structure):
+    """``moe_nt_weights`` of include/moe_nt.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("router", "w13", "w13_scales", "w13_zeros", "w2",
+                                               "w2_scales", "w2_zeros")] + [
+        (n, ctypes.c_int64) for n in ("experts", "hidden", "inner")] + [
+        (n, ctypes.c_int32) for n in ("group", "dtype")]
 
 
 class GemmError(RuntimeError):
@@ -94,6 +109,26 @@ def lib():
     L.gemm_nt_fp8_cs.restype = ctypes.c_int
     L.gemm_nt_fp8_tile.argtypes = [i64, i64, i64, ctypes.c_int, ip, ip]
     L.gemm_nt_fp8_tile.restype = ctypes.c_int
+    ci = ctypes.c_int
+    L.gemm_w4_packed_bytes.argtypes = [i64, i64]
+    L.gemm_w4_packed_bytes.restype = i64
+    L.gemm_w4_quantize.argtypes = [vp, vp, vp, vp, i64, i64, i64, ci, ci, vp]
+    L.gemm_w4_quantize.restype = ci
+    L.gemm_w4_dequantize.argtypes = [vp, vp, vp, vp, i64, i64, i64, ci, ci, vp]
+    L.gemm_w4_dequantize.restype = ci
+    L.gemm_nt_w4.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, ci, ci, vp, i64, vp]
+    L.gemm_nt_w4.restype = ci
+    L.gemm_nt_w4_ws_size.argtypes = [i64, i64, i64]
+    L.gemm_nt_w4_ws_size.restype = i64
+    mw = ctypes.POINTER(moe_nt_weights)
+    L.moe_nt_route.argtypes = [mw, vp, vp, vp, i64, i64, ci, ci, vp, i64, vp]
+    L.moe_nt_route.restype = ci
+    L.moe_nt_experts.argtypes = [mw, vp, vp, vp, vp, i64, i64, i64, ci, vp, i64, vp]
+    L.moe_nt_experts.restype = ci
+    L.moe_nt_layer.argtypes = [mw, vp, vp, vp, vp, i64, i64, i64, ci, ci, vp, i64, vp]
+    L.moe_nt_layer.restype = ci
+    L.moe_nt_ws_size.argtypes = [i64, mw, ci]
+    L.moe_nt_ws_size.restype = i64
     _lib = L
     return L
 
@@ -235,6 +270,62 @@ def gemm_nt_fp8_tile(M: int, N: int, K: int, aligned16: bool = True):
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_nt_fp8_tile")
     return bm.value, bn.value
+
+
+def gemm_w4_packed_bytes(N: int, K: int) -> int:
+    return lib().gemm_w4_packed_bytes(N, K)
+
+
+def gemm_w4_quantize(W: int, Q: int, S: int, Z: int, N: int, K: int, ldw: int, group: int,
+                     dtype: int, stream: int = 0) -> int:
+    """Raw call of the quantisation (Z: 0 for none); returns the C return code."""
+    return lib().gemm_w4_quantize(W or None, Q or None, S or None, Z or None, N, K, ldw, group,
+                                  dtype, stream or None)
+
+
+def gemm_w4_dequantize(Q: int, S: int, Z: int, W: int, N: int, K: int, ldw: int, group: int,
+                       dtype: int, stream: int = 0) -> int:
+    """Raw call of its reversal; returns the C return code."""
+    return lib().gemm_w4_dequantize(Q or None, S or None, Z or None, W or None, N, K, ldw, group,
+                                    dtype, stream or None)
+
+
+def gemm_nt_w4(A: int, Q: int, S: int, Z: int, D: int, M: int, N: int, K: int, lda: int, ldd: int,
+               group: int, dtype: int, workspace: int = 0, ws_bytes: int = 0,
+               stream: int = 0) -> int:
+    """Raw call of the product with a 4-bit weight; returns the C return code."""
+    return lib().gemm_nt_w4(A or None, Q or None, S or None, Z or None, D or None, M, N, K, lda,
+                            ldd, group, dtype, workspace or None, ws_bytes, stream or None)
+
+
+def gemm_nt_w4_ws_size(M: int, N: int, K: int) -> int:
+    return lib().gemm_nt_w4_ws_size(M, N, K)
+
+
+def moe_nt_route(w: moe_nt_weights, X: int, ids: int, weights: int, T: int, ldx: int, topk: int,
+                 flags: int, workspace: int, ws_bytes: int, stream: int = 0) -> int:
+    """Raw call of the router; returns the C return code."""
+    return lib().moe_nt_route(w, X or None, ids or None, weights or None, T, ldx, topk, flags,
+                              workspace or None, ws_bytes, stream or None)
+
+
+def moe_nt_experts(w: moe_nt_weights, X: int, ids: int, weights: int, D: int, T: int, ldx: int,
+                   ldd: int, topk: int, workspace: int, ws_bytes: int, stream: int = 0) -> int:
+    """Raw call of the experts' products; returns the C return code."""
+    return lib().moe_nt_experts(w, X or None, ids or None, weights or None, D or None, T, ldx,
+                                ldd, topk, workspace or None, ws_bytes, stream or None)
+
+
+def moe_nt_layer(w: moe_nt_weights, X: int, D: int, ids: int, weights: int, T: int, ldx: int,
+                 ldd: int, topk: int, flags: int, workspace: int, ws_bytes: int,
+                 stream: int = 0) -> int:
+    """Raw call of the whole layer; returns the C return code."""
+    return lib().moe_nt_layer(w, X or None, D or None, ids or None, weights or None, T, ldx, ldd,
+                              topk, flags, workspace or None, ws_bytes, stream or None)
+
+
+def moe_nt_ws_size(T: int, w: moe_nt_weights, topk: int) -> int:
+    return lib().moe_nt_ws_size(T, w, topk)
 
 
 # ---- tensor-level convenience ----------------------------------------------

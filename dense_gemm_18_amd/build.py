@@ -13,8 +13,10 @@ CSRC = PKG / "csrc"
 # compile in parallel.
 SOURCES = [CSRC / "gemm_nt_f16.hip", CSRC / "gemm_nt_f16_ex.hip", CSRC / "gemm_nt_bf16.hip",
            CSRC / "gemm_nt_fp8.hip", CSRC / "gemm_nt_fp8_b5.hip", CSRC / "gemm_nt_f16_noalloc.hip",
-           CSRC / "gemm_nt_f16_acc16.hip"]
-HEADERS = [CSRC / "gemm_kernels.h", CSRC / "gemm_fp8.h", ROOT / "include" / "gemm_nt_f16.h"]
+           CSRC / "gemm_nt_f16_acc16.hip", CSRC / "gemm_nt_w4.hip", CSRC / "gemm_nt_w4_f16.hip",
+           CSRC / "gemm_nt_w4_bf16.hip", CSRC / "moe_nt.hip", CSRC / "moe_nt_f16.hip",
+           CSRC / "moe_nt_bf16.hip"]
+HEADERS = [*CSRC.glob("*.h"), *(ROOT / "include").glob("*.h")]
 LIB = PKG / "libgemm18.so"
 
 HIPCC_FLAGS = [

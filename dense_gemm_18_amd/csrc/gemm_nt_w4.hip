@@ -1,0 +1,288 @@
+// gemm_nt_w4.hip -- C entry points of the 4-bit weight operators, and the
+// kernels that quantise a weight and reverse it.  The product's kernels:
+// w4_product.h, skinny.h.
+#include "w4_product.h"
+
+namespace {
+
+// Quantisation, eight consecutive elements of a row per lane: one 16-byte
+// load, one packed word.  Lanes follow K, so a group's 4, 8 or 16 lanes are
+// neighbours and its extremes take 2, 3 or 4 exchanges; a 64-byte block's
+// words leave permuted but together.  Bound by memory: 2.5 bytes and a few
+// ten instructions per element pair.
+template <bool BF, int GS>
+__global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restrict__ W,
+                                                       uint32_t *__restrict__ Q,
+                                                       uint16_t *__restrict__ S,
+                                                       uint8_t *__restrict__ Z, int64_t N, int K,
+                                                       int64_t ldw)
+{
+    constexpr int kLanes = GS / 8;
+    const int words = ((K + 127) >> 7) * 16, G = (K + GS - 1) / GS;
+    const int64_t total = N * words;
+    // every lane of a group of 16 runs the same number of times: words and the
+    // grid's lanes are multiples of 16
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * 256) {
+        const int64_t n = i / words;
+        const int at = (int)(i - n * words), k = at * 8;
+        const uint16_t *src = W + n * ldw + k;
+        u32x4 raw = {0, 0, 0, 0};
+        if (k + 8 <= K)
+            raw = load16(src);
+        else if (k < K)
+            raw = load16_part(src, K - k);
+        float x[8], lo = 0.0f, hi = 0.0f;
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = to_float<BF>((uint16_t)(raw[e >> 1] >> (16 * (e & 1))));
+            odd |= !(__builtin_fabsf(x[e]) < __builtin_inff());
+            lo = __builtin_fminf(lo, x[e]);
+            hi = __builtin_fmaxf(hi, x[e]);
+        }
+        int any = odd;
+#pragma unroll
+        for (int d = 1; d < kLanes; d *= 2) {
+            lo = __builtin_fminf(lo, __shfl_xor(lo, d));
+            hi = __builtin_fmaxf(hi, __shfl_xor(hi, d));
+            any |= __shfl_xor(any, d);
+        }
+        const uint16_t bits =
+            from_float<BF>(Z ? (hi - lo) / 15.0f : __builtin_fmaxf(hi, -lo) / 7.0f);
+        const float s = to_float<BF>(bits);
+        const bool live = s > 0.0f && !any;
+        float z = 8.0f;
+        if (Z && live)
+            z = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(-lo / s), 0.0f), 15.0f);
+        uint32_t word = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float r = live ? __builtin_rintf(x[e] / s) : 0.0f;
+            if (Z)
+                r = __builtin_fminf(__builtin_fmaxf(r + z, 0.0f), 15.0f);
+            else
+                r = __builtin_fminf(__builtin_fmaxf(r, -8.0f), 7.0f) + 8.0f;
+            const uint32_t q = k + e < K ? (uint32_t)r : 0u;
+            word |= q << (4 * (e >> 1) + 16 * (e & 1));
+        }
+        const int j = (at >> 2) & 3, c = at & 3;
+        Q[n * words + (at & ~15) + 4 * c + j] = word;
+        if (at % kLanes == 0 && k < K) {
+            const int64_t g = n * G + k / GS;
+            S[g] = any ? (BF ? 0x7fc0 : 0x7e00) : bits;
+            if (Z)
+                Z[g] = (uint8_t)z;
+        }
+    }
+}
+
+// The reverse: one packed word, eight elements per lane.
+template <bool BF, int GS>
+__global__ void __launch_bounds__(256) dequantize_kernel(const uint32_t *__restrict__ Q,
+                                                         const uint16_t *__restrict__ S,
+                                                         const uint8_t *__restrict__ Z,
+                                                         uint16_t *__restrict__ W, int64_t N,
+                                                         int K, int64_t ldw)
+{
+    const int words = ((K + 127) >> 7) * 16, G = (K + GS - 1) / GS;
+    const int64_t total = N * words;
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * 256) {
+        const int64_t n = i / words;
+        const int at = (int)(i - n * words), k = at * 8;
+        if (k >= K)
+            continue;
+        const int j = (at >> 2) & 3, c = at & 3;
+        const uint32_t word = Q[n * words + (at & ~15) + 4 * c + j];
+        const int64_t g = n * G + k / GS;
+        const float s = to_float<BF>(S[g]);
+        const float z = Z ? (float)(Z[g] & 15) : 8.0f;
+        u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float q = (float)((word >> (4 * (e >> 1) + 16 * (e & 1))) & 15u);
+            v[e >> 1] |= (uint32_t)from_float<BF>((q - z) * s) << (16 * (e & 1));
+        }
+        uint16_t *dst = W + n * ldw + k;
+        if (k + 8 <= K) {
+            *(u32x4_a2 *)dst = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (k + e < K)
+                    dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+
+constexpr int64_t kMaxLd = int64_t(1) << 40;
+
+uint64_t packed_bytes(int64_t N, int64_t K) { return (uint64_t)N * (uint64_t)cdiv(K, 128) * 64u; }
+
+// Bytes that rows of `cols` elements `ld` apart span.
+uint64_t span_bytes(int64_t rows, int64_t cols, int64_t ld)
+{
+    return rows && cols ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * 2u : 0u;
+}
+
+// The checks every entry point shares: sizes, group, type, and the packed
+// weight's pointers.
+bool weight_ok(const void *Q, const void *S, int64_t N, int64_t K, int group, int dtype)
+{
+    if (!sizes_ok(0, N, K) || !group_ok(group) || !dtype_ok(dtype))
+        return false;
+    if (N && K && (!Q || !S))
+        return false;
+    return aligned_to(Q, 16) && aligned_to(S, 2);
+}
+
+template <class F>
+void for_type(int dtype, F &&f)
+{
+    if (dtype == GEMM_T_BF16)
+        f(std::true_type{});
+    else
+        f(std::false_type{});
+}
+
+// Workgroups of 256 lanes for one lane per packed word, up to 16 per CU.
+unsigned word_grid(int64_t N, int64_t K)
+{
+    const int64_t wgs = cdiv(N * cdiv(K, 128) * 16, 256);
+    return (unsigned)(wgs < 4096 ? wgs : 4096);
+}
+
+// Shared by the two directions; W is written where dequantize is set.
+int convert(const void *W, const void *Q, const void *S, const void *Z, int64_t N, int64_t K,
+            int64_t ldw, int group, int dtype, bool dequantize, hipStream_t stream)
+{
+    if (!weight_ok(Q, S, N, K, group, dtype) || ldw < K || ldw > kMaxLd)
+        return GEMM_EINVAL;
+    if ((N && K && !W) || !aligned_to(W, 2))
+        return GEMM_EINVAL;
+    const uint64_t groups = (uint64_t)N * (uint64_t)cdiv(K, group);
+    const struct { const void *p; uint64_t n; bool out; } part[4] = {
+        {W, span_bytes(N, K, ldw), dequantize},
+        {Q, packed_bytes(N, K), !dequantize},
+        {S, groups * 2u, !dequantize},
+        {Z, Z ? groups : 0u, !dequantize}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 4; ++j)
+            if ((part[i].out || part[j].out) &&
+                overlap(part[i].p, part[i].n, part[j].p, part[j].n))
+                return GEMM_EINVAL;
+    if (N == 0 || K == 0)
+        return GEMM_OK;
+    const dim3 grid(word_grid(N, K));
+    for_type(dtype, [&](auto bf) {
+        with_group(group, [&](auto gs) {
+            constexpr bool BF = decltype(bf)::value;
+            constexpr int GS = decltype(gs)::value ? decltype(gs)::value : 128;
+            if (dequantize)
+                hipLaunchKernelGGL((dequantize_kernel<BF, GS>), grid, dim3(256), 0, stream,
+                                   (const uint32_t *)Q, (const uint16_t *)S, (const uint8_t *)Z,
+                                   (uint16_t *)W, N, (int)K, ldw);
+            else
+                hipLaunchKernelGGL((quantize_kernel<BF, GS>), grid, dim3(256), 0, stream,
+                                   (const uint16_t *)W, (uint32_t *)Q, (uint16_t *)S,
+                                   (uint8_t *)Z, N, (int)K, ldw);
+        });
+    });
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ELAUNCH;
+}
+
+// Zeroes the N columns of M rows `ldd` apart (the empty sum).
+__global__ void zero_rows_kernel(uint16_t *__restrict__ D, int64_t M, int64_t N, int64_t ldd)
+{
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < M * N;
+         i += (int64_t)gridDim.x * 256)
+        D[i / N * ldd + i % N] = 0;
+}
+
+} // namespace
+
+extern "C" {
+
+int64_t gemm_w4_packed_bytes(int64_t N, int64_t K)
+{
+    return sizes_ok(0, N, K) ? (int64_t)packed_bytes(N, K) : 0;
+}
+
+int gemm_w4_quantize(const void *W, void *Q, void *S, void *Z, int64_t N, int64_t K, int64_t ldw,
+                     int group, int dtype, hipStream_t stream)
+{
+    return convert(W, Q, S, Z, N, K, ldw, group, dtype, false, stream);
+}
+
+int gemm_w4_dequantize(const void *Q, const void *S, const void *Z, void *W, int64_t N, int64_t K,
+                       int64_t ldw, int group, int dtype, hipStream_t stream)
+{
+    return convert(W, Q, S, Z, N, K, ldw, group, dtype, true, stream);
+}
+
+int64_t gemm_nt_w4_ws_size(int64_t M, int64_t N, int64_t K)
+{
+    if (!sizes_ok(M, N, K) || M <= GEMM_W4_DIRECT_M || N == 0)
+        return 0;
+    return cdiv(N * K * 2, 256) * 256;
+}
+
+int gemm_nt_w4(const void *A, const void *Q, const void *S, const void *Z, void *D, int64_t M,
+               int64_t N, int64_t K, int64_t lda, int64_t ldd, int group, int dtype,
+               void *workspace, int64_t ws_bytes, hipStream_t stream)
+{
+    if (!sizes_ok(M, N, K) || !weight_ok(Q, S, N, K, group, dtype))
+        return GEMM_EINVAL;
+    if (lda < K || lda > kMaxLd || ldd < N || ldd > kMaxLd || ws_bytes < 0)
+        return GEMM_EINVAL;
+    if ((M && K && !A) || (M && N && !D) || !aligned_to(A, 2) || !aligned_to(D, 2))
+        return GEMM_EINVAL;
+    if (ws_bytes && (!workspace || !aligned_to(workspace, 256)))
+        return GEMM_EINVAL;
+    const uint64_t d_bytes = span_bytes(M, N, ldd);
+    const uint64_t groups = (uint64_t)N * (uint64_t)cdiv(K, group);
+    const struct { const void *p; uint64_t n; } in[4] = {{A, span_bytes(M, K, lda)},
+                                                         {Q, packed_bytes(N, K)},
+                                                         {S, groups * 2u},
+                                                         {Z, Z ? groups : 0u}};
+    for (const auto &x : in)
+        if (overlap(D, d_bytes, x.p, x.n) || overlap(workspace, (uint64_t)ws_bytes, x.p, x.n))
+            return GEMM_EINVAL;
+    if (overlap(D, d_bytes, workspace, (uint64_t)ws_bytes))
+        return GEMM_EINVAL;
+    if (M == 0 || N == 0)
+        return GEMM_OK;
+    if (K == 0) {
+        const int64_t wgs = cdiv(M * N, 256);
+        hipLaunchKernelGGL(zero_rows_kernel, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256),
+                           0, stream, (uint16_t *)D, M, N, ldd);
+        return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ELAUNCH;
+    }
+    const int64_t need = gemm_nt_w4_ws_size(M, N, K);
+    if (need && ws_bytes >= need && lda == K && ldd == N) {
+        const int rc = gemm_w4_dequantize(Q, S, Z, workspace, N, K, K, group, dtype, stream);
+        if (rc != GEMM_OK)
+            return rc;
+        return dtype == GEMM_T_BF16 ? gemm_nt_bf16(A, workspace, D, M, N, K, stream)
+                                    : gemm_nt_f16(A, workspace, D, M, N, K, stream);
+    }
+    W4Args a{};
+    a.A = (const uint16_t *)A;
+    a.W.q = (const uint32_t *)Q;
+    a.W.s = (const uint16_t *)S;
+    a.W.z = (const uint8_t *)Z;
+    a.D = (uint16_t *)D;
+    a.lda = lda;
+    a.ldd = ldd;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    if (dtype == GEMM_T_BF16)
+        gemm18_w4_bf16(a, group, stream);
+    else
+        gemm18_w4_f16(a, group, stream);
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ELAUNCH;
+}
+
+} // extern "C"

@@ -1,0 +1,256 @@
+// moe_nt.hip -- C entry points of the mixture-of-experts layer.  Kernels:
+// moe_product.h, skinny.h.
+#include "moe_product.h"
+
+namespace {
+
+constexpr int64_t kMaxLd = int64_t(1) << 40;
+constexpr int64_t kHeader = 256;
+
+bool sizes_ok_moe(const moe_nt_weights *w, int64_t T, int topk)
+{
+    return w && dtype_ok(w->dtype) && w->experts >= 1 && w->experts <= MOE_MAX_EXPERTS &&
+           w->hidden >= 1 && w->hidden <= GEMM_MAX_K && T >= 0 && T <= INT32_MAX && topk >= 1 &&
+           topk <= MOE_MAX_TOPK;
+}
+
+bool inner_ok(const moe_nt_weights *w)
+{
+    return w->inner >= 1 && w->inner <= GEMM_MAX_K && (w->group == 0 || group_ok(w->group));
+}
+
+// Workspace: header, logits of a chunk, gated rows of a chunk.
+int64_t logits_bytes(int64_t T, int64_t E) { return cdiv(T * E * 4, 256) * 256; }
+
+struct Span {
+    const void *p;
+    uint64_t n;
+};
+
+uint64_t span_bytes(int64_t rows, int64_t cols, int64_t ld)
+{
+    return rows ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * 2u : 0u;
+}
+
+// None of `out` overlaps another of them or any of `in`.
+template <int A, int B>
+bool apart(const Span (&out)[A], const Span (&in)[B])
+{
+    for (int i = 0; i < A; ++i) {
+        for (int j = i + 1; j < A; ++j)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+                return false;
+        for (int j = 0; j < B; ++j)
+            if (overlap(out[i].p, out[i].n, in[j].p, in[j].n))
+                return false;
+    }
+    return true;
+}
+
+WeightRef weight_ref(const void *w, const void *s, const void *z, int group)
+{
+    WeightRef r{};
+    if (group) {
+        r.q = (const uint32_t *)w;
+        r.s = (const uint16_t *)s;
+        r.z = (const uint8_t *)z;
+    } else {
+        r.w = (const uint16_t *)w;
+    }
+    return r;
+}
+
+// Bytes of a weight of `rows` rows of `cols`, and of its scales (zero points:
+// half of that).
+uint64_t weight_bytes(int64_t rows, int64_t cols, int group)
+{
+    return group ? (uint64_t)rows * (uint64_t)cdiv(cols, 128) * 64u
+                 : (uint64_t)rows * (uint64_t)cols * 2u;
+}
+uint64_t scale_bytes(int64_t rows, int64_t cols, int group)
+{
+    return group ? (uint64_t)rows * (uint64_t)cdiv(cols, group) * 2u : 0u;
+}
+
+// What the two halves share: the activations, the workspace.
+int check_common(const moe_nt_weights *w, const void *X, int64_t T, int64_t ldx, int topk,
+                 const void *ws, int64_t ws_bytes, int64_t need)
+{
+    if (ldx < w->hidden || ldx > kMaxLd || !X || !aligned_to(X, 2))
+        return GEMM_EINVAL;
+    return !ws || !aligned_to(ws, 256) || ws_bytes < need ? GEMM_EINVAL : GEMM_OK;
+}
+
+int check_route(const moe_nt_weights *w, const void *X, const int32_t *ids, const float *weights,
+                int64_t T, int64_t ldx, int topk, int flags, const void *ws, int64_t ws_bytes)
+{
+    if (!sizes_ok_moe(w, T, topk) || topk > w->experts || (flags & ~MOE_RENORMALIZE))
+        return GEMM_EINVAL;
+    if (T == 0)
+        return GEMM_OK;
+    if (!w->router || !aligned_to(w->router, 2) || !ids || !weights || !aligned_to(ids, 4) ||
+        !aligned_to(weights, 4))
+        return GEMM_EINVAL;
+    const int64_t chunk = moe_chunk(T, topk);
+    const int rc = check_common(w, X, T, ldx, topk, ws, ws_bytes,
+                                kHeader + logits_bytes(chunk, w->experts));
+    if (rc != GEMM_OK)
+        return rc;
+    const uint64_t slots = (uint64_t)T * (uint64_t)topk * 4u;
+    return apart<3, 2>({{ids, slots}, {weights, slots}, {ws, (uint64_t)ws_bytes}},
+                       {{X, span_bytes(T, w->hidden, ldx)},
+                        {w->router, (uint64_t)w->experts * (uint64_t)w->hidden * 2u}})
+               ? GEMM_OK
+               : GEMM_EINVAL;
+}
+
+int check_experts(const moe_nt_weights *w, const void *X, const int32_t *ids, const float *weights,
+                  const void *D, int64_t T, int64_t ldx, int64_t ldd, int topk, const void *ws,
+                  int64_t ws_bytes)
+{
+    if (!sizes_ok_moe(w, T, topk) || !inner_ok(w))
+        return GEMM_EINVAL;
+    if (T == 0)
+        return GEMM_OK;
+    if (!w->w13 || !w->w2 || !ids || !weights || !D || !aligned_to(D, 2) || !aligned_to(ids, 4) ||
+        !aligned_to(weights, 4) || ldd < w->hidden || ldd > kMaxLd)
+        return GEMM_EINVAL;
+    const uintptr_t wa = w->group ? 16 : 2;
+    if (!aligned_to(w->w13, wa) || !aligned_to(w->w2, wa))
+        return GEMM_EINVAL;
+    if (w->group && (!w->w13_scales || !w->w2_scales || !aligned_to(w->w13_scales, 2) ||
+                     !aligned_to(w->w2_scales, 2) || !w->w13_zeros != !w->w2_zeros))
+        return GEMM_EINVAL;
+    const int rc = check_common(w, X, T, ldx, topk, ws, ws_bytes, moe_nt_ws_size(T, w, topk));
+    if (rc != GEMM_OK)
+        return rc;
+    const int64_t n13 = w->experts * 2 * w->inner, n2 = w->experts * w->hidden;
+    const uint64_t s13 = scale_bytes(n13, w->hidden, w->group);
+    const uint64_t s2 = scale_bytes(n2, w->inner, w->group);
+    const uint64_t slots = (uint64_t)T * (uint64_t)topk * 4u;
+    return apart<2, 9>({{D, span_bytes(T, w->hidden, ldd)}, {ws, (uint64_t)ws_bytes}},
+                       {{X, span_bytes(T, w->hidden, ldx)},
+                        {ids, slots},
+                        {weights, slots},
+                        {w->w13, weight_bytes(n13, w->hidden, w->group)},
+                        {w->w2, weight_bytes(n2, w->inner, w->group)},
+                        {w->w13_scales, s13},
+                        {w->w2_scales, s2},
+                        {w->w13_zeros, w->w13_zeros ? s13 / 2 : 0},
+                        {w->w2_zeros, w->w2_zeros ? s2 / 2 : 0}})
+               ? GEMM_OK
+               : GEMM_EINVAL;
+}
+
+MoeArgs common_args(const moe_nt_weights *w, const void *X, const int32_t *ids,
+                    const float *weights, int64_t ldx, int topk, void *ws)
+{
+    MoeArgs p{};
+    p.X = (const uint16_t *)X;
+    p.router = (const uint16_t *)w->router;
+    p.logits = (float *)((char *)ws + kHeader);
+    p.ids = (int32_t *)ids;
+    p.weights = (float *)weights;
+    p.ldx = ldx;
+    p.E = (int)w->experts;
+    p.H = (int)w->hidden;
+    p.I = (int)w->inner;
+    p.topk = topk;
+    return p;
+}
+
+// Moves the arguments on by `T` tokens and sets the next chunk's count.
+bool next_chunk(MoeArgs &p, int64_t T, int64_t &done)
+{
+    if (p.T) {
+        p.X += p.T * p.ldx;
+        p.D += p.T * p.ldd;
+        p.ids += (int64_t)p.T * p.topk;
+        p.weights += (int64_t)p.T * p.topk;
+        done += p.T;
+    }
+    p.T = moe_chunk(T - done, p.topk);
+    return p.T > 0;
+}
+
+MoeLaunch launches(const moe_nt_weights *w)
+{
+    return w->dtype == GEMM_T_BF16 ? gemm18_moe_bf16() : gemm18_moe_f16();
+}
+
+int run_route(const moe_nt_weights *w, MoeArgs p, int64_t T, int flags, hipStream_t stream)
+{
+    p.renorm = flags & MOE_RENORMALIZE;
+    p.D = nullptr;
+    p.ldd = 0;
+    const MoeLaunch go = launches(w);
+    for (int64_t done = 0; next_chunk(p, T, done);)
+        go.route(p, stream);
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ELAUNCH;
+}
+
+int run_experts(const moe_nt_weights *w, MoeArgs p, void *D, int64_t T, int64_t ldd, void *ws,
+                hipStream_t stream)
+{
+    const int64_t chunk = moe_chunk(T, p.topk);
+    p.w13 = weight_ref(w->w13, w->w13_scales, w->w13_zeros, w->group);
+    p.w2 = weight_ref(w->w2, w->w2_scales, w->w2_zeros, w->group);
+    p.h = (uint16_t *)((char *)ws + kHeader + logits_bytes(chunk, w->experts));
+    p.D = (uint16_t *)D;
+    p.ldd = ldd;
+    const MoeLaunch go = launches(w);
+    for (int64_t done = 0; next_chunk(p, T, done);)
+        go.experts(p, w->group, stream);
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ELAUNCH;
+}
+
+} // namespace
+
+extern "C" {
+
+int64_t moe_nt_ws_size(int64_t T, const moe_nt_weights *w, int topk)
+{
+    if (!sizes_ok_moe(w, T, topk) || !inner_ok(w) || T == 0)
+        return 0;
+    const int64_t chunk = moe_chunk(T, topk);
+    return kHeader + logits_bytes(chunk, w->experts) +
+           cdiv(chunk * topk * w->inner * 2, 256) * 256;
+}
+
+int moe_nt_route(const moe_nt_weights *w, const void *X, int32_t *ids, float *weights, int64_t T,
+                 int64_t ldx, int topk, int flags, void *workspace, int64_t ws_bytes,
+                 hipStream_t stream)
+{
+    const int rc = check_route(w, X, ids, weights, T, ldx, topk, flags, workspace, ws_bytes);
+    if (rc != GEMM_OK || T == 0)
+        return rc;
+    return run_route(w, common_args(w, X, ids, weights, ldx, topk, workspace), T, flags, stream);
+}
+
+int moe_nt_experts(const moe_nt_weights *w, const void *X, const int32_t *ids,
+                   const float *weights, void *D, int64_t T, int64_t ldx, int64_t ldd, int topk,
+                   void *workspace, int64_t ws_bytes, hipStream_t stream)
+{
+    const int rc =
+        check_experts(w, X, ids, weights, D, T, ldx, ldd, topk, workspace, ws_bytes);
+    if (rc != GEMM_OK || T == 0)
+        return rc;
+    return run_experts(w, common_args(w, X, ids, weights, ldx, topk, workspace), D, T, ldd,
+                       workspace, stream);
+}
+
+int moe_nt_layer(const moe_nt_weights *w, const void *X, void *D, int32_t *ids, float *weights,
+                 int64_t T, int64_t ldx, int64_t ldd, int topk, int flags, void *workspace,
+                 int64_t ws_bytes, hipStream_t stream)
+{
+    int rc = check_route(w, X, ids, weights, T, ldx, topk, flags, workspace, ws_bytes);
+    if (rc == GEMM_OK)
+        rc = check_experts(w, X, ids, weights, D, T, ldx, ldd, topk, workspace, ws_bytes);
+    if (rc != GEMM_OK || T == 0)
+        return rc;
+    const MoeArgs p = common_args(w, X, ids, weights, ldx, topk, workspace);
+    rc = run_route(w, p, T, flags, stream);
+    return rc != GEMM_OK ? rc : run_experts(w, p, D, T, ldd, workspace, stream);
+}
+
+} // extern "C"

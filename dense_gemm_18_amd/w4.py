@@ -1,0 +1,170 @@
+"""4-bit weights with group scales: tensors in, tensors out.
+
+Over the C ABI of ``include/gemm_nt_w4.h``, which defines the packed layout,
+the rounding and the limits.  A call is enqueued on ``stream`` (default: the
+current stream of the tensors' device).
+"""
+from __future__ import annotations
+
+from . import binding
+from .binding import GEMM_OK, GemmError
+
+_DTYPES = None
+
+
+def dtype_code(dtype) -> int:
+    """GEMM_T_* of a torch dtype; TypeError for any other than the two."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float16: binding.GEMM_T_F16, torch.bfloat16: binding.GEMM_T_BF16}
+    try:
+        return _DTYPES[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {dtype}: float16 or bfloat16") from None
+
+
+def launch(name: str, device, stream, args) -> None:
+    """The raw entry point ``name`` with ``args`` and the stream, on ``device``."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    fn = getattr(binding.lib(), name)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, s.cuda_stream)
+    else:
+        # the library launches on the current device: make it the operands' one
+        with torch.cuda.device(device):
+            rc = fn(*args, s.cuda_stream)
+    if rc != GEMM_OK:
+        raise GemmError(rc, name)
+
+
+def row_stride(x, what: str) -> int:
+    """Elements between the rows of a 2-D tensor whose rows are dense."""
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError(f"{what} must have dense rows")
+    ld = x.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"the rows of {what} overlap")
+    return ld
+
+
+def check_out(out, shape, dtype, device) -> None:
+    if out.dtype != dtype or tuple(out.shape) != tuple(shape) or out.device != device:
+        raise ValueError(f"out must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+class W4Weight:
+    """A packed weight [..., N, K]: ``q`` (int32 words [..., N, ceil(K / 128) * 16]),
+    ``scales`` [..., N, ceil(K / group)] in float16 or bfloat16 and ``zeros`` of that
+    shape (uint8), or None for zero points of 8; all contiguous, on one GPU."""
+
+    __slots__ = ("q", "scales", "zeros", "shape", "group", "dtype", "device", "N", "K", "code",
+                 "pointers")
+
+    def __init__(self, q, scales, zeros=None, *, shape, group):
+        import torch
+        shape = tuple(int(n) for n in shape)
+        if group not in (32, 64, 128):
+            raise ValueError(f"group {group} is not 32, 64 or 128")
+        if len(shape) < 2:
+            raise ValueError(f"shape {shape} is not [..., N, K]")
+        K = shape[-1]
+        self.code = dtype_code(scales.dtype)
+        want = {"q": (q, torch.int32, -(-K // 128) * 16),
+                "scales": (scales, scales.dtype, -(-K // group))}
+        if zeros is not None:
+            want["zeros"] = (zeros, torch.uint8, -(-K // group))
+        for name, (x, dtype, last) in want.items():
+            if x.dtype != dtype or tuple(x.shape) != shape[:-1] + (last,):
+                raise ValueError(f"{name} must be a {dtype} tensor of shape "
+                                 f"{shape[:-1] + (last,)}, not {x.dtype} {tuple(x.shape)}")
+            if not x.is_contiguous() or not x.is_cuda or x.device != q.device:
+                raise ValueError(f"{name} must be contiguous, on the GPU of q")
+        self.q, self.scales, self.zeros = q, scales, zeros
+        self.shape, self.group = shape, group
+        self.dtype, self.device = scales.dtype, q.device
+        self.N, self.K = 1, K
+        for n in shape[:-1]:
+            self.N *= n
+        self.pointers = (q.data_ptr(), scales.data_ptr(),
+                         zeros.data_ptr() if zeros is not None else None)
+
+
+def quantize_w4(W, group: int = 128, zeros: bool = False, stream=None) -> W4Weight:
+    """``W`` [..., N, K] (float16 or bfloat16) in 4 bits with a scale per ``group``
+    elements of a row, and with ``zeros`` a zero point (otherwise symmetric).  A 2-D
+    W may have a row stride; with more dimensions it is contiguous."""
+    import torch
+    code = dtype_code(W.dtype)
+    if W.dim() < 2:
+        raise ValueError(f"shape {tuple(W.shape)} is not [..., N, K]")
+    if not W.is_cuda:
+        raise ValueError("W must be on a GPU")
+    if W.dim() > 2 and not W.is_contiguous():
+        raise ValueError("W must be contiguous")
+    if group not in (32, 64, 128):
+        raise ValueError(f"group {group} is not 32, 64 or 128")
+    K = W.shape[-1]
+    ldw = row_stride(W, "W") if W.dim() == 2 else K
+    lead = tuple(W.shape[:-1])
+    w = W4Weight(torch.empty(lead + (-(-K // 128) * 16,), dtype=torch.int32, device=W.device),
+                 torch.empty(lead + (-(-K // group),), dtype=W.dtype, device=W.device),
+                 torch.empty(lead + (-(-K // group),), dtype=torch.uint8, device=W.device)
+                 if zeros else None, shape=W.shape, group=group)
+    q, s, z = w.pointers
+    launch("gemm_w4_quantize", W.device, stream,
+           (W.data_ptr(), q, s, z, w.N, K, ldw, group, code))
+    return w
+
+
+def dequantize_w4(w: W4Weight, out=None, stream=None):
+    """The values of ``w``, rounded to its 16-bit type, in its shape.  ``out``
+    (optional): 2-D with a row stride, or contiguous."""
+    import torch
+    if out is None:
+        out = torch.empty(w.shape, dtype=w.dtype, device=w.device)
+    else:
+        check_out(out, w.shape, w.dtype, w.device)
+        if out.dim() > 2 and not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+    ldw = row_stride(out, "out") if out.dim() == 2 else w.K
+    launch("gemm_w4_dequantize", w.device, stream,
+           (*w.pointers, out.data_ptr(), w.N, w.K, ldw, w.group, w.code))
+    return out
+
+
+def gemm_nt_w4(A, w: W4Weight, out=None, stream=None, workspace=None):
+    """D = A @ W.T for ``A`` [M, K] in the weight's 16-bit type and a 2-D ``w`` [N, K].
+
+    A and ``out`` (optional, [M, N]) may have a row stride.  ``workspace`` (optional):
+    a contiguous uint8 tensor for the unpacked weight of large M, allocated here where
+    it is needed and none is given."""
+    import torch
+    if len(w.shape) != 2 or A.dim() != 2 or A.shape[1] != w.K:
+        raise ValueError(f"shapes {tuple(A.shape)} and {w.shape} are not [M, K] and [N, K]")
+    if A.dtype != w.dtype:
+        raise TypeError(f"A is {A.dtype}, the weight's scales are {w.dtype}")
+    if A.device != w.device:
+        raise ValueError("A and the weight must be on the same GPU")
+    M, N = A.shape[0], w.N
+    lda = row_stride(A, "A")
+    if out is None:
+        out = torch.empty((M, N), dtype=A.dtype, device=A.device)
+        ldd = N
+    else:
+        check_out(out, (M, N), A.dtype, A.device)
+        ldd = row_stride(out, "out")
+    if workspace is None:
+        need = binding.gemm_nt_w4_ws_size(M, N, w.K) if lda == w.K and ldd == N else 0
+        if need:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=A.device)
+    elif not workspace.is_cuda or workspace.device != A.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on A's device")
+    ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
+        if workspace is not None else (None, 0)
+    launch("gemm_nt_w4", A.device, stream,
+           (A.data_ptr(), *w.pointers, out.data_ptr(), M, N, w.K, lda, ldd, w.group, w.code, *ws))
+    return out

@@ -1,0 +1,303 @@
+"""GPU checks of the 4-bit weight operators against plain 64-bit forms.
+
+Tolerances, with u the 16-bit type's half step (2^-11 fp16, 2^-8 bfloat16):
+- integers and powers of two: every partial sum is exact in fp32, so the
+  result is the exact sum rounded once, bit for bit;
+- otherwise |D - ref| <= u |ref| + 2^-23 (group + 4) B + 2^-23 (G + 8) C,
+  one rounding of the result, the fp32 sums of a group (for bfloat16 of
+  128 + q and 128 + z times A: B = sum |A| s (256 + q + z); for fp16
+  B = sum |A| |q - z| s), and the sum over G groups and 8 waves with
+  C = sum |A| |q - z| s; and in the 2-norm u |ref| with a tenth to spare;
+- with the weight unpacked once to 16 bits, u more per weight: u C on top,
+  and 2 u in the 2-norm.
+"""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from dense_gemm_18_amd import W4Weight, binding, dequantize_w4, gemm_nt_w4, quantize_w4
+from tests import w4_ref
+from tests.gpu_util import device, note
+from tests.w4_ref import TYPES, half_step
+
+pytestmark = pytest.mark.gpu
+
+NAN_GUARD = {torch.float16: 0x7E5A, torch.bfloat16: 0x7FDA}
+
+
+def gen(seed):
+    return torch.Generator(device=device()).manual_seed(seed)
+
+
+def bits(x):
+    return x.contiguous().view(torch.int16)
+
+
+def strided(rows, cols, ld, dtype):
+    """A rows x cols view with row stride ld inside a buffer of a NaN pattern."""
+    buf = torch.full((rows * ld + 16,), NAN_GUARD[dtype], dtype=torch.int16, device=device())
+    return buf, buf.view(dtype)[8:8 + rows * ld].view(rows, ld)[:, :cols]
+
+
+def check_guard(buf, rows, cols, ld, dtype):
+    body = buf[8:8 + rows * ld].view(rows, ld)
+    for part in (buf[:8], body[:, cols:], buf[8 + rows * ld:]):
+        assert bool((part == NAN_GUARD[dtype]).all()), "write outside D"
+
+
+def product(A, Q, S, Z, group, lda_pad=0, ldd_pad=0):
+    M, K = A.shape
+    N = Q.shape[0]
+    w = W4Weight(Q, S, Z, shape=(N, K), group=group)
+    if lda_pad:
+        _, view = strided(M, K, K + lda_pad, A.dtype)
+        view.copy_(A)
+        A = view
+    ldd = N + ldd_pad
+    buf, out = strided(M, N, ldd, A.dtype)
+    gemm_nt_w4(A, w, out=out)
+    torch.cuda.synchronize()
+    check_guard(buf, M, N, ldd, A.dtype)
+    return out.clone()
+
+
+def check(D, A, Q, S, Z, group, unpacked=False):
+    """`unpacked`: the weight may have been rounded to 16 bits first."""
+    K = A.shape[1]
+    u = half_step(A.dtype)
+    a = A.double()
+    w = w4_ref.values(Q, S, Z, K, group)
+    ref = a @ w.T
+    g = w4_ref.group_of(K, group, Q.device)
+    s = S.double()[:, g]
+    C = a.abs() @ w.abs().T
+    if A.dtype == torch.bfloat16:
+        z = 8 if Z is None else (Z & 15).double()[:, g]
+        B = a.abs() @ (s * (256 + w4_ref.unpack(Q, K) + z)).T
+    else:
+        B = C
+    bound = u * ref.abs() + 2.0 ** -23 * ((group + 4) * B + (S.shape[1] + 8) * C)
+    bound = bound + (u * (1 + u) * C if unpacked else 0)
+    # below the type's smallest normal number a step no longer shrinks
+    bound = bound + torch.finfo(A.dtype).smallest_normal * u
+    bad = (D.double() - ref).abs() > bound
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outside"
+    if ref.numel() >= 64:
+        assert w4_ref.rel(D, ref) <= (2.2 if unpacked else 1.1) * u
+
+
+SHAPES = [(1, 1, 1), (1, 16, 128), (1, 17, 31), (1, 64, 127), (2, 33, 129), (1, 40, 1024),
+          (3, 100, 300), (15, 70, 256), (16, 64, 1152), (17, 65, 384), (31, 96, 130),
+          (32, 50, 1000), (33, 128, 640), (64, 200, 1025), (65, 48, 2050), (130, 77, 515),
+          (5, 1000, 4100)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_product_against_64_bits(M, N, K, group, dtype):
+    note(f"w4 {M}x{N}x{K} group {group} {dtype}")
+    for zeros in (False, True):
+        g = gen(M * 1000 + N + K + group + zeros)
+        A = torch.randn((M, K), generator=g, device=device(), dtype=dtype)
+        Q, S, Z = w4_ref.random_weight(g, N, K, group, zeros, dtype)
+        check(product(A, Q, S, Z, group), A, Q, S, Z, group)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 48, 640), (7, 50, 333), (20, 40, 256), (64, 33, 500),
+                                   (100, 64, 129)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_integers_are_exact(M, N, K, group, dtype):
+    note(f"w4 integers {M}x{N}x{K} group {group} {dtype}")
+    g = gen(7 * M + N + K)
+    A = torch.randint(-2, 3, (M, K), generator=g, device=device()).to(dtype)
+    Q, S, Z = w4_ref.random_weight(g, N, K, group, True, dtype)
+    S = torch.exp2(torch.randint(-2, 2, S.shape, generator=g, device=device()).float()).to(dtype)
+    ref = A.double() @ w4_ref.values(Q, S, Z, K, group).T
+    assert torch.equal(product(A, Q, S, Z, group), ref.to(dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_row_strides_and_odd_addresses(dtype):
+    for M, N, K, pa, pd in [(1, 40, 300, 5, 3), (6, 33, 256, 1, 7), (40, 64, 387, 64, 1),
+                            (300, 48, 200, 8, 16), (300, 48, 200, 0, 16)]:
+        note(f"w4 strides {M}x{N}x{K} +{pa} +{pd} {dtype}")
+        g = gen(M + K)
+        A = torch.randn((M, K), generator=g, device=device(), dtype=dtype)
+        Q, S, Z = w4_ref.random_weight(g, N, K, 64, True, dtype)
+        check(product(A, Q, S, Z, 64, pa, pd), A, Q, S, Z, 64, unpacked=True)
+    # A one element past an aligned address
+    flat = torch.randn(8 * 256 + 1, generator=gen(3), device=device(), dtype=dtype)
+    A = flat[1:].view(8, 256)
+    Q, S, Z = w4_ref.random_weight(gen(4), 50, 256, 32, False, dtype)
+    check(product(A, Q, S, Z, 32), A, Q, S, Z, 32)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_rows_with_and_without_workspace(dtype):
+    M, N, K, group = 700, 330, 520, 128
+    g = gen(11)
+    A = torch.randn((M, K), generator=g, device=device(), dtype=dtype)
+    Q, S, Z = w4_ref.random_weight(g, N, K, group, True, dtype)
+    w = W4Weight(Q, S, Z, shape=(N, K), group=group)
+    need = binding.gemm_nt_w4_ws_size(M, N, K)
+    assert need > 0
+    note(f"w4 workspace {dtype}")
+    D = gemm_nt_w4(A, w, workspace=torch.empty(need, dtype=torch.uint8, device=device()))
+    check(D, A, Q, S, Z, group, unpacked=True)
+    # the unpacked weight through the 16-bit product gives the same bits
+    from dense_gemm_18_amd import gemm_nt
+    assert torch.equal(bits(D), bits(gemm_nt(A, dequantize_w4(w))))
+    check(gemm_nt_w4(A, w), A, Q, S, Z, group, unpacked=True)
+    note(f"w4 no workspace {dtype}")
+    out = torch.empty((M, N), dtype=dtype, device=device())
+    rc = binding.gemm_nt_w4(A.data_ptr(), *w.pointers, out.data_ptr(), M, N, K, K, N, group,
+                            w.code, 0, 0, torch.cuda.current_stream().cuda_stream)
+    assert rc == binding.GEMM_OK
+    check(out, A, Q, S, Z, group)
+
+
+def test_empty_sum_and_empty_output():
+    for dtype in TYPES:
+        w = W4Weight(torch.empty((5, 0), dtype=torch.int32, device=device()),
+                     torch.empty((5, 0), dtype=dtype, device=device()), shape=(5, 0), group=32)
+        buf, out = strided(3, 5, 7, dtype)
+        gemm_nt_w4(torch.empty((3, 0), dtype=dtype, device=device()), w, out=out)
+        assert bool((bits(out) == 0).all())
+        check_guard(buf, 3, 5, 7, dtype)
+        assert gemm_nt_w4(torch.empty((0, 0), dtype=dtype, device=device()), w).shape == (0, 5)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [1, 20, 50])
+def test_infinities_and_nan_stay_where_they_belong(M, dtype):
+    note(f"w4 infinities {M} {dtype}")
+    N, K, group = 40, 300, 32
+    g = gen(M)
+    A = torch.randn((M, K), generator=g, device=device(), dtype=dtype)
+    clean = A.clone()
+    big = torch.finfo(dtype).max
+    Q, S, Z = w4_ref.random_weight(g, N, K, group, True, dtype)
+    w = w4_ref.values(Q, S, Z, K, group)
+    D0 = product(clean, Q, S, Z, group)
+    for value in (float("inf"), float("-inf"), float("nan"), big):
+        A = clean.clone()
+        A[M // 2, 137] = value
+        D = product(A, Q, S, Z, group)
+        other = torch.arange(M, device=device()) != M // 2
+        assert torch.equal(bits(D[other]), bits(D0[other])), "another row changed"
+        ref = (A[M // 2].double() * w).sum(-1).to(dtype)     # the row's own definition
+        got = D[M // 2]
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)), value
+        sure = torch.isinf(ref) if value != big else torch.zeros_like(ref, dtype=torch.bool)
+        assert torch.equal(got[sure], ref[sure]), value
+        if value == big:
+            ok = torch.isfinite(ref) & (ref.double().abs() < 0.9 * big)
+            d = (got.double() - ref.double()).abs()[ok]
+            assert bool((d <= 4 * half_step(dtype) * ref.double().abs()[ok] + 1e-2 * K).all())
+    # a NaN scale marks its group: that weight row alone
+    S2 = S.clone()
+    S2[7, 4] = float("nan")
+    D = product(clean, Q, S2, Z, group)
+    assert bool(torch.isnan(D[:, 7]).all())
+    keep = torch.arange(N, device=device()) != 7
+    assert torch.equal(bits(D[:, keep]), bits(D0[:, keep]))
+
+
+@pytest.mark.parametrize("K", [1, 8, 31, 128, 129, 257, 1000])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_quantize_by_the_definition(K, group, zeros):
+    for dtype in TYPES:
+        note(f"quantize K {K} group {group} zeros {zeros} {dtype}")
+        N = 37
+        g = torch.Generator().manual_seed(K + group)
+        W = (torch.randn((N, K), generator=g) * 0.05).to(dtype)
+        W[0] = 0                                            # scale 0
+        W[1] = torch.finfo(dtype).smallest_normal / 64      # scale rounds to 0 or nearly
+        W[2] = W[2].abs()                                   # one sign
+        W[3] = -W[3].abs()
+        W[4] = torch.finfo(dtype).max                       # the largest
+        W[4, ::2] = -torch.finfo(dtype).max
+        W[5, K // 2] = float("nan")
+        W[6, K - 1] = float("-inf")
+        q, s, z = w4_ref.quantize(W, group, zeros)
+        buf, view = strided(N, K, K + 9, dtype)
+        view.copy_(W)
+        w = quantize_w4(view, group=group, zeros=zeros)
+        torch.cuda.synchronize()
+        assert torch.equal(torch.isnan(w.scales.cpu()), torch.isnan(s))
+        fine = ~torch.isnan(s)
+        assert torch.equal(w.scales.cpu()[fine], s[fine])
+        if zeros:
+            assert torch.equal(w.zeros.cpu().to(torch.int64), z)
+        assert torch.equal(w.q.cpu(), w4_ref.pack(q))       # padding bits are 0
+        # and back, into rows with a stride
+        buf, out = strided(N, K, K + 3, dtype)
+        dequantize_w4(w, out=out)
+        torch.cuda.synchronize()
+        check_guard(buf, N, K, K + 3, dtype)
+        ref = w4_ref.values(w4_ref.pack(q), s, z, K, group).float().to(dtype)
+        got = out.cpu()
+        nan = torch.isnan(ref)
+        assert torch.equal(torch.isnan(got), nan)
+        assert torch.equal(got[~nan], ref[~nan])
+        assert torch.equal(bits(dequantize_w4(w).cpu()), bits(got))
+
+
+def test_quantize_many_rows_and_leading_dimensions():
+    W = torch.randn((3, 70, 900), generator=gen(5), device=device(), dtype=torch.bfloat16)
+    w = quantize_w4(W, group=64, zeros=True)
+    one = quantize_w4(W[2], group=64, zeros=True)
+    assert w.shape == (3, 70, 900) and torch.equal(w.q[2], one.q)
+    assert torch.equal(w.scales[2], one.scales) and torch.equal(w.zeros[2], one.zeros)
+    assert torch.equal(dequantize_w4(w)[2], dequantize_w4(one))
+
+
+def test_offsets_past_32_bits():
+    # 5.2e9 weights, 2.6 GB packed; the last rows lie past 2^31 bytes
+    N, K, group = 320000, 16384, 128
+    dtype = torch.float16
+    note("w4 offsets past 2^31")
+    g = gen(9)
+    Q = torch.empty((N, K // 8), dtype=torch.int32, device=device())
+    Q.random_(-2 ** 31, 2 ** 31 - 1, generator=g)
+    S = (torch.rand((N, K // group), generator=g, device=device()) * 0.01).to(dtype)
+    A = torch.randn((2, K), generator=g, device=device(), dtype=dtype)
+    D = gemm_nt_w4(A, W4Weight(Q, S, shape=(N, K), group=group))
+    for rows in (slice(0, 64), slice(N // 2 - 32, N // 2 + 32), slice(N - 64, N)):
+        check(D[:, rows], A, Q[rows], S[rows], None, group)
+    # unpacking writes past 2^32 bytes
+    last = dequantize_w4(W4Weight(Q, S, shape=(N, K), group=group))[-3:]
+    assert torch.equal(last, w4_ref.values(Q[-3:], S[-3:], None, K, group).float().to(dtype))
+
+
+def test_other_stream_and_graph_replays():
+    M, N, K, group = 3, 200, 700, 64
+    note("w4 stream and graph")
+    g = gen(21)
+    Q, S, Z = w4_ref.random_weight(g, N, K, group, True, torch.bfloat16)
+    w = W4Weight(Q, S, Z, shape=(N, K), group=group)
+    A = torch.randn((M, K), generator=g, device=device(), dtype=torch.bfloat16)
+    big = torch.randn((400, K), generator=g, device=device(), dtype=torch.bfloat16)
+    want, want_big = gemm_nt_w4(A, w).clone(), gemm_nt_w4(big, w).clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out, out_big = torch.empty_like(want), torch.empty_like(want_big)
+    gemm_nt_w4(A, w, out=out, stream=side)
+    gemm_nt_w4(big, w, out=out_big, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(out_big, want_big)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gemm_nt_w4(A, w, out=out)
+        gemm_nt_w4(big, w, out=out_big)
+    for i in range(4):
+        A.copy_(torch.randn((M, K), generator=g, device=device()).to(torch.bfloat16))
+        out.zero_()
+        out_big.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, gemm_nt_w4(A, w)) and torch.equal(out_big, want_big), i
