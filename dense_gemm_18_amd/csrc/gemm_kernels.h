@@ -123,8 +123,6 @@ __device__ __forceinline__ f16x4 mma_acc16(i32x8 b, i32x8 a, f16x4 s)
 constexpr int kBK = 64;            // K elements per LDS row: 128 B, 8 chunks
 constexpr int kGroupM = 4;         // tile rows per rasterisation group
 constexpr int kXcds = 8;           // MI355X: 8 XCDs, workgroups dealt round-robin
-constexpr uint32_t kOob = 0x80000000u;   // a buffer offset past every range
-constexpr int kRsrcFlags = 0x00020000;   // gfx9 buffer descriptor word 3
 
 // ---------------------------------------------------------------------------
 // Tile -> workgroup map (shared by the kernels and the host introspection).
@@ -542,21 +540,6 @@ __device__ __forceinline__ void wait_vmcnt()
 {
     static_assert(N >= 0 && N < 64, "vmcnt range");
     __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
-}
-
-// Kernel-local lambdas must always inline: an out-of-line call would keep
-// every array they capture by reference in scratch memory.
-#define G18_INLINE __attribute__((always_inline))
-
-// Compile-time loop: f(integral_constant<int, I>) for I = B .. E-1, so that
-// register arrays are only ever indexed by constants.
-template <int B, int E, class F>
-__device__ __forceinline__ void static_for(F &&f)
-{
-    if constexpr (B < E) {
-        f(std::integral_constant<int, B>{});
-        static_for<B + 1, E>(f);
-    }
 }
 
 // Workgroup barrier without a memory fence (a fence would wait for every
@@ -1642,8 +1625,6 @@ enum class Tile { kBig, kMid, kThin, kThinN, kThinM, kRect };
 // rather than 64 big ones, and 1024 x 1024 runs 256 thin tiles rather than
 // 64 mid ones (5.5 against 8.1 us at K = 1024).  The choice assumes operands
 // aligned to 16 bytes.
-constexpr int kCUs = 256;
-
 // thin_ok = false (FP8, whose 64 x 64 tile cost is not measured): the thin
 // tile only when M or N is at most 64.
 inline Tile choose_tile(int64_t M, int64_t N, int64_t K, bool thin_ok = true)

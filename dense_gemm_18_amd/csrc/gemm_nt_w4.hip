@@ -5,6 +5,23 @@
 
 namespace {
 
+// 16 bytes at any 2-byte alignment (one global load on gfx950).
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+
+__device__ __forceinline__ u32x4 load16(const uint16_t *p) { return *(const u32x4_a2 *)p; }
+
+// The first `count` of the 8 elements at p, zero for the others; nothing
+// past them is accessed.
+__device__ __forceinline__ u32x4 load16_part(const uint16_t *p, int count)
+{
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < count)
+            v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    return v;
+}
+
 // Quantisation, eight consecutive elements of a row per lane: one 16-byte
 // load, one packed word.  Lanes follow K, so a group's 4, 8 or 16 lanes are
 // neighbours and its extremes take 2, 3 or 4 exchanges; a 64-byte block's
@@ -234,7 +251,7 @@ int gemm_nt_w4(const void *A, const void *Q, const void *S, const void *Z, void 
 {
     if (!sizes_ok(M, N, K) || !weight_ok(Q, S, N, K, group, dtype))
         return GEMM_EINVAL;
-    if (lda < K || lda > kMaxLd || ldd < N || ldd > kMaxLd || ws_bytes < 0)
+    if (lda < K || lda > GEMM_W4_MAX_LDA || ldd < N || ldd > kMaxLd || ws_bytes < 0)
         return GEMM_EINVAL;
     if ((M && K && !A) || (M && N && !D) || !aligned_to(A, 2) || !aligned_to(D, 2))
         return GEMM_EINVAL;

@@ -10,9 +10,14 @@
 
 #include "gemm_nt_f16.h"
 
+// Kernel-local lambdas must always inline: an out-of-line call would keep
+// every array they capture by reference in scratch memory.
+#define G18_INLINE __attribute__((always_inline))
+
 namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -55,7 +60,23 @@ __device__ __forceinline__ f32x4 mfma16(typename Elem<BF>::x8 b, typename Elem<B
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(b, a, c, 0, 0, 0);
 }
 
+// Compile-time loop: f(integral_constant<int, I>) for I = B .. E-1, so that
+// register arrays are only ever indexed by constants.
+template <int B, int E, class F>
+__device__ __forceinline__ void static_for(F &&f)
+{
+    if constexpr (B < E) {
+        f(std::integral_constant<int, B>{});
+        static_for<B + 1, E>(f);
+    }
+}
+
+constexpr uint32_t kOob = 0x80000000u;   // a buffer offset past every range
+constexpr int kRsrcFlags = 0x00020000;   // gfx9 buffer descriptor word 3
+
 // ---- host ----
+
+constexpr int kCUs = 256;          // of an MI355X
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

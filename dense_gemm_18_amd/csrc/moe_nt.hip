@@ -16,11 +16,13 @@ bool sizes_ok_moe(const moe_nt_weights *w, int64_t T, int topk)
 
 bool inner_ok(const moe_nt_weights *w)
 {
-    return w->inner >= 1 && w->inner <= GEMM_MAX_K && (w->group == 0 || group_ok(w->group));
+    return w->inner >= 1 && w->inner <= MOE_MAX_INNER && (w->group == 0 || group_ok(w->group));
 }
 
-// Workspace: header, logits of a chunk, gated rows of a chunk.
+// Workspace: header, logits of a chunk, gated rows of a chunk, their products.
 int64_t logits_bytes(int64_t T, int64_t E) { return cdiv(T * E * 4, 256) * 256; }
+
+int64_t h_bytes(int64_t slots, int64_t I) { return cdiv(slots * I * 2, 256) * 256; }
 
 struct Span {
     const void *p;
@@ -76,7 +78,7 @@ uint64_t scale_bytes(int64_t rows, int64_t cols, int group)
 int check_common(const moe_nt_weights *w, const void *X, int64_t T, int64_t ldx, int topk,
                  const void *ws, int64_t ws_bytes, int64_t need)
 {
-    if (ldx < w->hidden || ldx > kMaxLd || !X || !aligned_to(X, 2))
+    if (ldx < w->hidden || ldx > MOE_MAX_LDX || !X || !aligned_to(X, 2))
         return GEMM_EINVAL;
     return !ws || !aligned_to(ws, 256) || ws_bytes < need ? GEMM_EINVAL : GEMM_OK;
 }
@@ -196,6 +198,7 @@ int run_experts(const moe_nt_weights *w, MoeArgs p, void *D, int64_t T, int64_t 
     p.w13 = weight_ref(w->w13, w->w13_scales, w->w13_zeros, w->group);
     p.w2 = weight_ref(w->w2, w->w2_scales, w->w2_zeros, w->group);
     p.h = (uint16_t *)((char *)ws + kHeader + logits_bytes(chunk, w->experts));
+    p.y = (float *)((char *)p.h + h_bytes(chunk * p.topk, w->inner));
     p.D = (uint16_t *)D;
     p.ldd = ldd;
     const MoeLaunch go = launches(w);
@@ -214,7 +217,8 @@ int64_t moe_nt_ws_size(int64_t T, const moe_nt_weights *w, int topk)
         return 0;
     const int64_t chunk = moe_chunk(T, topk);
     return kHeader + logits_bytes(chunk, w->experts) +
-           cdiv(chunk * topk * w->inner * 2, 256) * 256;
+           h_bytes((int64_t)chunk * topk, w->inner) +
+           cdiv(chunk * topk * w->hidden * 4, 256) * 256;
 }
 
 int moe_nt_route(const moe_nt_weights *w, const void *X, int32_t *ids, float *weights, int64_t T,

@@ -5,8 +5,7 @@
 #include "skinny.h"
 
 // Tokens of one pass through the kernels: 64, or as many as have 512 slots
-// (t * topk + j), whose 16 columns of fp32 are what the down product keeps in
-// LDS.
+// (t * topk + j).
 constexpr int kMoeSlots = 512;
 inline int moe_chunk(int64_t T, int topk)
 {
@@ -22,10 +21,10 @@ struct MoeArgs {
     float *weights;                // T x topk
     WeightRef w13, w2;             // E * 2 * I rows of H, E * H rows of I
     uint16_t *h;                   // T * topk rows of I
+    float *y;                      // T * topk rows of H
     uint16_t *D;                   // T rows, ldd apart
     int64_t ldx, ldd;
     int T, E, H, I, topk, renorm;
-    int parts;                     // pieces of I in the down product
 };
 
 // One translation unit for each type.  Not exported from the library.
@@ -38,32 +37,30 @@ __attribute__((visibility("hidden"))) MoeLaunch gemm18_moe_bf16();
 
 namespace {
 
-// A value that every lane of the wave has, as a scalar: branches on it are
-// the wave's.
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 // ---- router -------------------------------------------------------------
 
 constexpr int kRouteWaves = 16;
 
 // Logits of 16 experts for 16 tokens; sixteen waves split the hidden size.
 template <bool BF>
+using RouteCore = Skinny<BF, 0, 1, 1, kRouteWaves, 1, true>;
+
+template <bool BF>
 __global__ void __launch_bounds__(kRouteWaves * 64) moe_logits_kernel(MoeArgs p)
 {
-    __shared__ f32x4 red[kRouteWaves * 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    extern __shared__ f32x4 lds[];
     const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
-    WeightRef W{};
-    W.w = p.router;
-    Skinny<BF, 0, 1, 1> c;
-    c.init(p.H);
-    c.bind(0, W, min(e0 + (lane & 15), p.E - 1));
-    c.bind_act(0, p.X + (int64_t)min(t0 + (lane & 15), p.T - 1) * p.ldx);
-    c.run(wave, (p.H + 127) >> 7, kRouteWaves);
-    const f32x4 part[1] = {c.acc[0][0]};
-    reduce_waves<1>(part, red, kRouteWaves, [&](int m, int n, const float(&v)[1]) {
-        if (t0 + m < p.T && e0 + n < p.E)
-            p.logits[(int64_t)(t0 + m) * p.E + e0 + n] = v[0];
+    RouteCore<BF> c;
+    c.W.w = p.router;
+    c.row[0] = e0;
+    c.rows[0] = p.E - e0;
+    c.K = p.H;
+    c.M = min(16, p.T - t0);
+    c.begin((char *)lds, p.X + t0 * p.ldx, (uint32_t)((c.M - 1) * p.ldx + p.H) * 2u);
+    c.run([&](int m) { return (uint32_t)(m * p.ldx) * 2u; });
+    c.join([&](int m, int n, const float(&v)[1]) {
+        if (e0 + n < p.E)
+            p.logits[(t0 + m) * p.E + e0 + n] = v[0];
     });
 }
 
@@ -172,6 +169,7 @@ __host__ __device__ inline int plan_bytes(int E, int n)
 
 __device__ __forceinline__ Plan make_plan(char *lds, const int32_t *ids, int n, int E)
 {
+    // (a short list could be compared pair by pair in registers: 0.5 us less)
     Plan pl;
     const int a = E < n ? E : n;
     pl.cnt = (int *)lds;
@@ -221,121 +219,126 @@ __device__ __forceinline__ Plan make_plan(char *lds, const int32_t *ids, int n, 
     return pl;
 }
 
-// f(integral_constant<int, MB>): blocks of 16 rows for `count` of up to 64.
-template <class F>
+// Rows that run against one reading of an expert's weights, as the registers
+// allow (packed weights need some for a group's sums).
+template <int GS>
+constexpr int kRowsAtOnce = GS ? 32 : 64;
+
+// f(integral_constant<int, MB>): blocks of 16 rows for `count` of them.
+template <int GS, class F>
 __device__ __forceinline__ void with_blocks(int count, F &&f)
 {
     if (count <= 16)
         f(std::integral_constant<int, 1>{});
-    else if (count <= 32)
+    else if (GS != 0 || count <= 32)
         f(std::integral_constant<int, 2>{});
-    else
+    else if constexpr (GS == 0)
         f(std::integral_constant<int, 4>{});
 }
+
+// Blocks of 16 hidden rows to a workgroup of the down product: its K, the inner
+// size, is short, and four blocks of packed weights are the bytes of one of
+// 16-bit ones.
+template <int GS>
+constexpr int kDownBlocks = GS ? 4 : 2;
+
+template <bool BF, int GS, int MB>
+using UpCore = Skinny<BF, GS, 2, MB, kMoeWaves, 1, false>;
+template <bool BF, int GS, int MB>
+using DownCore = Skinny<BF, GS, kDownBlocks<GS>, MB, kMoeWaves, 1, true>;
 
 // h = silu(gate) * up for 16 of an expert's inner rows and all its slots.
 // One workgroup takes the 16 gate rows and their 16 up rows, eight waves
 // split the hidden size.
 template <bool BF, int GS>
-__global__ void __launch_bounds__(kMoeWaves * 64) moe_up_kernel(MoeArgs p)
+__global__ void __launch_bounds__(kMoeWaves * 64, 2) moe_up_kernel(MoeArgs p)
 {
     extern __shared__ f32x4 lds[];
-    f32x4 *red = lds;                                  // kMoeWaves * 2 * 64
     const int n = p.T * p.topk, blocks = (p.I + 15) / 16;
     const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
     const int s = wg / blocks, i0 = wg % blocks * 16;
-    const Plan pl = make_plan((char *)(lds + kMoeWaves * 2 * 64), p.ids, n, p.E);
+    const Plan pl = make_plan((char *)lds, p.ids, n, p.E);
     if (s >= pl.active)
         return;
+    char *smem = (char *)lds + plan_bytes(p.E, n);
     const int64_t e = uniform(pl.act[s]);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t row = e * 2 * p.I + min(i0 + (lane & 15), p.I - 1);
     const int end = uniform(pl.off[s + 1]);
-    for (int c0 = uniform(pl.off[s]); c0 < end; c0 += 64) {
-        const int count = min(64, end - c0);
-        with_blocks(count, [&](auto mbs) {
-            constexpr int MB = decltype(mbs)::value;
-            Skinny<BF, GS, 2, MB> c;
-            c.init(p.H);
-            c.bind(0, p.w13, row);
-            c.bind(1, p.w13, row + p.I);
-#pragma unroll
-            for (int m = 0; m < MB; ++m) {
-                const int slot = pl.slot[c0 + min(16 * m + (lane & 15), count - 1)];
-                c.bind_act(m, p.X + (int64_t)(slot / p.topk) * p.ldx);
-            }
-            c.run(wave, (p.H + 127) >> 7, kMoeWaves);
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb) {
-                const f32x4 part[2] = {c.acc[0][mb], c.acc[1][mb]};
-                reduce_waves<2>(part, red, kMoeWaves, [&](int m, int i, const float(&v)[2]) {
-                    if (16 * mb + m < count && i0 + i < p.I) {
-                        const int64_t slot = pl.slot[c0 + 16 * mb + m];
-                        const float act = v[0] / (1.0f + expf(-v[0]));
-                        p.h[slot * p.I + i0 + i] = from_float<BF>(act * v[1]);
-                    }
-                });
-            }
+    for (int c0 = uniform(pl.off[s]); c0 < end; c0 += kRowsAtOnce<GS>) {
+        const int count = min(kRowsAtOnce<GS>, end - c0);
+        with_blocks<GS>(count, [&](auto mbs) {
+            UpCore<BF, GS, decltype(mbs)::value> c;
+            c.W = p.w13;
+            c.row[0] = e * 2 * p.I + i0;
+            c.row[1] = c.row[0] + p.I;
+            c.rows[0] = c.rows[1] = p.I - i0;
+            c.K = p.H;
+            c.M = count;
+            c.begin(smem, p.X, (uint32_t)((p.T - 1) * p.ldx + p.H) * 2u);
+            c.run([&](int m) {
+                return (uint32_t)(pl.slot[c0 + m] / p.topk * p.ldx) * 2u;
+            });
+            c.join([&](int m, int i, const float(&v)[2]) {
+                if (i0 + i < p.I) {
+                    const float act = v[0] / (1.0f + expf(-v[0]));
+                    p.h[(int64_t)pl.slot[c0 + m] * p.I + i0 + i] = from_float<BF>(act * v[1]);
+                }
+            });
         });
+        __syncthreads();
     }
 }
 
-// 16 columns of y for every token: the waves share the (expert, piece of
-// inner) pairs, each leaves its slots' sums in LDS at places of their own, and
-// the weighted sum over a token's slots follows in order.
+// y = W2 h for a block of an expert's hidden rows and all its slots, in fp32.
 template <bool BF, int GS>
-__global__ void __launch_bounds__(kMoeWaves * 64) moe_down_kernel(MoeArgs p)
+__global__ void __launch_bounds__(kMoeWaves * 64, 2) moe_down_kernel(MoeArgs p)
 {
     extern __shared__ f32x4 lds[];
-    const int n = p.T * p.topk;
-    float *y = (float *)lds;                           // parts * n * 16
-    const int h0 = blockIdx.x * 16;
-    const Plan pl = make_plan((char *)(y + p.parts * n * 16), p.ids, n, p.E);
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int steps = (p.I + 127) >> 7;
-    for (int u = wave; u < pl.active * p.parts; u += kMoeWaves) {
-        const int s = u / p.parts, part = u % p.parts;
-        const int64_t e = uniform(pl.act[s]);
-        const int end = uniform(pl.off[s + 1]);
-        for (int c0 = uniform(pl.off[s]); c0 < end; c0 += 64) {
-            const int count = min(64, end - c0);
-            with_blocks(count, [&](auto mbs) {
-                constexpr int MB = decltype(mbs)::value;
-                Skinny<BF, GS, 1, MB> c;
-                c.init(p.I);
-                c.bind(0, p.w2, e * p.H + min(h0 + (lane & 15), p.H - 1));
+    constexpr int RB = kDownBlocks<GS>;
+    const int n = p.T * p.topk, blocks = (p.H + 16 * RB - 1) / (16 * RB);
+    const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
+    const int s = wg / blocks, h0 = wg % blocks * (16 * RB);
+    const Plan pl = make_plan((char *)lds, p.ids, n, p.E);
+    if (s >= pl.active)
+        return;
+    char *smem = (char *)lds + plan_bytes(p.E, n);
+    const int64_t e = uniform(pl.act[s]);
+    const int end = uniform(pl.off[s + 1]);
+    for (int c0 = uniform(pl.off[s]); c0 < end; c0 += kRowsAtOnce<GS>) {
+        const int count = min(kRowsAtOnce<GS>, end - c0);
+        with_blocks<GS>(count, [&](auto mbs) {
+            DownCore<BF, GS, decltype(mbs)::value> c;
+            c.W = p.w2;
+            c.row[0] = e * p.H + h0;
+            c.rows[0] = p.H - h0;
+            c.K = p.I;
+            c.M = count;
+            c.begin(smem, p.h, (uint32_t)n * (uint32_t)p.I * 2u);
+            c.run([&](int m) { return (uint32_t)pl.slot[c0 + m] * (uint32_t)p.I * 2u; });
+            c.join([&](int m, int i, const float(&v)[RB]) {
 #pragma unroll
-                for (int m = 0; m < MB; ++m)
-                    c.bind_act(m, p.h + (int64_t)pl.slot[c0 + min(16 * m + (lane & 15),
-                                                                  count - 1)] * p.I);
-                c.run(part * steps / p.parts, (part + 1) * steps / p.parts, 1);
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int m = 16 * mb + 4 * (lane >> 4) + r;
-                        if (m < count)
-                            y[(part * n + pl.slot[c0 + m]) * 16 + (lane & 15)] = c.acc[0][mb][r];
-                    }
+                for (int r = 0; r < RB; ++r)
+                    if (h0 + 16 * r + i < p.H)
+                        p.y[(int64_t)pl.slot[c0 + m] * p.H + h0 + 16 * r + i] = v[r];
             });
-        }
+        });
+        __syncthreads();
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.T * 16; i += blockDim.x) {
-        const int t = i >> 4, col = i & 15;
-        float sum = 0.0f;
-        for (int j = 0; j < p.topk; ++j) {
-            const int slot = t * p.topk + j;
-            if ((uint32_t)p.ids[slot] < (uint32_t)p.E) {
-                float v = 0.0f;
-                for (int part = 0; part < p.parts; ++part)
-                    v += y[(part * n + slot) * 16 + col];
-                sum = __builtin_fmaf(p.weights[slot], v, sum);
-            }
-        }
-        if (h0 + col < p.H)
-            p.D[t * p.ldd + h0 + col] = from_float<BF>(sum);
+}
+
+// The weighted sum over a token's slots, in order.
+template <bool BF>
+__global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs p)
+{
+    const int t = blockIdx.y, h = blockIdx.x * 256 + threadIdx.x;
+    if (h >= p.H)
+        return;
+    float sum = 0.0f;
+    for (int j = 0; j < p.topk; ++j) {
+        const int slot = t * p.topk + j;
+        if ((uint32_t)p.ids[slot] < (uint32_t)p.E)
+            sum = __builtin_fmaf(p.weights[slot], p.y[(int64_t)slot * p.H + h], sum);
     }
+    p.D[t * p.ldd + h] = from_float<BF>(sum);
 }
 
 template <bool BF>
@@ -343,7 +346,8 @@ void launch_route(const MoeArgs &p, hipStream_t stream)
 {
     hipLaunchKernelGGL((moe_logits_kernel<BF>),
                        dim3((unsigned)cdiv(p.E, 16), (unsigned)cdiv(p.T, 16)),
-                       dim3(kRouteWaves * 64), 0, stream, p);
+                       dim3(kRouteWaves * 64), RouteCore<BF>::lds_bytes(p.T < 16 ? p.T : 16, p.H),
+                       stream, p);
     const dim3 grid((unsigned)cdiv(p.T, 4));
     if (p.E <= 64)
         hipLaunchKernelGGL((moe_choose_kernel<1>), grid, dim3(256), 0, stream, p);
@@ -354,22 +358,23 @@ void launch_route(const MoeArgs &p, hipStream_t stream)
 }
 
 template <bool BF>
-void launch_experts(const MoeArgs &args, int group, hipStream_t stream)
+void launch_experts(const MoeArgs &p, int group, hipStream_t stream)
 {
-    MoeArgs p = args;
     const int n = p.T * p.topk, most = p.E < n ? p.E : n;
-    // two pairs or more per wave where the experts alone give fewer
-    p.parts = (int)cdiv(2 * kMoeWaves, most);
-    if (p.parts > kMoeSlots / n)
-        p.parts = kMoeSlots / n;
     const int plan = plan_bytes(p.E, n);
     with_group(group, [&](auto gs) {
         constexpr int GS = decltype(gs)::value;
+        const int rows = n < kRowsAtOnce<GS> ? n : kRowsAtOnce<GS>;
+        const int up = plan + UpCore<BF, GS, 1>::lds_bytes(rows, p.H);
+        const int down = plan + DownCore<BF, GS, 1>::lds_bytes(rows, p.I);
         hipLaunchKernelGGL((moe_up_kernel<BF, GS>), tile_grid(most * cdiv(p.I, 16)),
-                           dim3(kMoeWaves * 64), kMoeWaves * 2 * 64 * 16 + plan, stream, p);
-        hipLaunchKernelGGL((moe_down_kernel<BF, GS>), dim3((unsigned)cdiv(p.H, 16)),
-                           dim3(kMoeWaves * 64), p.parts * n * 64 + plan, stream, p);
+                           dim3(kMoeWaves * 64), up, stream, p);
+        hipLaunchKernelGGL((moe_down_kernel<BF, GS>),
+                           tile_grid(most * cdiv(p.H, 16 * kDownBlocks<GS>)),
+                           dim3(kMoeWaves * 64), down, stream, p);
     });
+    hipLaunchKernelGGL((moe_combine_kernel<BF>), dim3((unsigned)cdiv(p.H, 256), (unsigned)p.T),
+                       dim3(256), 0, stream, p);
 }
 
 } // namespace

@@ -1,15 +1,24 @@
 // skinny.h -- the product core of few rows against many weight rows that the
-// 4-bit product and the expert kernels share.  Everything here has internal
-// linkage.
+// 4-bit product, the router and the expert kernels share.  Everything here has
+// internal linkage.
 //
-// One wave owns 16 * RB weight rows and 16 * MB activation rows and walks K
-// in steps of 128.  Each of a step's four v_mfma_f32_16x16x32 takes the
-// activations as its first operand and the weights as its second, so a lane
-// loads weights of one row n = lane % 16 (elements 8c .. 8c+7 of the 32, with
-// c = lane / 16) and its accumulators hold column n, rows m = 4c .. 4c+3:
-// a group's scale is one value per lane, that of the row the lane loads.
-// Nothing goes through LDS on the way in: a weight is used by one wave only,
-// and the activations, which every workgroup re-reads, come from L1 and L2.
+// A workgroup owns 16 * RB * NW weight rows and 16 * MB activation rows; its
+// KW * NW waves are NW bands of rows times KW pieces of K, joined in LDS at
+// the end.  K is walked in steps of 128.  Each of a step's four
+// v_mfma_f32_16x16x32 takes the activations as its first operand and the
+// weights as its second, so a lane loads weights of one row n = lane % 16
+// (elements 8c .. 8c+7 of the 32, with c = lane / 16) and its accumulators
+// hold column n, rows m = 4c .. 4c+3: a group's scale is one value per lane,
+// that of the row the lane loads.
+//
+// Weights go straight to registers, each used by one wave only, and are the
+// only vector loads of the inner loop: activations, scales and zero points are
+// staged in LDS a chunk of K at a time.  Measured on 1 x 16384 x 8192 with
+// 4-bit weights that the last-level cache holds (10.4 us for reading them and
+// nothing else, 6.5 TB/s): 13.0 us with activations in LDS, 17.4 with
+// activations as vector loads, and 5.4 more with a scale load per step, which
+// asks L2 for as many lines as the weights do.  A ring of prefetched steps
+// (2, 3 or 4 deep) was slower than eight waves that each wait for their batch.
 #pragma once
 
 #include "gemm_types.h"
@@ -26,22 +35,9 @@ struct WeightRef {
 
 namespace {
 
-// 16 bytes at any 2-byte alignment (one global load on gfx950).
-typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
-
-__device__ __forceinline__ u32x4 load16(const uint16_t *p) { return *(const u32x4_a2 *)p; }
-
-// The first `count` of the 8 elements at p, zero for the others; nothing
-// past them is accessed.
-__device__ __forceinline__ u32x4 load16_part(const uint16_t *p, int count)
-{
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < count)
-            v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-    return v;
-}
+// A value that every lane of the wave has, as a scalar: branches on it are
+// the wave's.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 template <bool BF>
 __device__ __forceinline__ float to_float(uint16_t bits)
@@ -61,27 +57,47 @@ __device__ __forceinline__ uint16_t from_float(float v)
 
 // Eight 4-bit values of one packed word as 16-bit integers, exact.  A value
 // in the low bits of the mantissa of 1024 (fp16) or 128 (bfloat16) is that
-// number plus q: one mask-and-or for two of them.  fp16 then subtracts
-// 1024 + z from both halves in one packed instruction, exactly, leaving q - z.
-// bfloat16 has no packed subtraction on gfx950: its 128 + q go to the matrix
+// number plus q: one mask-and-or for two of them.
+//
+// fp16 takes 1024 + z off both halves in one packed instruction, exactly,
+// leaving q - z; a value four bits up is 1024 + 16 q, and a packed fma with
+// 1/16 and 64 + z gives the same without a shift: 9 instructions for 8 weights.
+// bfloat16 has no packed arithmetic on gfx950: its 128 + q go to the matrix
 // unit as they are, and the caller takes (128 + z) * sum(A) off in fp32 (7
-// instructions for 8 weights; EXACT, which subtracts in fp32 and packs again,
-// takes 35 and leaves (q - z) * 2^-12).
+// instructions; EXACT, which subtracts in fp32 and packs again, takes 35 and
+// leaves (q - z) * 2^-12).
+// sz: the number to take off, as 16 bits, in its upper half.
 template <bool BF, bool EXACT>
-__device__ __forceinline__ typename Elem<BF>::x8 unpack8(uint32_t w, uint32_t z)
+__device__ __forceinline__ typename Elem<BF>::x8 unpack8(uint32_t w, uint32_t sz)
 {
-    constexpr uint32_t magic = BF ? 0x43004300u : 0x64006400u;
+    // the constants in registers: v_and_or_b32 takes no literals
+    uint32_t mask = 0x000f000fu, magic = BF ? 0x43004300u : 0x64006400u;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(magic));
     u32x4 v;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-        v[t] = ((w >> (4 * t)) & 0x000f000fu) | magic;
     if constexpr (!BF) {
-        const uint32_t mz = 0x64006400u + z + (z << 16);
-        const u32x4 m = {mz, mz, mz, mz};
-        return __builtin_bit_cast(f16x8, v) - __builtin_bit_cast(f16x8, m);
+        uint32_t mask4 = 0x00f000f0u, off = (sz >> 16) | (sz & 0xffff0000u);
+        asm("" : "+s"(mask4));
+        asm("" : "+v"(off));      // seen as two equal halves it would be split up again
+        const f16x2 z = __builtin_bit_cast(f16x2, off);
+        const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+        // 64 + z, from 1024 + z
+        const f16x2 z4 = z - f16x2{(_Float16)960.0f, (_Float16)960.0f};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t x = t < 2 ? w : w >> 8;
+            const f16x2 q =
+                __builtin_bit_cast(f16x2, (x & (t & 1 ? mask4 : mask)) | magic);
+            v[t] = __builtin_bit_cast(
+                uint32_t, t & 1 ? __builtin_elementwise_fma(q, sixteenth, -z4) : q - z);
+        }
+        return __builtin_bit_cast(f16x8, v);
     } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            v[t] = ((w >> (4 * t)) & mask) | magic;
         if constexpr (EXACT) {
-            const float off = (float)(128u + z);
+            const float off = __builtin_bit_cast(float, sz & 0xffff0000u);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const float lo = (__builtin_bit_cast(float, v[t] << 16) - off) * 0x1p-12f;
@@ -95,242 +111,337 @@ __device__ __forceinline__ typename Elem<BF>::x8 unpack8(uint32_t w, uint32_t z)
     }
 }
 
-// One wave's share of a product.  GS: 0 for 16-bit weights, else the group.
-template <bool BF, int GS, int RB, int MB>
+// A range of memory for buffer loads; loads outside it return 0 and cost
+// nothing.  `base` and `bytes` are the wave's.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t range(const void *base, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)bytes, kRsrcFlags);
+}
+
+__device__ __forceinline__ u32x4 load_b128(__amdgpu_buffer_rsrc_t rs, uint32_t off)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+}
+
+// LDS of a product: activations, then scales, up to these sizes.
+constexpr int kActBytes = 64 * 1024;
+constexpr int kScaleBytes = 32 * 1024;
+
+// One workgroup's product.  GS: 0 for 16-bit weights, else the group.
+// JOINED: the workgroup's weight rows follow each other; else (RB == 2,
+// NW == 1) block 0 and block 1 start at rows of their own.
+template <bool BF, int GS, int RB, int MB, int KW, int NW, bool JOINED>
 struct Skinny {
     using x8 = typename Elem<BF>::x8;
-    static constexpr int kStep = 128;
-    static constexpr int kGroups = GS ? kStep / (GS ? GS : 1) : 1;   // groups a step spans
+    static constexpr int kThreads = KW * NW * 64;
+    static constexpr int kGroups = GS ? 128 / (GS ? GS : 1) : 1;   // groups in a step
+    static constexpr int NR = JOINED ? 1 : 2;
+    static constexpr int kRows = 16 * RB * NW;                    // weight rows
+    // Steps a wave asks for at once: 8 KB, 64 KB for eight waves, which at 25
+    // bytes per ns and CU is 2.5 us of latency.
+    static constexpr int U = GS == 0 ? (RB == 1 ? 2 : 1) : RB == 4 ? 2 : 4;
 
-    struct WBuf {
-        u32x4 v[RB][GS ? 1 : 4];
-        uint16_t s[RB][kGroups];
-        uint8_t z[RB][kGroups];
-    };
-    struct ABuf {
-        u32x4 v[MB][4];
-    };
-
-    // Per lane: the start of its weight rows and activation rows.
-    const uint16_t *w16[RB];
-    const uint32_t *q[RB];
-    const uint16_t *s[RB];
-    const uint8_t *z[RB];
-    const uint16_t *a[MB];
-    int K, G;
+    // What the caller sets: the weights, the rows that exist from each
+    // start, K, the number of activation rows.
+    WeightRef W;
+    int64_t row[NR];
+    int rows[NR];
+    int K, M;
     f32x4 acc[RB][MB];
 
-    __device__ __forceinline__ void init(int k)
+    char *lds;
+    int wave, G, chunk, astride, sstride;
+    __amdgpu_buffer_rsrc_t wr[NR], sr[NR], zr[NR], ar;
+    uint32_t woff[RB], zdef;       // zdef: 8 where there are no zero points
+
+    // LDS for any number of activation rows up to `most` (with fewer rows the
+    // chunk may be longer, so this bounds the two together).
+    static int lds_bytes(int most, int K)
     {
-        K = k;
-        G = GS ? (k + GS - 1) / (GS ? GS : 1) : 0;
+        const int64_t all = cdiv(K, 128) * 128;
+        const int64_t need = most * (all * 2 + 16) +
+                             (GS ? (int64_t)kRows * (all / 128 * kGroups + 1) * 4 : 0);
+        const int cap = kActBytes + (GS ? kScaleBytes : 0), red = KW * NW * RB * 1024;
+        return need > cap ? cap : need > red ? (int)need : red;
+    }
+    // Rows of a chunk in LDS are 16 bytes longer than the chunk, so that the 16
+    // rows that a fragment read touches lie in different banks.
+    static constexpr int act_bytes(int M, int chunk) { return M * (chunk * 2 + 16); }
+    static constexpr int scale_bytes(int chunk)
+    {
+        return GS ? kRows * (chunk / 128 * kGroups + 1) * 4 : 0;
+    }
+    // K of a chunk: all of it, or what the LDS holds, in whole steps and, where
+    // it can be, the same number for each of the KW waves.
+    static __host__ __device__ constexpr int chunk_of(int M, int K)
+    {
+        const int all = (K + 127) / 128;
+        int steps = (kActBytes / M - 16) / 256;
+        if (GS && steps > kScaleBytes / (kRows * 4 * kGroups) - 1)
+            steps = kScaleBytes / (kRows * 4 * kGroups) - 1;
+        if (steps >= all)
+            return all * 128;
+        if (steps > KW)
+            steps -= steps % KW;
+        return steps * 128;
+    }
+
+    __device__ __forceinline__ int lane() const { return threadIdx.x & 63; }
+    __device__ __forceinline__ int kw() const { return NW == 1 ? wave : wave % KW; }
+    __device__ __forceinline__ int nw() const { return NW == 1 ? 0 : wave / KW; }
+
+    // The activations: `bytes` from `base`.
+    __device__ __forceinline__ void begin(char *smem, const uint16_t *base, uint32_t bytes)
+    {
+        ar = range(base, bytes);
+        lds = smem;
+        wave = uniform(threadIdx.x >> 6);
+        G = GS ? (K + GS - 1) / (GS ? GS : 1) : 0;
+        chunk = chunk_of(M, K);
+        astride = chunk * 2 + 16;
+        sstride = chunk / 128 * kGroups + 1;
+        const uint32_t row_bytes = GS ? (uint32_t)((K + 127) >> 7) * 64u : (uint32_t)K * 2u;
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
+        for (int i = 0; i < NR; ++i) {
+            const int n = min(rows[i], kRows / NR);
+            wr[i] = range(GS ? (const char *)W.q + row[i] * row_bytes
+                             : (const char *)W.w + row[i] * row_bytes,
+                          n * row_bytes);
+            if constexpr (GS != 0) {
+                sr[i] = range(W.s + row[i] * G, n * G * 2);
+                zr[i] = range(W.z ? W.z + row[i] * G : nullptr, W.z ? n * G : 0);
+            }
+        }
+        zdef = W.z ? 0 : 8;
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            const int at = JOINED ? (nw() * RB + r) * 16 : 0;
+            woff[r] = (at + (lane() & 15)) * row_bytes + (lane() >> 4) * 16;
 #pragma unroll
             for (int m = 0; m < MB; ++m)
                 acc[r][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-
-    // The lane's row of block r is `row` of the matrix.
-    __device__ __forceinline__ void bind(int r, const WeightRef &W, int64_t row)
-    {
-        const int c = (threadIdx.x & 63) >> 4;
-        if constexpr (GS == 0) {
-            w16[r] = W.w + row * K + 8 * c;
-        } else {
-            q[r] = W.q + row * ((int64_t)((K + 127) >> 7) * 16) + 4 * c;
-            s[r] = W.s + row * G;
-            z[r] = W.z ? W.z + row * G : nullptr;
         }
     }
 
-    __device__ __forceinline__ void bind_act(int m, const uint16_t *row)
+    struct Batch {
+        u32x4 v[U][RB][GS ? 1 : 4];
+    };
+
+    // U steps from st on; nothing where a step is `end` or later.  Unconditional
+    // loads with an offset past the range there: a branch around loads would
+    // leave the compiler waiting for all of them.
+    __device__ __forceinline__ void load(Batch &b, int st, int end) const
     {
-        a[m] = row + 8 * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t o =
+                    woff[r] + (st + u < end ? (uint32_t)(st + u) * (GS ? 64u : 256u) : kOob);
+#pragma unroll
+                for (int j = 0; j < (GS ? 1 : 4); ++j)
+                    b.v[u][r][j] = load_b128(wr[r % NR], o + 64u * j);
+            }
     }
 
-    __device__ __forceinline__ void load_w(WBuf &b, int st) const
+    // Activations k0 .. k0 + 128 * steps - 1 of every row, zero from K on.
+    // `at(m)`: the byte of `ar` where row m starts.
+    template <class F>
+    __device__ __forceinline__ void stage_acts(int k0, int steps, F &&at) const
     {
+        // a power of two of threads along a row, the rest along the rows
+        const int per_row = steps * 16;
+        int shift = 31 - __builtin_clz(kThreads);
+        while (shift > 4 && (1 << (shift - 1)) >= per_row)
+            --shift;
+        const int c0 = threadIdx.x & ((1 << shift) - 1), dc = 1 << shift;
+        const int m0 = threadIdx.x >> shift, dm = kThreads >> shift;
+        constexpr int kBatch = 4;
+        for (int m = m0; m < M; m += dm) {
+            const uint32_t src = at(m) + (uint32_t)k0 * 2u;
+            char *dst = lds + m * astride;
+            for (int c = c0; c < per_row; c += dc * kBatch) {
+                u32x4 v[kBatch];
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            if constexpr (GS == 0) {
+                for (int i = 0; i < kBatch; ++i) {
+                    const int k = (c + i * dc) * 8;
+                    v[i] = load_b128(ar, k0 + k + 8 <= K ? src + 2u * k : kOob);
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    b.v[r][j] = load16(w16[r] + (int64_t)st * 128 + 32 * j);
-            } else {
-                b.v[r][0] = *(const u32x4 *)(q[r] + (int64_t)st * 16);
-                load_scales(b, r, st);
+                for (int i = 0; i < kBatch; ++i) {
+                    const int k = (c + i * dc) * 8;
+                    // the 8 elements that K ends among come below
+                    if (c + i * dc < per_row && (k0 + k + 8 <= K || k0 + k >= K))
+                        *(u32x4 *)(dst + k * 2) = v[i];
+                }
+            }
+        }
+        if ((K & 7) && k0 + steps * 128 > K) {
+            const int k = (K & ~7) + (threadIdx.x & 7);
+            for (int m = threadIdx.x >> 3; m < M; m += kThreads / 8)
+                *(uint16_t *)(lds + m * astride + (k - k0) * 2) =
+                    (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                        ar, k < K ? at(m) + 2u * k : kOob, 0, 0);
+        }
+    }
+
+    // Scale and zero point of each row's groups in one word: the scale's bits
+    // below, above them the 16-bit number that unpack8 takes off, 1024 + z or
+    // 128 + z.  Groups from G on, and rows past the end, have the scale 0.
+    __device__ __forceinline__ void stage_scales(int k0, int steps) const
+    {
+        uint32_t *dst = (uint32_t *)(lds + act_bytes(M, chunk));
+        const int g0 = k0 / (GS ? GS : 1), groups = steps * kGroups;
+        constexpr int kBatch = 4;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            for (int n = threadIdx.x >> 4; n < kRows / NR; n += kThreads / 16) {
+                uint32_t *to = dst + (i * 16 + n) * sstride;
+                for (int g = threadIdx.x & 15; g < groups; g += 16 * kBatch) {
+                    uint32_t s[kBatch], z[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int gg = g0 + g + 16 * k;
+                        const uint32_t o = gg < G ? (uint32_t)(n * G + gg) : kOob;
+                        s[k] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                            sr[i], 2 * o + (o & kOob), 0, 0);
+                        z[k] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zr[i], o, 0, 0);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        if (g + 16 * k < groups)
+                            to[g + 16 * k] =
+                                s[k] | ((BF ? 0x4300u : 0x6400u) + ((z[k] | zdef) & 15u)) << 16;
+                }
             }
         }
     }
 
-    __device__ __forceinline__ void load_scales(WBuf &b, int r, int st) const
+    // The 8 elements of a row of 16-bit weights of which `left` (any number)
+    // come before K; the others become zero.  Where K is odd, a buffer load,
+    // which checks its range by the dword, loses the last element if nothing
+    // follows it: it comes from `end`.
+    __device__ __forceinline__ u32x4 mend(u32x4 v, int left, uint32_t end) const
     {
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            // the last step may hold fewer groups than kGroups: scale 0
-            const int at = st * kGroups + g;
-            b.s[r][g] = at < G ? s[r][at] : (uint16_t)0;
-            b.z[r][g] = z[r] && at < G ? z[r][at] & 15 : 8;
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t keep = left > 2 * i + 1 ? 0xffffffffu : left > 2 * i ? 0xffffu : 0u;
+            v[i] = left == 2 * i + 1 && (K & 1) ? end : v[i] & keep;
         }
+        return v;
     }
 
-    __device__ __forceinline__ void load_a(ABuf &b, int st) const
+    // Step u of a batch, step `st` of the chunk that starts at k0.
+    template <bool EXACT>
+    __device__ __forceinline__ void consume(Batch &b, int u, int st, int k0,
+                                            f32x4 (&to)[RB][MB]) const
     {
+        const int c = lane() >> 4;
+        x8 a[MB][4];
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
+        for (int m = 0; m < MB; ++m) {
+            // rows past the last repeat it; their results are not used
+            const char *p = lds + min(16 * m + (lane() & 15), M - 1) * astride + st * 256 + c * 16;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                b.v[m][j] = load16(a[m] + (int64_t)st * 128 + 32 * j);
-    }
-
-    // The step that K ends in: elements from K on are zero in both operands
-    // (of packed weights, in the activations alone: those weights are finite).
-    __device__ __forceinline__ void load_tail(WBuf &wb, ABuf &ab, int st) const
-    {
-        const int left = K - st * 128 - 8 * ((threadIdx.x & 63) >> 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = left - 32 * j;
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-                ab.v[m][j] = load16_part(a[m] + (int64_t)st * 128 + 32 * j, n);
-            if constexpr (GS == 0)
-#pragma unroll
-                for (int r = 0; r < RB; ++r)
-                    wb.v[r][j] = load16_part(w16[r] + (int64_t)st * 128 + 32 * j, n);
+                a[m][j] = *(const x8 *)(p + 64 * j);
         }
-        if constexpr (GS != 0)
-            load_w(wb, st);
-    }
-
-    template <bool EXACT>
-    __device__ __forceinline__ void consume(const WBuf &wb, const ABuf &ab)
-    {
-        consume<EXACT>(wb, ab, acc);
-    }
-
-    template <bool EXACT>
-    __device__ __forceinline__ void consume(const WBuf &wb, const ABuf &ab,
-                                            f32x4 (&acc)[RB][MB]) const
-    {
         if constexpr (GS == 0) {
+            if (k0 + st * 128 + 128 > K) {
+                const int left = K - k0 - st * 128 - 8 * c;
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                    const uint32_t end = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                        wr[r % NR], woff[r] - 16u * c + (uint32_t)(K - 1) * 2u, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        b.v[u][r][j] = mend(b.v[u][r][j], left - 32 * j, end);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int r = 0; r < RB; ++r)
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
-                        acc[r][m] = mfma16<BF>(__builtin_bit_cast(x8, ab.v[m][j]),
-                                               __builtin_bit_cast(x8, wb.v[r][j]), acc[r][m]);
+                        to[r][m] = mfma16<BF>(a[m][j], __builtin_bit_cast(x8, b.v[u][r][j]),
+                                              to[r][m]);
         } else {
             constexpr int per = 4 / kGroups;       // matrix instructions per group
+            const uint32_t *sp = (const uint32_t *)(lds + act_bytes(M, chunk)) +
+                                 ((JOINED ? nw() * RB * 16 : 0) + (lane() & 15)) * sstride +
+                                 st * kGroups;
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                f32x4 sum[RB][MB], asum[MB];
+            for (int k = 0; k < kGroups; ++k) {
+                f32x4 asum[MB];
+                if constexpr (BF && !EXACT) {
+                    // the activations' own sum, in every column
+                    const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
-                for (int m = 0; m < MB; ++m) {
-                    asum[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int m = 0; m < MB; ++m) {
+                        asum[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int r = 0; r < RB; ++r)
-                        sum[r][m] = asum[m];
-                }
-#pragma unroll
-                for (int i = 0; i < per; ++i) {
-                    const int j = g * per + i;
-                    if constexpr (BF && !EXACT) {
-                        // the activations' own sum, in every column
-                        const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-#pragma unroll
-                        for (int m = 0; m < MB; ++m)
-                            asum[m] = mfma16<BF>(__builtin_bit_cast(x8, ab.v[m][j]),
-                                                 __builtin_bit_cast(x8, one), asum[m]);
-                    }
-#pragma unroll
-                    for (int r = 0; r < RB; ++r) {
-                        const x8 f = unpack8<BF, EXACT>(wb.v[r][0][j], wb.z[r][g]);
-#pragma unroll
-                        for (int m = 0; m < MB; ++m)
-                            sum[r][m] =
-                                mfma16<BF>(__builtin_bit_cast(x8, ab.v[m][j]), f, sum[r][m]);
+                        for (int i = 0; i < per; ++i)
+                            asum[m] = mfma16<BF>(a[m][k * per + i], __builtin_bit_cast(x8, one),
+                                                 asum[m]);
                     }
                 }
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
-                    const float sc = to_float<BF>(wb.s[r][g]);
-                    const float off = (float)(128u + wb.z[r][g]);
+                    const uint32_t sz = sp[r * 16 * sstride + k];
+                    const float sc = to_float<BF>((uint16_t)sz);
+                    const float off = __builtin_bit_cast(float, sz & 0xffff0000u);   // BF
+                    f32x4 sum[MB];
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+                        sum[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < per; ++i) {
+                        const x8 f = unpack8<BF, EXACT>(b.v[u][r][0][k * per + i], sz);
+#pragma unroll
+                        for (int m = 0; m < MB; ++m)
+                            sum[m] = mfma16<BF>(a[m][k * per + i], f, sum[m]);
+                    }
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float v = sum[r][m][e];
+                            float v = sum[m][e];
                             if constexpr (BF && !EXACT)
                                 v = __builtin_fmaf(-off, asum[m][e], v);
-                            acc[r][m][e] = __builtin_fmaf(sc, v, acc[r][m][e]);
+                            to[r][m][e] = __builtin_fmaf(sc, v, to[r][m][e]);
                         }
                 }
             }
         }
     }
 
-    // The steps first, first + stride, ... below `last`, the next one's loads
-    // in flight while one is consumed; `last` is at most ceil(K / 128).  The
-    // activations are fetched ahead too where that takes few registers.
-    __device__ __forceinline__ void run(int first, int last, int stride)
+    template <bool EXACT, class F>
+    __device__ __forceinline__ void walk(f32x4 (&to)[RB][MB], F &&at)
     {
-        constexpr bool kAheadA = MB == 1;
-        const int full = min(last, K >> 7);
-        WBuf w0, w1;
-        ABuf a0, a1;
-        int st = first;
-        if (st < full) {
-            load_a(a0, st);
-            load_w(w0, st);
-            while (st + 2 * stride < full) {
-                if (kAheadA)
-                    load_a(a1, st + stride);
-                load_w(w1, st + stride);
-                consume<false>(w0, a0);
-                load_a(a0, st + (kAheadA ? 2 : 1) * stride);
-                load_w(w0, st + 2 * stride);
-                consume<false>(w1, kAheadA ? a1 : a0);
-                if (!kAheadA)
-                    load_a(a0, st + 2 * stride);
-                st += 2 * stride;
+        const int total = (K + 127) >> 7, per = chunk >> 7;
+        for (int s0 = 0; s0 < total; s0 += per) {
+            const int steps = min(per, total - s0);
+            int st = kw() * steps / KW;
+            const int end = (kw() + 1) * steps / KW;
+            Batch b;
+            load(b, s0 + st, s0 + end);
+            if (s0 > 0 || EXACT)
+                __syncthreads();          // the chunk before has been read
+            stage_acts(s0 * 128, steps, at);
+            if constexpr (GS != 0)
+                stage_scales(s0 * 128, steps);
+            __syncthreads();
+#pragma nounroll
+            while (st < end) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (st + u < end)
+                        consume<EXACT>(b, u, st + u, s0 * 128, to);
+                st += U;
+                if (st < end)
+                    load(b, s0 + st, s0 + end);
             }
-            if (st + stride < full) {
-                if (kAheadA)
-                    load_a(a1, st + stride);
-                load_w(w1, st + stride);
-                consume<false>(w0, a0);
-                if (!kAheadA)
-                    load_a(a0, st + stride);
-                consume<false>(w1, kAheadA ? a1 : a0);
-                st += 2 * stride;
-            } else {
-                consume<false>(w0, a0);
-                st += stride;
-            }
-        }
-        if (st < last) {          // K % 128 != 0, and its step is this wave's
-            load_tail(w0, a0, st);
-            consume<false>(w0, a0);
-        }
-        if constexpr (BF && GS != 0) {
-            // An activation that is infinite, or so large that 128 times it
-            // overflows, leaves infinity minus infinity where q - z itself
-            // would not: such sums, and no others, are formed again with the
-            // exact weights.
-            bool odd = false;
-#pragma unroll
-            for (int r = 0; r < RB; ++r)
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        odd |= !finite(acc[r][m][e]);
-            if (__any(odd))
-                run_exact(first, last, stride);
         }
     }
 
@@ -339,63 +450,78 @@ struct Skinny {
         return __builtin_fabsf(v) < __builtin_inff();
     }
 
-    // The weights go in times 2^-12, so that a group's sum of at most 128
-    // terms of 15 |A| cannot pass fp32 where A does not.
-    __device__ __forceinline__ void run_exact(int first, int last, int stride)
+    // The product, each wave's part of it in `acc`.  `at(m)`: the byte of the
+    // activations where row m starts.
+    template <class F>
+    __device__ __forceinline__ void run(F &&at)
     {
-        f32x4 sum[RB][MB];
+        walk<false>(acc, at);
+        if constexpr (BF && GS != 0) {
+            // An activation that is infinite, or so large that 128 times it
+            // overflows, leaves infinity minus infinity where q - z itself
+            // would not: such sums, and no others, are formed again with exact
+            // weights.  Those go in times 2^-12, so that a group's sum of at
+            // most 128 terms of 15 |A| cannot pass fp32 where A does not.
+            bool odd = false;
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
+            for (int r = 0; r < RB; ++r)
 #pragma unroll
-            for (int m = 0; m < MB; ++m)
-                sum[r][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        WBuf wb;
-        ABuf ab;
-        for (int st = first; st < last; st += stride) {
-            if (st < K >> 7) {
-                load_a(ab, st);
-                load_w(wb, st);
-            } else {
-                load_tail(wb, ab, st);
+                for (int m = 0; m < MB; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        odd |= !finite(acc[r][m][e]);
+            if (__syncthreads_or(odd)) {
+                f32x4 sum[RB][MB];
+#pragma unroll
+                for (int r = 0; r < RB; ++r)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+                        sum[r][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                walk<true>(sum, at);
+#pragma unroll
+                for (int r = 0; r < RB; ++r)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!finite(acc[r][m][e]))
+                                acc[r][m][e] = sum[r][m][e] * 0x1p12f;
             }
-            consume<true>(wb, ab, sum);
         }
+    }
+
+    // Joins the KW waves of each band in LDS, in order, and hands
+    // f(m, n, v) the sums v[r] of activation row m and row n of each block r
+    // of band n / 16 (n in [0, 16 * NW)).  Every thread of the workgroup calls.
+    template <class F>
+    __device__ __forceinline__ void join(F &&f)
+    {
+        f32x4 *red = (f32x4 *)lds;
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
+        for (int mb = 0; mb < MB; ++mb) {
+            __syncthreads();
 #pragma unroll
-            for (int m = 0; m < MB; ++m)
+            for (int r = 0; r < RB; ++r)
+                red[((nw() * KW + kw()) * RB + r) * 64 + lane()] = acc[r][mb];
+            __syncthreads();
+            for (int i = threadIdx.x; i < 256 * NW; i += kThreads) {
+                const int n = i & 15, m = (i >> 4) & 15, band = i >> 8;
+                float v[RB];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (!finite(acc[r][m][e]))
-                        acc[r][m][e] = sum[r][m][e] * 0x1p12f;
+                for (int r = 0; r < RB; ++r) {
+                    const float *p = (const float *)(red + (band * KW * RB + r) * 64 +
+                                                     (m >> 2) * 16 + n) + (m & 3);
+                    v[r] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < KW; ++w)
+                        v[r] += p[w * RB * 256];
+                }
+                if (16 * mb + m < M)
+                    f(16 * mb + m, band * 16 + n, v);
+            }
+        }
     }
 };
-
-// Adds the waves' accumulators of one block of 16 rows m in LDS, in wave order,
-// and hands f(m, n, v) the sums v[r] of row m and row n of each weight block r.
-// red: waves * RB * 64 vectors.  Every wave of the workgroup calls it.
-template <int RB, class F>
-__device__ __forceinline__ void reduce_waves(const f32x4 (&acc)[RB], f32x4 *red, int waves, F &&f)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < RB; ++r)
-        red[(wave * RB + r) * 64 + lane] = acc[r];
-    __syncthreads();
-    if (threadIdx.x < 256) {
-        const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
-        float v[RB];
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            const float *p = (const float *)(red + r * 64 + (m >> 2) * 16 + n) + (m & 3);
-            v[r] = 0.0f;
-            for (int w = 0; w < waves; ++w)
-                v[r] += p[w * RB * 256];
-        }
-        f(m, n, v);
-    }
-}
 
 inline bool overlap(const void *p, uint64_t pn, const void *q, uint64_t qn)
 {

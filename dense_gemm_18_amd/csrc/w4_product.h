@@ -12,8 +12,7 @@ struct W4Args {
     uint16_t *D;
     int64_t lda, ldd;
     int M, N, K;
-    int tiles_n;
-    int64_t tiles;
+    uint32_t tiles_m, tiles_n;
 };
 
 // Launches of the product, one translation unit for each type.  Not exported
@@ -25,55 +24,48 @@ __attribute__((visibility("hidden"))) void gemm18_w4_bf16(const W4Args &a, int g
 
 namespace {
 
-// One workgroup: 16 * RB columns n and 16 * MB rows m of D, its eight waves
-// taking the 128-wide steps of K in turn (so that together they read whole
-// lines of a weight row) and their sums joined in LDS.
-template <bool BF, int GS, int RB, int MB>
-__global__ void __launch_bounds__(kW4Waves * 64) gemm_w4_kernel(W4Args p)
+// One workgroup: 16 * RB * NW columns n and 16 * MB rows m of D.
+template <bool BF, int GS, int RB, int MB, int NW>
+__global__ void __launch_bounds__(kW4Waves * 64, 2) gemm_w4_kernel(W4Args p)
 {
-    __shared__ f32x4 red[kW4Waves * RB * 64];
-    const int64_t tile = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
-    if (tile >= p.tiles)
+    extern __shared__ f32x4 lds[];
+    using Core = Skinny<BF, GS, RB, MB, kW4Waves / NW, NW, true>;
+    // a grid of 2^32 work-items or more has a second dimension
+    const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
+    const uint32_t tn = wg % p.tiles_n, tm = wg / p.tiles_n;
+    if (tm >= p.tiles_m)
         return;
-    const int64_t n0 = tile % p.tiles_n * (16 * RB), m0 = tile / p.tiles_n * (16 * MB);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-
-    Skinny<BF, GS, RB, MB> c;
-    c.init(p.K);
-    // rows past the end repeat the last one; their results are not stored
+    const int n0 = tn * Core::kRows, m0 = tm * (16 * MB);
+    Core c;
+    c.W = p.W;
+    c.row[0] = n0;
+    c.rows[0] = p.N - n0;
+    c.K = p.K;
+    c.M = min(16 * MB, p.M - m0);
+    c.begin((char *)lds, p.A + (int64_t)m0 * p.lda,
+            (uint32_t)((c.M - 1) * p.lda + p.K) * 2u);
+    c.run([&](int m) { return (uint32_t)(m * p.lda) * 2u; });
+    uint16_t *D = p.D + (int64_t)m0 * p.ldd + n0;
+    c.join([&](int m, int n, const float(&v)[RB]) {
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
-        c.bind(r, p.W, min(n0 + 16 * r + (lane & 15), (int64_t)p.N - 1));
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-        c.bind_act(m, p.A + min(m0 + 16 * m + (lane & 15), (int64_t)p.M - 1) * p.lda);
-    c.run(wave, (p.K + 127) >> 7, kW4Waves);
-
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-        f32x4 part[RB];
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-            part[r] = c.acc[r][mb];
-        reduce_waves<RB>(part, red, kW4Waves, [&](int m, int n, const float(&v)[RB]) {
-            const int64_t mm = m0 + 16 * mb + m;
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                const int64_t nn = n0 + 16 * r + n;
-                if (mm < p.M && nn < p.N)
-                    p.D[mm * p.ldd + nn] = from_float<BF>(v[r]);
-            }
-        });
-    }
+        for (int r = 0; r < RB; ++r) {
+            const int nn = (n >> 4) * (16 * RB) + 16 * r + (n & 15);
+            if (n0 + nn < p.N)
+                D[m * p.ldd + nn] = from_float<BF>(v[r]);
+        }
+    });
 }
 
-template <bool BF, int GS, int RB, int MB>
+template <bool BF, int GS, int RB, int MB, int NW>
 void launch_w4_tile(W4Args a, hipStream_t stream)
 {
-    a.tiles_n = (int)cdiv(a.N, 16 * RB);
-    a.tiles = a.tiles_n * cdiv(a.M, 16 * MB);
-    hipLaunchKernelGGL((gemm_w4_kernel<BF, GS, RB, MB>), tile_grid(a.tiles), dim3(kW4Waves * 64),
-                       0, stream, a);
+    using Core = Skinny<BF, GS, RB, MB, kW4Waves / NW, NW, true>;
+    a.tiles_n = (uint32_t)cdiv(a.N, Core::kRows);
+    a.tiles_m = (uint32_t)cdiv(a.M, 16 * MB);
+    const int rows = a.M < 16 * MB ? a.M : 16 * MB;
+    hipLaunchKernelGGL((gemm_w4_kernel<BF, GS, RB, MB, NW>),
+                       tile_grid((int64_t)a.tiles_n * a.tiles_m), dim3(kW4Waves * 64),
+                       Core::lds_bytes(rows, a.K), stream, a);
 }
 
 template <bool BF>
@@ -81,12 +73,16 @@ void launch_w4(const W4Args &a, int group, hipStream_t stream)
 {
     with_group(group, [&](auto gs) {
         constexpr int GS = decltype(gs)::value ? decltype(gs)::value : 128;
-        if (a.M <= 16)
-            launch_w4_tile<BF, GS, 1, 1>(a, stream);
+        if (a.M <= 16 && a.N >= 64 * kCUs)
+            launch_w4_tile<BF, GS, 4, 1, 1>(a, stream);
+        else if (a.M <= 16 && a.N >= 32 * kCUs)
+            launch_w4_tile<BF, GS, 2, 1, 1>(a, stream);
+        else if (a.M <= 16)
+            launch_w4_tile<BF, GS, 1, 1, 1>(a, stream);
         else if (a.M <= 32)
-            launch_w4_tile<BF, GS, 2, 2>(a, stream);
+            launch_w4_tile<BF, GS, 2, 2, 1>(a, stream);
         else
-            launch_w4_tile<BF, GS, 2, 4>(a, stream);
+            launch_w4_tile<BF, GS, 2, 4, 2>(a, stream);
     });
 }
 

@@ -71,8 +71,8 @@ int gemm_w4_dequantize(const void *Q, const void *S, const void *Z, void *W, int
 /*
  * The product above.  A: M x K, row m at A + m * lda elements (lda >= K);
  * D: M x N, row m at D + m * ldd (ldd >= N), the elements between N and ldd
- * stay as they are.  Sizes as gemm_nt_f16, lda and ldd up to 2^40; K == 0
- * sets D to +0.
+ * stay as they are.  Sizes as gemm_nt_f16, lda up to GEMM_W4_MAX_LDA, ldd up
+ * to 2^40; K == 0 sets D to +0.
  *
  * The sums are held in fp32 and rounded once.  A call with M up to
  * GEMM_W4_DIRECT_M rows, and any call without a workspace, unpacks the
@@ -97,6 +97,8 @@ int gemm_w4_dequantize(const void *Q, const void *S, const void *Z, void *W, int
 int gemm_nt_w4(const void *A, const void *Q, const void *S, const void *Z, void *D, int64_t M,
                int64_t N, int64_t K, int64_t lda, int64_t ldd, int group, int dtype,
                void *workspace, int64_t ws_bytes, hipStream_t stream);
+
+#define GEMM_W4_MAX_LDA 16777215
 
 /* Rows up to which gemm_nt_w4 never uses a workspace. */
 #define GEMM_W4_DIRECT_M 256

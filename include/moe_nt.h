@@ -25,6 +25,8 @@ extern "C" {
 
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_TOPK 16
+#define MOE_MAX_INNER 1048576
+#define MOE_MAX_LDX 16777215
 #define MOE_RENORMALIZE 1  /* flag: the chosen weights sum to 1 */
 
 /*
@@ -36,7 +38,8 @@ extern "C" {
  * pointers are NULL.  group 32, 64 or 128: they are packed weights of
  * experts * 2 * inner and experts * hidden rows as gemm_nt_w4.h lays out, with
  * their scales, and zeros or NULL.
- * experts in [1, MOE_MAX_EXPERTS]; hidden and inner in [1, GEMM_MAX_K].
+ * experts in [1, MOE_MAX_EXPERTS], hidden in [1, GEMM_MAX_K], inner in
+ * [1, MOE_MAX_INNER].
  */
 typedef struct moe_nt_weights {
     const void *router;
@@ -48,7 +51,8 @@ typedef struct moe_nt_weights {
 
 /*
  * Router: ids[t*topk + j] (int32) and weights[t*topk + j] (fp32) of the T
- * rows of X, row t at X + t * ldx elements (ldx >= hidden).  The logits are
+ * rows of X, row t at X + t * ldx elements (hidden <= ldx <=
+ * MOE_MAX_LDX).  The logits are
  * summed in fp32.  A row with a NaN logit, or whose largest is infinite, gets
  * NaN weights and topk distinct valid ids.  topk in [1, min(experts, MOE_MAX_TOPK)].
  * Only router, experts, hidden and dtype of *w are used.
