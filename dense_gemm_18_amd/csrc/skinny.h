@@ -124,7 +124,7 @@ __device__ __forceinline__ u32x4 load_b128(__amdgpu_buffer_rsrc_t rs, uint32_t o
 }
 
 // LDS of a product: activations, then scales, up to these sizes.
-constexpr int kActBytes = 64 * 1024;
+constexpr int kActBytes = 66 * 1024;
 constexpr int kScaleBytes = 32 * 1024;
 
 // One workgroup's product.  GS: 0 for 16-bit weights, else the group.
@@ -223,19 +223,21 @@ struct Skinny {
         }
     }
 
+    template <int N>
     struct Batch {
-        u32x4 v[U][RB][GS ? 1 : 4];
+        u32x4 v[N][RB][GS ? 1 : 4];
     };
 
-    // U steps from st on; nothing where a step is `end` or later.  Unconditional
+    // N steps from st on; nothing where a step is `end` or later.  Unconditional
     // loads with an offset past the range there: a branch around loads would
     // leave the compiler waiting for all of them.
-    __device__ __forceinline__ void load(Batch &b, int st, int end) const
+    template <int N>
+    __device__ __forceinline__ void load(Batch<N> &b, int st, int end) const
     {
 #pragma unroll
         for (int r = 0; r < RB; ++r)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < N; ++u) {
                 const uint32_t o =
                     woff[r] + (st + u < end ? (uint32_t)(st + u) * (GS ? 64u : 256u) : kOob);
 #pragma unroll
@@ -331,9 +333,11 @@ struct Skinny {
         return v;
     }
 
-    // Step u of a batch, step `st` of the chunk that starts at k0.
-    template <bool EXACT>
-    __device__ __forceinline__ void consume(Batch &b, int u, int st, int k0,
+    // Step u of a batch, step `st` of the chunk that starts at k0 and whose
+    // activations and scales are at `acts` and `scales`.
+    template <bool EXACT, int N>
+    __device__ __forceinline__ void consume(Batch<N> &b, int u, int st, int k0,
+                                            const char *acts, const uint32_t *scales,
                                             f32x4 (&to)[RB][MB]) const
     {
         const int c = lane() >> 4;
@@ -341,7 +345,7 @@ struct Skinny {
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             // rows past the last repeat it; their results are not used
-            const char *p = lds + min(16 * m + (lane() & 15), M - 1) * astride + st * 256 + c * 16;
+            const char *p = acts + min(16 * m + (lane() & 15), M - 1) * astride + st * 256 + c * 16;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 a[m][j] = *(const x8 *)(p + 64 * j);
@@ -368,9 +372,8 @@ struct Skinny {
                                               to[r][m]);
         } else {
             constexpr int per = 4 / kGroups;       // matrix instructions per group
-            const uint32_t *sp = (const uint32_t *)(lds + act_bytes(M, chunk)) +
-                                 ((JOINED ? nw() * RB * 16 : 0) + (lane() & 15)) * sstride +
-                                 st * kGroups;
+            const uint32_t *sp =
+                scales + ((JOINED ? nw() * RB * 16 : 0) + (lane() & 15)) * sstride + st * kGroups;
 #pragma unroll
             for (int k = 0; k < kGroups; ++k) {
                 f32x4 asum[MB];
@@ -424,7 +427,7 @@ struct Skinny {
             const int steps = min(per, total - s0);
             int st = kw() * steps / KW;
             const int end = (kw() + 1) * steps / KW;
-            Batch b;
+            Batch<U> b;
             load(b, s0 + st, s0 + end);
             if (s0 > 0 || EXACT)
                 __syncthreads();          // the chunk before has been read
@@ -437,7 +440,8 @@ struct Skinny {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (st + u < end)
-                        consume<EXACT>(b, u, st + u, s0 * 128, to);
+                        consume<EXACT>(b, u, st + u, s0 * 128, lds,
+                                       (const uint32_t *)(lds + act_bytes(M, chunk)), to);
                 st += U;
                 if (st < end)
                     load(b, s0 + st, s0 + end);
@@ -455,7 +459,15 @@ struct Skinny {
     template <class F>
     __device__ __forceinline__ void run(F &&at)
     {
-        walk<false>(acc, at);
+        finish([&](auto exact, f32x4 (&to)[RB][MB])
+                   G18_INLINE { walk<decltype(exact)::value>(to, at); });
+    }
+
+    // walk(false_type, acc), and what infinities need after it.
+    template <class W>
+    __device__ __forceinline__ void finish(W &&walk)
+    {
+        walk(std::false_type{}, acc);
         if constexpr (BF && GS != 0) {
             // An activation that is infinite, or so large that 128 times it
             // overflows, leaves infinity minus infinity where q - z itself
@@ -477,7 +489,7 @@ struct Skinny {
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
                         sum[r][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                walk<true>(sum, at);
+                walk(std::true_type{}, sum);
 #pragma unroll
                 for (int r = 0; r < RB; ++r)
 #pragma unroll
@@ -520,6 +532,127 @@ struct Skinny {
                     f(16 * mb + m, band * 16 + n, v);
             }
         }
+    }
+};
+
+// The same product where the activations do not fit the LDS: chunks of CS steps
+// of K in two LDS buffers.  While one is consumed, the next one's activations
+// and scales travel to registers and its weights to theirs; then they are
+// written to the other buffer, and one barrier ends the chunk.  Rows of packed
+// weights that follow each other.
+template <bool BF, int GS, int RB, int MB, int KW, int NW, int CS>
+struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
+    using Base = Skinny<BF, GS, RB, MB, KW, NW, true>;
+    using Base::kGroups;
+    using Base::kRows;
+    using Base::kThreads;
+    static constexpr int kSteps = CS / KW;                   // of a wave, in a chunk
+    static constexpr int kStride = CS * 256 + 16;            // of activation rows in LDS
+    static constexpr int kScales = CS * kGroups + 1;         // of scale rows, words
+    static constexpr int kActs = 16 * MB * kStride;
+    static constexpr int kBuffer = kActs + kRows * kScales * 4;
+    static constexpr int NA = 16 * MB * CS * 16 / kThreads;  // 16-byte pieces of a thread
+    static constexpr int NS = (kRows * CS * kGroups + kThreads - 1) / kThreads;
+    static_assert(CS % KW == 0 && 16 * MB * CS * 16 % kThreads == 0, "whole pieces");
+    static constexpr int kLds = 2 * kBuffer > KW * NW * RB * 1024 ? 2 * kBuffer
+                                                                  : KW * NW * RB * 1024;
+
+    struct Next {
+        u32x4 a[NA];
+        uint32_t s[NS], z[NS];
+    };
+
+    // What the thread stages of the chunk from k0 on (nothing from K on).
+    template <class F>
+    __device__ __forceinline__ void fetch(Next &x, int k0, F &&at) const
+    {
+        const int K = this->K, G = this->G;
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int idx = i * kThreads + threadIdx.x, m = idx / (CS * 16);
+            const int k = k0 + idx % (CS * 16) * 8;
+            x.a[i] = load_b128(this->ar,
+                               m < this->M && k + 8 <= K ? at(m) + 2u * (uint32_t)k : kOob);
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int idx = i * kThreads + threadIdx.x, n = idx / (CS * kGroups);
+            const int g = k0 / GS + idx % (CS * kGroups);
+            const uint32_t o = g < G && n < kRows ? (uint32_t)(n * G + g) : kOob;
+            x.s[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(this->sr[0],
+                                                                    2 * o + (o & kOob), 0, 0);
+            x.z[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(this->zr[0], o, 0, 0);
+        }
+    }
+
+    template <class F>
+    __device__ __forceinline__ void store(const Next &x, int k0, char *buf, F &&at) const
+    {
+        const int K = this->K;
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int idx = i * kThreads + threadIdx.x;
+            const int m = idx / (CS * 16), c = idx % (CS * 16), k = k0 + c * 8;
+            // the 8 elements that K ends among come below
+            if (k + 8 <= K || k >= K)
+                *(u32x4 *)(buf + m * kStride + c * 16) = x.a[i];
+        }
+        uint32_t *scales = (uint32_t *)(buf + kActs);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int idx = i * kThreads + threadIdx.x;
+            const int n = idx / (CS * kGroups), g = idx % (CS * kGroups);
+            if (n < kRows)
+                scales[n * kScales + g] =
+                    x.s[i] | ((BF ? 0x4300u : 0x6400u) + ((x.z[i] | this->zdef) & 15u)) << 16;
+        }
+        if ((K & 7) && k0 <= K && k0 + CS * 128 > K) {
+            const int k = (K & ~7) + (threadIdx.x & 7);
+            for (int m = threadIdx.x >> 3; m < 16 * MB; m += kThreads / 8)
+                *(uint16_t *)(buf + m * kStride + (k - k0) * 2) =
+                    (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                        this->ar, m < this->M && k < K ? at(m) + 2u * k : kOob, 0, 0);
+        }
+    }
+
+    template <bool EXACT, class F>
+    __device__ __forceinline__ void walk(f32x4 (&to)[RB][MB], F &&at)
+    {
+        const int total = (this->K + 127) >> 7, mine = this->kw() * kSteps;
+        typename Base::template Batch<kSteps> now, ahead;
+        Next x;
+        if (EXACT)
+            __syncthreads();
+        fetch(x, 0, at);
+        this->load(now, mine, total);
+        store(x, 0, this->lds, at);
+        __syncthreads();
+        char *buf = this->lds, *other = this->lds + kBuffer;
+#pragma nounroll
+        for (int s0 = 0; s0 < total; s0 += CS) {
+            fetch(x, (s0 + CS) * 128, at);
+            this->load(ahead, s0 + CS + mine, total);
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u)
+                if (s0 + mine + u < total)
+                    this->template consume<EXACT>(now, u, mine + u, s0 * 128, buf,
+                                                  (const uint32_t *)(buf + kActs), to);
+            store(x, (s0 + CS) * 128, other, at);
+            __syncthreads();
+            char *t = buf;
+            buf = other;
+            other = t;
+            now = ahead;
+        }
+    }
+
+    template <class F>
+    __device__ __forceinline__ void run(F &&at)
+    {
+        this->astride = kStride;
+        this->sstride = kScales;
+        this->finish([&](auto exact, f32x4 (&to)[RB][MB])
+                         G18_INLINE { walk<decltype(exact)::value>(to, at); });
     }
 };
 

@@ -24,12 +24,12 @@ __attribute__((visibility("hidden"))) void gemm18_w4_bf16(const W4Args &a, int g
 
 namespace {
 
-// One workgroup: 16 * RB * NW columns n and 16 * MB rows m of D.
-template <bool BF, int GS, int RB, int MB, int NW>
-__global__ void __launch_bounds__(kW4Waves * 64, 2) gemm_w4_kernel(W4Args p)
+// One workgroup's tile of D, 16 * MB rows and as many columns as Core has
+// weight rows.
+template <bool BF, int MB, class Core>
+__global__ void __launch_bounds__(Core::kThreads, 2) gemm_w4_kernel(W4Args p)
 {
     extern __shared__ f32x4 lds[];
-    using Core = Skinny<BF, GS, RB, MB, kW4Waves / NW, NW, true>;
     // a grid of 2^32 work-items or more has a second dimension
     const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
     const uint32_t tn = wg % p.tiles_n, tm = wg / p.tiles_n;
@@ -46,7 +46,8 @@ __global__ void __launch_bounds__(kW4Waves * 64, 2) gemm_w4_kernel(W4Args p)
             (uint32_t)((c.M - 1) * p.lda + p.K) * 2u);
     c.run([&](int m) { return (uint32_t)(m * p.lda) * 2u; });
     uint16_t *D = p.D + (int64_t)m0 * p.ldd + n0;
-    c.join([&](int m, int n, const float(&v)[RB]) {
+    c.join([&](int m, int n, const auto &v) {
+        constexpr int RB = sizeof(v) / sizeof(v[0]);
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
             const int nn = (n >> 4) * (16 * RB) + 16 * r + (n & 15);
@@ -56,16 +57,29 @@ __global__ void __launch_bounds__(kW4Waves * 64, 2) gemm_w4_kernel(W4Args p)
     });
 }
 
-template <bool BF, int GS, int RB, int MB, int NW>
-void launch_w4_tile(W4Args a, hipStream_t stream)
+template <bool BF, int MB, class Core>
+void launch_w4_tile(W4Args a, int lds, hipStream_t stream)
 {
-    using Core = Skinny<BF, GS, RB, MB, kW4Waves / NW, NW, true>;
     a.tiles_n = (uint32_t)cdiv(a.N, Core::kRows);
     a.tiles_m = (uint32_t)cdiv(a.M, 16 * MB);
-    const int rows = a.M < 16 * MB ? a.M : 16 * MB;
-    hipLaunchKernelGGL((gemm_w4_kernel<BF, GS, RB, MB, NW>),
-                       tile_grid((int64_t)a.tiles_n * a.tiles_m), dim3(kW4Waves * 64),
-                       Core::lds_bytes(rows, a.K), stream, a);
+    hipLaunchKernelGGL((gemm_w4_kernel<BF, MB, Core>),
+                       tile_grid((int64_t)a.tiles_n * a.tiles_m), dim3(Core::kThreads), lds,
+                       stream, a);
+}
+
+// Activations that LDS holds whole: every wave walks its eighth of K freely.
+template <bool BF, int GS, int RB>
+void launch_w4_resident(const W4Args &a, hipStream_t stream)
+{
+    using Core = Skinny<BF, GS, RB, 1, kW4Waves, 1, true>;
+    launch_w4_tile<BF, 1, Core>(a, Core::lds_bytes(a.M, a.K), stream);
+}
+
+template <bool BF, int GS, int RB, int MB, int KW, int CS>
+void launch_w4_piped(const W4Args &a, hipStream_t stream)
+{
+    using Core = Piped<BF, GS, RB, MB, KW, kW4Waves / KW, CS>;
+    launch_w4_tile<BF, MB, Core>(a, Core::kLds, stream);
 }
 
 template <bool BF>
@@ -73,16 +87,20 @@ void launch_w4(const W4Args &a, int group, hipStream_t stream)
 {
     with_group(group, [&](auto gs) {
         constexpr int GS = decltype(gs)::value ? decltype(gs)::value : 128;
-        if (a.M <= 16 && a.N >= 64 * kCUs)
-            launch_w4_tile<BF, GS, 4, 1, 1>(a, stream);
-        else if (a.M <= 16 && a.N >= 32 * kCUs)
-            launch_w4_tile<BF, GS, 2, 1, 1>(a, stream);
-        else if (a.M <= 16)
-            launch_w4_tile<BF, GS, 1, 1, 1>(a, stream);
-        else if (a.M <= 32)
-            launch_w4_tile<BF, GS, 2, 2, 1>(a, stream);
-        else
-            launch_w4_tile<BF, GS, 2, 4, 2>(a, stream);
+        if (a.M <= 16 && (int64_t)a.M * (cdiv(a.K, 128) * 256 + 16) <= kActBytes) {
+            if (a.N >= 64 * kCUs)
+                launch_w4_resident<BF, GS, 4>(a, stream);
+            else if (a.N >= 32 * kCUs)
+                launch_w4_resident<BF, GS, 2>(a, stream);
+            else
+                launch_w4_resident<BF, GS, 1>(a, stream);
+        } else if (a.M <= 16) {
+            launch_w4_piped<BF, GS, 2, 1, 8, 8>(a, stream);
+        } else if (a.M <= 32) {
+            launch_w4_piped<BF, GS, 2, 2, 4, 4>(a, stream);
+        } else {
+            launch_w4_piped<BF, GS, 2, 4, 4, 4>(a, stream);
+        }
     });
 }
 
