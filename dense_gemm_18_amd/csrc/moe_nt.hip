@@ -5,7 +5,6 @@
 namespace {
 
 constexpr int64_t kMaxLd = int64_t(1) << 40;
-constexpr int64_t kHeader = 256;
 
 bool sizes_ok_moe(const moe_nt_weights *w, int64_t T, int topk)
 {
@@ -19,10 +18,25 @@ bool inner_ok(const moe_nt_weights *w)
     return w->inner >= 1 && w->inner <= MOE_MAX_INNER && (w->group == 0 || group_ok(w->group));
 }
 
-// Workspace: header, logits of a chunk, gated rows of a chunk, their products.
-int64_t logits_bytes(int64_t T, int64_t E) { return cdiv(T * E * 4, 256) * 256; }
+// Workspace: tickets (kept at zero between calls), the plan, and a chunk's
+// logits, gated rows and their products.
+struct Layout {
+    int64_t plan, logits, h, y, bytes;
+};
 
-int64_t h_bytes(int64_t slots, int64_t I) { return cdiv(slots * I * 2, 256) * 256; }
+Layout layout_of(int64_t T, const moe_nt_weights *w, int topk)
+{
+    auto up = [](int64_t n) { return cdiv(n, 256) * 256; };
+    const int64_t chunk = moe_chunk(T, topk), slots = chunk * topk;
+    Layout l;
+    // a ticket for each 16 hidden rows is more than any block size needs
+    l.plan = up(4 * (1 + cdiv(w->hidden, 16)));
+    l.logits = l.plan + up(sizeof(Plan));
+    l.h = l.logits + up(chunk * w->experts * 4);
+    l.y = l.h + up(slots * w->inner * 2);
+    l.bytes = l.y + up(slots * w->hidden * 4);
+    return l;
+}
 
 struct Span {
     const void *p;
@@ -86,16 +100,15 @@ int check_common(const moe_nt_weights *w, const void *X, int64_t T, int64_t ldx,
 int check_route(const moe_nt_weights *w, const void *X, const int32_t *ids, const float *weights,
                 int64_t T, int64_t ldx, int topk, int flags, const void *ws, int64_t ws_bytes)
 {
-    if (!sizes_ok_moe(w, T, topk) || topk > w->experts || (flags & ~MOE_RENORMALIZE))
+    if (!sizes_ok_moe(w, T, topk) || !inner_ok(w) || topk > w->experts || (flags & ~MOE_RENORMALIZE))
         return GEMM_EINVAL;
     if (T == 0)
         return GEMM_OK;
     if (!w->router || !aligned_to(w->router, 2) || !ids || !weights || !aligned_to(ids, 4) ||
         !aligned_to(weights, 4))
         return GEMM_EINVAL;
-    const int64_t chunk = moe_chunk(T, topk);
-    const int rc = check_common(w, X, T, ldx, topk, ws, ws_bytes,
-                                kHeader + logits_bytes(chunk, w->experts));
+    const int rc =
+        check_common(w, X, T, ldx, topk, ws, ws_bytes, layout_of(T, w, topk).bytes);
     if (rc != GEMM_OK)
         return rc;
     const uint64_t slots = (uint64_t)T * (uint64_t)topk * 4u;
@@ -145,12 +158,19 @@ int check_experts(const moe_nt_weights *w, const void *X, const int32_t *ids, co
 }
 
 MoeArgs common_args(const moe_nt_weights *w, const void *X, const int32_t *ids,
-                    const float *weights, int64_t ldx, int topk, void *ws)
+                    const float *weights, int64_t T, int64_t ldx, int topk, void *ws)
 {
+    const Layout l = layout_of(T, w, topk);
     MoeArgs p{};
+    p.tickets = (uint32_t *)ws;
+    p.plan = (Plan *)((char *)ws + l.plan);
+    p.h = (uint16_t *)((char *)ws + l.h);
+    p.y = (float *)((char *)ws + l.y);
+    p.w13 = weight_ref(w->w13, w->w13_scales, w->w13_zeros, w->group);
+    p.w2 = weight_ref(w->w2, w->w2_scales, w->w2_zeros, w->group);
     p.X = (const uint16_t *)X;
     p.router = (const uint16_t *)w->router;
-    p.logits = (float *)((char *)ws + kHeader);
+    p.logits = (float *)((char *)ws + l.logits);
     p.ids = (int32_t *)ids;
     p.weights = (float *)weights;
     p.ldx = ldx;
@@ -166,7 +186,8 @@ bool next_chunk(MoeArgs &p, int64_t T, int64_t &done)
 {
     if (p.T) {
         p.X += p.T * p.ldx;
-        p.D += p.T * p.ldd;
+        if (p.D)
+            p.D += p.T * p.ldd;
         p.ids += (int64_t)p.T * p.topk;
         p.weights += (int64_t)p.T * p.topk;
         done += p.T;
@@ -180,30 +201,19 @@ MoeLaunch launches(const moe_nt_weights *w)
     return w->dtype == GEMM_T_BF16 ? gemm18_moe_bf16() : gemm18_moe_f16();
 }
 
-int run_route(const moe_nt_weights *w, MoeArgs p, int64_t T, int flags, hipStream_t stream)
+// The router, the experts or both, a chunk of tokens at a time.
+int run(const moe_nt_weights *w, MoeArgs p, int64_t T, bool route, bool experts,
+        hipStream_t stream)
 {
-    p.renorm = flags & MOE_RENORMALIZE;
-    p.D = nullptr;
-    p.ldd = 0;
+    if (!experts)
+        p.plan = nullptr;
     const MoeLaunch go = launches(w);
-    for (int64_t done = 0; next_chunk(p, T, done);)
-        go.route(p, stream);
-    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ELAUNCH;
-}
-
-int run_experts(const moe_nt_weights *w, MoeArgs p, void *D, int64_t T, int64_t ldd, void *ws,
-                hipStream_t stream)
-{
-    const int64_t chunk = moe_chunk(T, p.topk);
-    p.w13 = weight_ref(w->w13, w->w13_scales, w->w13_zeros, w->group);
-    p.w2 = weight_ref(w->w2, w->w2_scales, w->w2_zeros, w->group);
-    p.h = (uint16_t *)((char *)ws + kHeader + logits_bytes(chunk, w->experts));
-    p.y = (float *)((char *)p.h + h_bytes(chunk * p.topk, w->inner));
-    p.D = (uint16_t *)D;
-    p.ldd = ldd;
-    const MoeLaunch go = launches(w);
-    for (int64_t done = 0; next_chunk(p, T, done);)
-        go.experts(p, w->group, stream);
+    for (int64_t done = 0; next_chunk(p, T, done);) {
+        if (route)
+            go.route(p, stream);
+        if (experts)
+            go.experts(p, w->group, route, stream);
+    }
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ELAUNCH;
 }
 
@@ -215,10 +225,7 @@ int64_t moe_nt_ws_size(int64_t T, const moe_nt_weights *w, int topk)
 {
     if (!sizes_ok_moe(w, T, topk) || !inner_ok(w) || T == 0)
         return 0;
-    const int64_t chunk = moe_chunk(T, topk);
-    return kHeader + logits_bytes(chunk, w->experts) +
-           h_bytes((int64_t)chunk * topk, w->inner) +
-           cdiv(chunk * topk * w->hidden * 4, 256) * 256;
+    return layout_of(T, w, topk).bytes;
 }
 
 int moe_nt_route(const moe_nt_weights *w, const void *X, int32_t *ids, float *weights, int64_t T,
@@ -228,7 +235,9 @@ int moe_nt_route(const moe_nt_weights *w, const void *X, int32_t *ids, float *we
     const int rc = check_route(w, X, ids, weights, T, ldx, topk, flags, workspace, ws_bytes);
     if (rc != GEMM_OK || T == 0)
         return rc;
-    return run_route(w, common_args(w, X, ids, weights, ldx, topk, workspace), T, flags, stream);
+    MoeArgs p = common_args(w, X, ids, weights, T, ldx, topk, workspace);
+    p.renorm = flags & MOE_RENORMALIZE;
+    return run(w, p, T, true, false, stream);
 }
 
 int moe_nt_experts(const moe_nt_weights *w, const void *X, const int32_t *ids,
@@ -239,8 +248,10 @@ int moe_nt_experts(const moe_nt_weights *w, const void *X, const int32_t *ids,
         check_experts(w, X, ids, weights, D, T, ldx, ldd, topk, workspace, ws_bytes);
     if (rc != GEMM_OK || T == 0)
         return rc;
-    return run_experts(w, common_args(w, X, ids, weights, ldx, topk, workspace), D, T, ldd,
-                       workspace, stream);
+    MoeArgs p = common_args(w, X, ids, weights, T, ldx, topk, workspace);
+    p.D = (uint16_t *)D;
+    p.ldd = ldd;
+    return run(w, p, T, false, true, stream);
 }
 
 int moe_nt_layer(const moe_nt_weights *w, const void *X, void *D, int32_t *ids, float *weights,
@@ -252,9 +263,11 @@ int moe_nt_layer(const moe_nt_weights *w, const void *X, void *D, int32_t *ids, 
         rc = check_experts(w, X, ids, weights, D, T, ldx, ldd, topk, workspace, ws_bytes);
     if (rc != GEMM_OK || T == 0)
         return rc;
-    const MoeArgs p = common_args(w, X, ids, weights, ldx, topk, workspace);
-    rc = run_route(w, p, T, flags, stream);
-    return rc != GEMM_OK ? rc : run_experts(w, p, D, T, ldd, workspace, stream);
+    MoeArgs p = common_args(w, X, ids, weights, T, ldx, topk, workspace);
+    p.renorm = flags & MOE_RENORMALIZE;
+    p.D = (uint16_t *)D;
+    p.ldd = ldd;
+    return run(w, p, T, true, true, stream);
 }
 
 } // extern "C"

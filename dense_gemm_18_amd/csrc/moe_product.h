@@ -13,6 +13,17 @@ inline int moe_chunk(int64_t T, int topk)
     return T < most ? (int)T : most;
 }
 
+// Which slots (t * topk + j) go to which expert: the experts that have any, in
+// rising order, and each one's slots side by side.  In the workspace, for the
+// launches that follow.  The order of an expert's slots is that of the LDS
+// atomics and changes no result: a slot is a row of its own in every product.
+struct Plan {
+    int active;
+    int act[kMoeSlots];          // active experts
+    int off[kMoeSlots + 1];      // where their slots start
+    int slot[kMoeSlots];
+};
+
 struct MoeArgs {
     const uint16_t *X;             // T rows, ldx apart
     const uint16_t *router;        // E x H
@@ -22,6 +33,8 @@ struct MoeArgs {
     WeightRef w13, w2;             // E * 2 * I rows of H, E * H rows of I
     uint16_t *h;                   // T * topk rows of I
     float *y;                      // T * topk rows of H
+    Plan *plan;                    // null: the router leaves none
+    uint32_t *tickets;             // the router's, then one for each block of the down product
     uint16_t *D;                   // T rows, ldd apart
     int64_t ldx, ldd;
     int T, E, H, I, topk, renorm;
@@ -30,23 +43,199 @@ struct MoeArgs {
 // One translation unit for each type.  Not exported from the library.
 struct MoeLaunch {
     void (*route)(const MoeArgs &, hipStream_t);
-    void (*experts)(const MoeArgs &, int group, hipStream_t);
+    void (*experts)(const MoeArgs &, int group, bool planned, hipStream_t);
 };
 __attribute__((visibility("hidden"))) MoeLaunch gemm18_moe_f16();
 __attribute__((visibility("hidden"))) MoeLaunch gemm18_moe_bf16();
 
 namespace {
 
+// Words that several workgroups of one launch share (logits, products of the
+// slots, tickets) move with agent-scope relaxed atomics, which on gfx950 are
+// loads and stores that every XCD's L2 passes on; no fence, which would write
+// back or drop a whole L2.
+template <class T>
+__device__ __forceinline__ void put(T *p, T v)
+{
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T get(const T *p)
+{
+    return __hip_atomic_load(const_cast<T *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// True in the last of `count` workgroups to come here: what every one of them
+// has put() before is then visible.  The counter goes back to 0 for the next
+// launch.  Every thread of the workgroup calls it; `flag` is a word of LDS.
+__device__ __forceinline__ bool last_of(uint32_t *counter, uint32_t count, uint32_t *flag)
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);       // this wave's stores have reached memory
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t before =
+            __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *flag = before + 1 == count;
+        if (before + 1 == count)
+            put(counter, 0u);
+    }
+    __syncthreads();
+    const bool last = *flag;
+    asm volatile("" ::: "memory");
+    return last;
+}
+
+// ---- plan ---------------------------------------------------------------
+
+// By one workgroup.  cnt: MOE_MAX_EXPERTS ints of LDS.  ids(i): slot i's id.
+template <class F>
+__device__ __forceinline__ void make_plan(Plan *plan, int n, int E, int *cnt, F &&ids)
+{
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
+        cnt[e] = 0;
+    __syncthreads();
+    int id = -1;
+    if (threadIdx.x < n) {               // n <= kMoeSlots <= blockDim.x
+        id = ids(threadIdx.x);
+        id = (uint32_t)id < (uint32_t)E ? id : -1;
+        if (id >= 0)
+            atomicAdd(&cnt[id], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x;
+        int at = 0, base = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const int c = e0 + lane < E ? cnt[e0 + lane] : 0;
+            int sum = c;                               // inclusive prefix sum
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int up = __shfl_up(sum, d);
+                sum += lane >= d ? up : 0;
+            }
+            const uint64_t has = __ballot(c > 0);
+            if (c > 0) {
+                const int k = at + __popcll(has & ((1ull << lane) - 1));
+                plan->act[k] = e0 + lane;
+                plan->off[k] = base + sum - c;
+                cnt[e0 + lane] = base + sum - c;
+            }
+            at += __popcll(has);
+            base += __shfl(sum, 63);
+        }
+        if (lane == 0) {
+            plan->off[at] = base;
+            plan->active = at;
+        }
+    }
+    __syncthreads();
+    if (id >= 0)
+        plan->slot[atomicAdd(&cnt[id], 1)] = threadIdx.x;
+}
+
+template <int = 0>
+__global__ void __launch_bounds__(kMoeSlots) moe_plan_kernel(MoeArgs p)
+{
+    __shared__ int cnt[MOE_MAX_EXPERTS];
+    make_plan(p.plan, p.T * p.topk, p.E, cnt, [&](int i) { return p.ids[i]; });
+}
+
 // ---- router -------------------------------------------------------------
 
 constexpr int kRouteWaves = 16;
 
-// Logits of 16 experts for 16 tokens; sixteen waves split the hidden size.
+// Order of logits as unsigned numbers: rising with the value, both zeros
+// alike, every NaN below everything.
+__device__ __forceinline__ uint32_t order_of(float v)
+{
+    if (!(v == v))
+        return 0;
+    const uint32_t u = __builtin_bit_cast(uint32_t, v + 0.0f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Reductions over the wave by data-parallel moves (in order, no LDS): the
+// result in every lane.
+template <class F>
+__device__ __forceinline__ float reduce_wave(float v, float none, F &&f)
+{
+    auto step = [&](auto ctrl, auto rows) G18_INLINE {
+        const int moved = __builtin_amdgcn_update_dpp(
+            __builtin_bit_cast(int, none), __builtin_bit_cast(int, v), decltype(ctrl)::value,
+            decltype(rows)::value, 0xf, false);
+        v = f(v, __builtin_bit_cast(float, moved));
+    };
+    step(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xf>{});  // 1 up
+    step(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xf>{});  // 2 up
+    step(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xf>{});  // 4 up
+    step(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xf>{});  // 8 up
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});  // lane 15 on
+    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // lane 31 on
+    return __builtin_bit_cast(float,
+                              __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// The topk largest of a token's logits and their softmax weights, by one wave
+// with PER logits v per lane (E <= 64 * PER).  An expert's place is the number of those
+// that come before it, larger ones and equal ones of lower index: E * PER
+// comparisons per lane whatever topk is, and no exchange that waits for the
+// one before (topk maxima over the wave took 1 us each for 4).
+template <int PER>
+__device__ __forceinline__ void choose(const float (&v)[PER], int E, int topk, bool renorm,
+                                       int32_t *ids, float *weights, int *lds_ids)
+{
+    const int lane = threadIdx.x & 63;
+    uint32_t key[PER];
+    int place[PER];
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        key[i] = order_of(v[i]);
+        place[i] = lane + 64 * i < E ? 0 : INT32_MAX / 2;
+        top = __builtin_fmaxf(top, v[i]);      // a NaN shows in the sum below
+    }
+    top = reduce_wave(top, -__builtin_inff(),
+                      [](float a, float b) { return __builtin_fmaxf(a, b); });
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int most = min(64, E - 64 * k);
+        for (int o = 0; o < most; ++o) {
+            const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key[k], o);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const bool lower = i > k || (i == k && lane > o);
+                place[i] += other > key[i] || (other == key[i] && lower);
+            }
+        }
+    }
+    float sum = 0.0f, chosen = 0.0f, p[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        p[i] = lane + 64 * i < E ? expf(v[i] - top) : 0.0f;
+        sum += p[i];
+        chosen += place[i] < topk ? p[i] : 0.0f;
+    }
+    auto add = [](float a, float b) { return a + b; };
+    sum = reduce_wave(sum, 0.0f, add);
+    chosen = reduce_wave(chosen, 0.0f, add);
+    const float over = renorm && sum == sum ? chosen : sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (place[i] < topk) {
+            ids[place[i]] = lane + 64 * i;
+            lds_ids[place[i]] = lane + 64 * i;
+            weights[place[i]] = p[i] / over;
+        }
+}
+
+// Logits of 16 experts for 16 tokens, sixteen waves splitting the hidden
+// size; the last workgroup then chooses for every token and makes the plan.
 template <bool BF>
 using RouteCore = Skinny<BF, 0, 1, 1, kRouteWaves, 1, true>;
 
-template <bool BF>
-__global__ void __launch_bounds__(kRouteWaves * 64) moe_logits_kernel(MoeArgs p)
+template <bool BF, int PER>
+__global__ void __launch_bounds__(kRouteWaves * 64) moe_route_kernel(MoeArgs p)
 {
     extern __shared__ f32x4 lds[];
     const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
@@ -60,321 +249,187 @@ __global__ void __launch_bounds__(kRouteWaves * 64) moe_logits_kernel(MoeArgs p)
     c.run([&](int m) { return (uint32_t)(m * p.ldx) * 2u; });
     c.join([&](int m, int n, const float(&v)[1]) {
         if (e0 + n < p.E)
-            p.logits[(t0 + m) * p.E + e0 + n] = v[0];
+            put(p.logits + (t0 + m) * p.E + e0 + n, v[0]);
     });
-}
-
-// Order of logits as unsigned numbers: rising with the value, both zeros
-// alike, every NaN below everything.
-__device__ __forceinline__ uint32_t order_of(float v)
-{
-    if (!(v == v))
-        return 0;
-    const uint32_t u = __builtin_bit_cast(uint32_t, v + 0.0f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-// The topk largest of E logits and their softmax weights, one wave per token.
-// PER logits per lane (E <= 64 * PER).  A key is the order of the logit above
-// the complement of its index, so keys differ, equal logits fall by rising
-// index, and 0 marks what is taken: topk maxima over the wave.
-template <int PER>
-__device__ __forceinline__ void choose(const float *logits, int E, int topk, bool renorm,
-                                       int32_t *ids, float *weights)
-{
-    const int lane = threadIdx.x & 63;
-    float v[PER];
-    uint64_t key[PER];
-    float top = -__builtin_inff();
+    __syncthreads();
+    int *cnt = (int *)lds, *ids = cnt + MOE_MAX_EXPERTS;
+    if (!last_of(p.tickets, gridDim.x * gridDim.y, (uint32_t *)ids))
+        return;
+    __syncthreads();
+    // a wave's tokens, at most four, all their logits under way at once
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    constexpr int kTokens = 64 / kRouteWaves;
+    float v[kTokens][PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        v[i] = e < E ? logits[e] : -__builtin_inff();
-        key[i] = e < E ? (uint64_t)order_of(v[i]) << 32 | (0xffffffffu - (uint32_t)e) : 0;
-        top = __builtin_fmaxf(top, v[i]);      // a NaN shows in the sum below
-    }
+    for (int k = 0; k < kTokens; ++k)
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        top = __builtin_fmaxf(top, __shfl_xor(top, d));
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        sum += lane + 64 * i < E ? expf(v[i] - top) : 0.0f;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        sum += __shfl_xor(sum, d);
-
-    float mine = 0.0f, chosen = 0.0f;
-    int id = 0;
-    for (int j = 0; j < topk; ++j) {
-        uint64_t best = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            best = key[i] > best ? key[i] : best;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const uint64_t other = __shfl_xor((unsigned long long)best, d);
-            best = other > best ? other : best;
+        for (int i = 0; i < PER; ++i) {
+            const int t = wave + k * kRouteWaves, e = lane + 64 * i;
+            v[k][i] = t < p.T && e < p.E ? get(p.logits + t * p.E + e) : -__builtin_inff();
         }
-        const int e = (int)(0xffffffffu - (uint32_t)best);
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] == best)
-                key[i] = 0;
-        const float p = expf(logits[e] - top);
-        chosen += p;
-        if (lane == j) {
-            id = e;
-            mine = p;
-        }
+    for (int k = 0; k < kTokens; ++k) {
+        const int t = wave + k * kRouteWaves;
+        if (t < p.T)
+            choose<PER>(v[k], p.E, p.topk, p.renorm, p.ids + t * p.topk, p.weights + t * p.topk,
+                        ids + t * p.topk);
     }
-    const float over = renorm && sum == sum ? chosen : sum;
-    if (lane < topk) {
-        ids[lane] = id;
-        weights[lane] = mine / over;
-    }
-}
-
-template <int PER>
-__global__ void __launch_bounds__(256) moe_choose_kernel(MoeArgs p)
-{
-    const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t < p.T)
-        choose<PER>(p.logits + (int64_t)t * p.E, p.E, p.topk, p.renorm,
-                    p.ids + (int64_t)t * p.topk, p.weights + (int64_t)t * p.topk);
+    __syncthreads();
+    if (p.plan)
+        make_plan(p.plan, p.T * p.topk, p.E, cnt, [&](int i) { return ids[i]; });
 }
 
 // ---- experts ------------------------------------------------------------
 
 constexpr int kMoeWaves = 8;
 
-// Which slots (t * topk + j) go to which expert: the experts that have any,
-// in rising order, and each one's slots side by side.  Every workgroup works
-// it out for itself: at most 512 ids, read from L2.  The order of an
-// expert's slots is that of the LDS atomics and changes no result: a slot is
-// a row of its own in every product.
-struct Plan {
-    int *cnt;            // E: slots of an expert, then its cursor into `slot`
-    int *off;            // active + 1
-    uint16_t *act;       // active experts
-    uint16_t *slot;      // slots, expert by expert
-    int active;
-};
-
-__host__ __device__ inline int plan_bytes(int E, int n)
-{
-    const int a = E < n ? E : n;
-    return (E * 4 + (a + 1) * 4 + a * 2 + n * 2 + 4 + 15) / 16 * 16;
-}
-
-__device__ __forceinline__ Plan make_plan(char *lds, const int32_t *ids, int n, int E)
-{
-    // (a short list could be compared pair by pair in registers: 0.5 us less)
-    Plan pl;
-    const int a = E < n ? E : n;
-    pl.cnt = (int *)lds;
-    pl.off = pl.cnt + E;
-    int *active = pl.off + a + 1;
-    pl.act = (uint16_t *)(active + 1);
-    pl.slot = pl.act + a;
-    for (int e = threadIdx.x; e < E; e += blockDim.x)
-        pl.cnt[e] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x)
-        if ((uint32_t)ids[i] < (uint32_t)E)
-            atomicAdd(&pl.cnt[ids[i]], 1);
-    __syncthreads();
-    if (threadIdx.x < 64) {
-        const int lane = threadIdx.x;
-        int at = 0, base = 0;
-        for (int e0 = 0; e0 < E; e0 += 64) {
-            const int c = e0 + lane < E ? pl.cnt[e0 + lane] : 0;
-            int sum = c;                               // inclusive prefix sum
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const int up = __shfl_up(sum, d);
-                sum += lane >= d ? up : 0;
-            }
-            const uint64_t has = __ballot(c > 0);
-            if (c > 0) {
-                const int k = at + __popcll(has & ((1ull << lane) - 1));
-                pl.act[k] = (uint16_t)(e0 + lane);
-                pl.off[k] = base + sum - c;
-                pl.cnt[e0 + lane] = base + sum - c;
-            }
-            at += __popcll(has);
-            base += __shfl(sum, 63);
-        }
-        if (lane == 0) {
-            pl.off[at] = base;
-            *active = at;
-        }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x)
-        if ((uint32_t)ids[i] < (uint32_t)E)
-            pl.slot[atomicAdd(&pl.cnt[ids[i]], 1)] = (uint16_t)i;
-    pl.active = uniform(*active);
-    __syncthreads();
-    return pl;
-}
-
-// Rows that run against one reading of an expert's weights, as the registers
-// allow (packed weights need some for a group's sums).
+// Waves along K and blocks of 16 hidden rows to a wave of the down product,
+// whose K, the inner size, is short.
 template <int GS>
-constexpr int kRowsAtOnce = GS ? 32 : 64;
-
-// f(integral_constant<int, MB>): blocks of 16 rows for `count` of them.
-template <int GS, class F>
-__device__ __forceinline__ void with_blocks(int count, F &&f)
-{
-    if (count <= 16)
-        f(std::integral_constant<int, 1>{});
-    else if (GS != 0 || count <= 32)
-        f(std::integral_constant<int, 2>{});
-    else if constexpr (GS == 0)
-        f(std::integral_constant<int, 4>{});
-}
-
-// Blocks of 16 hidden rows to a workgroup of the down product: its K, the inner
-// size, is short, and four blocks of packed weights are the bytes of one of
-// 16-bit ones.
+constexpr int kDownWaves = GS ? 4 : 8;
 template <int GS>
-constexpr int kDownBlocks = GS ? 4 : 2;
+constexpr int kDownRows = 16 * 2 * (kMoeWaves / kDownWaves<GS>);
 
 template <bool BF, int GS, int MB>
 using UpCore = Skinny<BF, GS, 2, MB, kMoeWaves, 1, false>;
 template <bool BF, int GS, int MB>
-using DownCore = Skinny<BF, GS, kDownBlocks<GS>, MB, kMoeWaves, 1, true>;
+using DownCore = Skinny<BF, GS, 2, MB, kDownWaves<GS>, kMoeWaves / kDownWaves<GS>, true>;
 
 // h = silu(gate) * up for 16 of an expert's inner rows and all its slots.
 // One workgroup takes the 16 gate rows and their 16 up rows, eight waves
 // split the hidden size.
-template <bool BF, int GS>
-__global__ void __launch_bounds__(kMoeWaves * 64, 2) moe_up_kernel(MoeArgs p)
+template <bool BF, int GS, int MB>
+__global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel(MoeArgs p)
 {
     extern __shared__ f32x4 lds[];
-    const int n = p.T * p.topk, blocks = (p.I + 15) / 16;
+    const int blocks = (p.I + 15) / 16;
     const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
     const int s = wg / blocks, i0 = wg % blocks * 16;
-    const Plan pl = make_plan((char *)lds, p.ids, n, p.E);
-    if (s >= pl.active)
+    if (s >= p.plan->active)
         return;
-    char *smem = (char *)lds + plan_bytes(p.E, n);
-    const int64_t e = uniform(pl.act[s]);
-    const int end = uniform(pl.off[s + 1]);
-    for (int c0 = uniform(pl.off[s]); c0 < end; c0 += kRowsAtOnce<GS>) {
-        const int count = min(kRowsAtOnce<GS>, end - c0);
-        with_blocks<GS>(count, [&](auto mbs) {
-            UpCore<BF, GS, decltype(mbs)::value> c;
-            c.W = p.w13;
-            c.row[0] = e * 2 * p.I + i0;
-            c.row[1] = c.row[0] + p.I;
-            c.rows[0] = c.rows[1] = p.I - i0;
-            c.K = p.H;
-            c.M = count;
-            c.begin(smem, p.X, (uint32_t)((p.T - 1) * p.ldx + p.H) * 2u);
-            c.run([&](int m) {
-                return (uint32_t)(pl.slot[c0 + m] / p.topk * p.ldx) * 2u;
-            });
-            c.join([&](int m, int i, const float(&v)[2]) {
-                if (i0 + i < p.I) {
-                    const float act = v[0] / (1.0f + expf(-v[0]));
-                    p.h[(int64_t)pl.slot[c0 + m] * p.I + i0 + i] = from_float<BF>(act * v[1]);
-                }
-            });
+    const int64_t e = p.plan->act[s];
+    const int end = p.plan->off[s + 1];
+    for (int c0 = p.plan->off[s]; c0 < end; c0 += 16 * MB) {
+        const int count = min(16 * MB, end - c0);
+        const int *slot = p.plan->slot + c0;
+        UpCore<BF, GS, MB> c;
+        c.W = p.w13;
+        c.row[0] = e * 2 * p.I + i0;
+        c.row[1] = c.row[0] + p.I;
+        c.rows[0] = c.rows[1] = p.I - i0;
+        c.K = p.H;
+        c.M = count;
+        c.begin((char *)lds, p.X, (uint32_t)((p.T - 1) * p.ldx + p.H) * 2u);
+        c.run([&](int m) { return (uint32_t)(slot[m] / p.topk * p.ldx) * 2u; });
+        c.join([&](int m, int i, const float(&v)[2]) {
+            if (i0 + i < p.I) {
+                const float act = v[0] / (1.0f + expf(-v[0]));
+                p.h[(int64_t)slot[m] * p.I + i0 + i] = from_float<BF>(act * v[1]);
+            }
         });
         __syncthreads();
     }
 }
 
-// y = W2 h for a block of an expert's hidden rows and all its slots, in fp32.
-template <bool BF, int GS>
-__global__ void __launch_bounds__(kMoeWaves * 64, 2) moe_down_kernel(MoeArgs p)
+// y = W2 h for a block of an expert's hidden rows and all its slots, in fp32;
+// the last expert's workgroup of a block then forms each token's weighted
+// sum, over its slots in order.
+template <bool BF, int GS, int MB>
+__global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_down_kernel(MoeArgs p)
 {
     extern __shared__ f32x4 lds[];
-    constexpr int RB = kDownBlocks<GS>;
-    const int n = p.T * p.topk, blocks = (p.H + 16 * RB - 1) / (16 * RB);
+    const int n = p.T * p.topk, blocks = (p.H + kDownRows<GS> - 1) / kDownRows<GS>;
     const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
-    const int s = wg / blocks, h0 = wg % blocks * (16 * RB);
-    const Plan pl = make_plan((char *)lds, p.ids, n, p.E);
-    if (s >= pl.active)
+    const int s = wg / blocks, block = wg % blocks, h0 = block * kDownRows<GS>;
+    const int active = p.plan->active;
+    if (s >= active && s > 0)
         return;
-    char *smem = (char *)lds + plan_bytes(p.E, n);
-    const int64_t e = uniform(pl.act[s]);
-    const int end = uniform(pl.off[s + 1]);
-    for (int c0 = uniform(pl.off[s]); c0 < end; c0 += kRowsAtOnce<GS>) {
-        const int count = min(kRowsAtOnce<GS>, end - c0);
-        with_blocks<GS>(count, [&](auto mbs) {
-            DownCore<BF, GS, decltype(mbs)::value> c;
+    if (s < active) {
+        const int64_t e = p.plan->act[s];
+        const int end = p.plan->off[s + 1];
+        for (int c0 = p.plan->off[s]; c0 < end; c0 += 16 * MB) {
+            const int count = min(16 * MB, end - c0);
+            const int *slot = p.plan->slot + c0;
+            DownCore<BF, GS, MB> c;
             c.W = p.w2;
             c.row[0] = e * p.H + h0;
             c.rows[0] = p.H - h0;
             c.K = p.I;
             c.M = count;
-            c.begin(smem, p.h, (uint32_t)n * (uint32_t)p.I * 2u);
-            c.run([&](int m) { return (uint32_t)pl.slot[c0 + m] * (uint32_t)p.I * 2u; });
-            c.join([&](int m, int i, const float(&v)[RB]) {
+            c.begin((char *)lds, p.h, (uint32_t)n * (uint32_t)p.I * 2u);
+            c.run([&](int m) { return (uint32_t)slot[m] * (uint32_t)p.I * 2u; });
+            c.join([&](int m, int i, const float(&v)[2]) {
+                const int h = h0 + (i >> 4) * 32 + (i & 15);
 #pragma unroll
-                for (int r = 0; r < RB; ++r)
-                    if (h0 + 16 * r + i < p.H)
-                        p.y[(int64_t)pl.slot[c0 + m] * p.H + h0 + 16 * r + i] = v[r];
+                for (int r = 0; r < 2; ++r)
+                    if (h + 16 * r < p.H)
+                        put(p.y + (int64_t)slot[m] * p.H + h + 16 * r, v[r]);
             });
-        });
-        __syncthreads();
+            __syncthreads();
+        }
+        if (!last_of(p.tickets + 1 + block, active, (uint32_t *)lds))
+            return;
+    }
+    for (int i = threadIdx.x; i < p.T * kDownRows<GS>; i += kMoeWaves * 64) {
+        const int t = i / kDownRows<GS>, h = h0 + i % kDownRows<GS>;
+        if (h >= p.H)
+            continue;
+        float sum = 0.0f;
+        for (int j = 0; j < p.topk; ++j) {
+            const int slot = t * p.topk + j;
+            if ((uint32_t)p.ids[slot] < (uint32_t)p.E)
+                sum = __builtin_fmaf(p.weights[slot], get(p.y + (int64_t)slot * p.H + h), sum);
+        }
+        p.D[t * p.ldd + h] = from_float<BF>(sum);
     }
 }
 
-// The weighted sum over a token's slots, in order.
-template <bool BF>
-__global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs p)
+template <bool BF, int PER>
+void launch_route_per(const MoeArgs &p, hipStream_t stream)
 {
-    const int t = blockIdx.y, h = blockIdx.x * 256 + threadIdx.x;
-    if (h >= p.H)
-        return;
-    float sum = 0.0f;
-    for (int j = 0; j < p.topk; ++j) {
-        const int slot = t * p.topk + j;
-        if ((uint32_t)p.ids[slot] < (uint32_t)p.E)
-            sum = __builtin_fmaf(p.weights[slot], p.y[(int64_t)slot * p.H + h], sum);
-    }
-    p.D[t * p.ldd + h] = from_float<BF>(sum);
+    const int act = RouteCore<BF>::lds_bytes(p.T < 16 ? p.T : 16, p.H);
+    const int last = (MOE_MAX_EXPERTS + kMoeSlots) * 4;
+    hipLaunchKernelGGL((moe_route_kernel<BF, PER>),
+                       dim3((unsigned)cdiv(p.E, 16), (unsigned)cdiv(p.T, 16)),
+                       dim3(kRouteWaves * 64), act > last ? act : last, stream, p);
 }
 
 template <bool BF>
 void launch_route(const MoeArgs &p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((moe_logits_kernel<BF>),
-                       dim3((unsigned)cdiv(p.E, 16), (unsigned)cdiv(p.T, 16)),
-                       dim3(kRouteWaves * 64), RouteCore<BF>::lds_bytes(p.T < 16 ? p.T : 16, p.H),
-                       stream, p);
-    const dim3 grid((unsigned)cdiv(p.T, 4));
     if (p.E <= 64)
-        hipLaunchKernelGGL((moe_choose_kernel<1>), grid, dim3(256), 0, stream, p);
+        launch_route_per<BF, 1>(p, stream);
     else if (p.E <= 256)
-        hipLaunchKernelGGL((moe_choose_kernel<4>), grid, dim3(256), 0, stream, p);
+        launch_route_per<BF, 4>(p, stream);
     else
-        hipLaunchKernelGGL((moe_choose_kernel<16>), grid, dim3(256), 0, stream, p);
+        launch_route_per<BF, 16>(p, stream);
 }
 
 template <bool BF>
-void launch_experts(const MoeArgs &p, int group, hipStream_t stream)
+void launch_experts(const MoeArgs &p, int group, bool planned, hipStream_t stream)
 {
     const int n = p.T * p.topk, most = p.E < n ? p.E : n;
-    const int plan = plan_bytes(p.E, n);
+    if (!planned)
+        hipLaunchKernelGGL((moe_plan_kernel<>), dim3(1), dim3(kMoeSlots), 0, stream, p);
     with_group(group, [&](auto gs) {
         constexpr int GS = decltype(gs)::value;
-        const int rows = n < kRowsAtOnce<GS> ? n : kRowsAtOnce<GS>;
-        const int up = plan + UpCore<BF, GS, 1>::lds_bytes(rows, p.H);
-        const int down = plan + DownCore<BF, GS, 1>::lds_bytes(rows, p.I);
-        hipLaunchKernelGGL((moe_up_kernel<BF, GS>), tile_grid(most * cdiv(p.I, 16)),
-                           dim3(kMoeWaves * 64), up, stream, p);
-        hipLaunchKernelGGL((moe_down_kernel<BF, GS>),
-                           tile_grid(most * cdiv(p.H, 16 * kDownBlocks<GS>)),
-                           dim3(kMoeWaves * 64), down, stream, p);
+        auto go = [&](auto mbs) {
+            constexpr int MB = decltype(mbs)::value;
+            const int rows = n < 16 * MB ? n : 16 * MB;
+            hipLaunchKernelGGL((moe_up_kernel<BF, GS, MB>), tile_grid(most * cdiv(p.I, 16)),
+                               dim3(kMoeWaves * 64), (UpCore<BF, GS, MB>::lds_bytes(rows, p.H)),
+                               stream, p);
+            hipLaunchKernelGGL((moe_down_kernel<BF, GS, MB>),
+                               tile_grid(most * cdiv(p.H, kDownRows<GS>)), dim3(kMoeWaves * 64),
+                               (DownCore<BF, GS, MB>::lds_bytes(rows, p.I)), stream, p);
+        };
+        // 16 rows against one reading of an expert's weights, in registers that
+        // let two workgroups share a CU, or 32 where the mean is above 8
+        if (n <= 8 * p.E)
+            go(std::integral_constant<int, 1>{});
+        else
+            go(std::integral_constant<int, 2>{});
     });
-    hipLaunchKernelGGL((moe_combine_kernel<BF>), dim3((unsigned)cdiv(p.H, 256), (unsigned)p.T),
-                       dim3(256), 0, stream, p);
 }
 
 } // namespace

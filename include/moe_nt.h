@@ -55,7 +55,8 @@ typedef struct moe_nt_weights {
  * MOE_MAX_LDX).  The logits are
  * summed in fp32.  A row with a NaN logit, or whose largest is infinite, gets
  * NaN weights and topk distinct valid ids.  topk in [1, min(experts, MOE_MAX_TOPK)].
- * Only router, experts, hidden and dtype of *w are used.
+ * Of *w the sizes, group and dtype have to be valid, and router; w13, w2 and
+ * their scales and zeros are not used.
  *
  * workspace: device memory of moe_nt_ws_size(T, w, topk) bytes or more,
  * 256-byte aligned, zero-filled before its first use; every call leaves it
