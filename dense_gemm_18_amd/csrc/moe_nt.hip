@@ -32,7 +32,7 @@ Layout layout_of(int64_t T, const moe_nt_weights *w, int topk)
     // a ticket for each 16 hidden rows is more than any block size needs
     l.plan = up(4 * (1 + cdiv(w->hidden, 16)));
     l.logits = l.plan + up(sizeof(Plan));
-    l.h = l.logits + up(chunk * w->experts * 4);
+    l.h = l.logits + up(route_parts(w->hidden) * chunk * w->experts * 4);
     l.y = l.h + up(slots * w->inner * 2);
     l.bytes = l.y + up(slots * w->hidden * 4);
     return l;
@@ -178,6 +178,7 @@ MoeArgs common_args(const moe_nt_weights *w, const void *X, const int32_t *ids,
     p.H = (int)w->hidden;
     p.I = (int)w->inner;
     p.topk = topk;
+    p.parts = route_parts(w->hidden);
     return p;
 }
 

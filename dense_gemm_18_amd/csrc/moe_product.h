@@ -18,16 +18,18 @@ inline int moe_chunk(int64_t T, int topk)
 // launches that follow.  The order of an expert's slots is that of the LDS
 // atomics and changes no result: a slot is a row of its own in every product.
 struct Plan {
-    int active;
-    int act[kMoeSlots];          // active experts
-    int off[kMoeSlots + 1];      // where their slots start
+    struct Item {
+        int expert, first, count;    // slots slot[first .. first + count); count 0: none
+        int slot;                    // slot[first]
+    } item[kMoeSlots];
+    int active;                      // items in use
     int slot[kMoeSlots];
 };
 
 struct MoeArgs {
     const uint16_t *X;             // T rows, ldx apart
     const uint16_t *router;        // E x H
-    float *logits;                 // T x E
+    float *logits;                 // parts x T x E
     int32_t *ids;                  // T x topk
     float *weights;                // T x topk
     WeightRef w13, w2;             // E * 2 * I rows of H, E * H rows of I
@@ -38,6 +40,7 @@ struct MoeArgs {
     uint16_t *D;                   // T rows, ldd apart
     int64_t ldx, ldd;
     int T, E, H, I, topk, renorm;
+    int parts;                     // pieces of H in the router
 };
 
 // One translation unit for each type.  Not exported from the library.
@@ -117,21 +120,31 @@ __device__ __forceinline__ void make_plan(Plan *plan, int n, int E, int *cnt, F 
             const uint64_t has = __ballot(c > 0);
             if (c > 0) {
                 const int k = at + __popcll(has & ((1ull << lane) - 1));
-                plan->act[k] = e0 + lane;
-                plan->off[k] = base + sum - c;
-                cnt[e0 + lane] = base + sum - c;
+                plan->item[k].expert = e0 + lane;
+                plan->item[k].first = base + sum - c;
+                plan->item[k].count = c;
+                cnt[e0 + lane] = (base + sum - c) << 16 | k;
             }
             at += __popcll(has);
             base += __shfl(sum, 63);
         }
-        if (lane == 0) {
-            plan->off[at] = base;
+        // what a launch for as many items as there can be also looks at
+        for (int k = at + lane; k < min(E, n); k += 64)
+            plan->item[k].count = 0;
+        if (lane == 0)
             plan->active = at;
-        }
     }
     __syncthreads();
-    if (id >= 0)
-        plan->slot[atomicAdd(&cnt[id], 1)] = threadIdx.x;
+    if (id >= 0) {
+        const int place = atomicAdd(&cnt[id], 1 << 16);
+        plan->slot[place >> 16] = threadIdx.x;
+    }
+    __syncthreads();
+    // the first slots, now that all are in place
+    if (id >= 0) {
+        const int k = cnt[id] & 0xffff;
+        plan->item[k].slot = plan->slot[plan->item[k].first];
+    }
 }
 
 template <int = 0>
@@ -143,7 +156,9 @@ __global__ void __launch_bounds__(kMoeSlots) moe_plan_kernel(MoeArgs p)
 
 // ---- router -------------------------------------------------------------
 
-constexpr int kRouteWaves = 16;
+constexpr int kRouteWaves = 8;
+constexpr int kRouteK = 1024;        // of the hidden size, to a workgroup
+inline int route_parts(int64_t H) { return H <= 16 * kRouteK ? (int)cdiv(H, kRouteK) : 16; }
 
 // Order of logits as unsigned numbers: rising with the value, both zeros
 // alike, every NaN below everything.
@@ -156,15 +171,15 @@ __device__ __forceinline__ uint32_t order_of(float v)
 }
 
 // Reductions over the wave by data-parallel moves (in order, no LDS): the
-// result in every lane.
-template <class F>
-__device__ __forceinline__ float reduce_wave(float v, float none, F &&f)
+// result as a scalar.  `none`: what leaves a value as it is.
+template <class T, class F>
+__device__ __forceinline__ T reduce_wave(T v, T none, F &&f)
 {
     auto step = [&](auto ctrl, auto rows) G18_INLINE {
         const int moved = __builtin_amdgcn_update_dpp(
             __builtin_bit_cast(int, none), __builtin_bit_cast(int, v), decltype(ctrl)::value,
             decltype(rows)::value, 0xf, false);
-        v = f(v, __builtin_bit_cast(float, moved));
+        v = f(v, __builtin_bit_cast(T, moved));
     };
     step(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xf>{});  // 1 up
     step(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xf>{});  // 2 up
@@ -172,65 +187,85 @@ __device__ __forceinline__ float reduce_wave(float v, float none, F &&f)
     step(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xf>{});  // 8 up
     step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});  // lane 15 on
     step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // lane 31 on
-    return __builtin_bit_cast(float,
-                              __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-// The topk largest of a token's logits and their softmax weights, by one wave
-// with PER logits v per lane (E <= 64 * PER).  An expert's place is the number of those
-// that come before it, larger ones and equal ones of lower index: E * PER
-// comparisons per lane whatever topk is, and no exchange that waits for the
-// one before (topk maxima over the wave took 1 us each for 4).
-template <int PER>
-__device__ __forceinline__ void choose(const float (&v)[PER], int E, int topk, bool renorm,
-                                       int32_t *ids, float *weights, int *lds_ids)
+// The topk largest logits of the tokens first, first + step, ... (NT of them,
+// those below T) and their softmax weights, by one wave with PER logits of
+// each token per lane (E <= 64 * PER): topk maxima over the wave of the
+// logits' order, each taken at its lowest index.  Several tokens at once hide
+// the moves' latency (64 tokens, 16 experts: 17 us one after the other by
+// counting larger ones, 64 comparisons for each).
+template <int PER, int NT>
+__device__ __forceinline__ void choose(const float (&v)[NT][PER], const MoeArgs &p, int first,
+                                       int step, int *lds_ids)
 {
     const int lane = threadIdx.x & 63;
-    uint32_t key[PER];
-    int place[PER];
-    float top = -__builtin_inff();
+    uint32_t key[NT][PER];
+    int place[NT][PER];
+    float top[NT];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        key[i] = order_of(v[i]);
-        place[i] = lane + 64 * i < E ? 0 : INT32_MAX / 2;
-        top = __builtin_fmaxf(top, v[i]);      // a NaN shows in the sum below
+    for (int t = 0; t < NT; ++t) {
+        float most = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            // 0: absent or taken
+            key[t][i] = lane + 64 * i < p.E ? order_of(v[t][i]) + 1 : 0;
+            place[t][i] = INT32_MAX;
+            most = __builtin_fmaxf(most, v[t][i]);      // a NaN shows in the sum below
+        }
+        top[t] = reduce_wave(most, -__builtin_inff(),
+                             [](float a, float b) { return __builtin_fmaxf(a, b); });
     }
-    top = reduce_wave(top, -__builtin_inff(),
-                      [](float a, float b) { return __builtin_fmaxf(a, b); });
+    for (int j = 0; j < p.topk; ++j) {
+        auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int most = min(64, E - 64 * k);
-        for (int o = 0; o < most; ++o) {
-            const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key[k], o);
+        for (int t = 0; t < NT; ++t) {
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                most = larger(most, key[t][i]);
+            most = reduce_wave(most, 0u, larger);
+            bool found = false;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const bool lower = i > k || (i == k && lane > o);
-                place[i] += other > key[i] || (other == key[i] && lower);
+                const uint64_t who = __ballot(key[t][i] == most);
+                const bool mine = !found && who && lane == __builtin_ctzll(who);
+                found |= who != 0;
+                place[t][i] = mine ? j : place[t][i];
+                key[t][i] = mine ? 0 : key[t][i];
             }
         }
     }
-    float sum = 0.0f, chosen = 0.0f, p[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        p[i] = lane + 64 * i < E ? expf(v[i] - top) : 0.0f;
-        sum += p[i];
-        chosen += place[i] < topk ? p[i] : 0.0f;
-    }
-    auto add = [](float a, float b) { return a + b; };
-    sum = reduce_wave(sum, 0.0f, add);
-    chosen = reduce_wave(chosen, 0.0f, add);
-    const float over = renorm && sum == sum ? chosen : sum;
+    for (int t = 0; t < NT; ++t) {
+        float sum = 0.0f, chosen = 0.0f, w[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (place[i] < topk) {
-            ids[place[i]] = lane + 64 * i;
-            lds_ids[place[i]] = lane + 64 * i;
-            weights[place[i]] = p[i] / over;
+        for (int i = 0; i < PER; ++i) {
+            w[i] = lane + 64 * i < p.E ? expf(v[t][i] - top[t]) : 0.0f;
+            sum += w[i];
+            chosen += place[t][i] < p.topk ? w[i] : 0.0f;
         }
+        auto add = [](float a, float b) { return a + b; };
+        sum = reduce_wave(sum, 0.0f, add);
+        chosen = reduce_wave(chosen, 0.0f, add);
+        const float over = p.renorm && sum == sum ? chosen : sum;
+        const int token = first + t * step;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (token < p.T && place[t][i] < p.topk) {
+                const int slot = token * p.topk + place[t][i];
+                p.ids[slot] = lane + 64 * i;
+                lds_ids[slot] = lane + 64 * i;
+                p.weights[slot] = w[i] / over;
+            }
+    }
 }
 
-// Logits of 16 experts for 16 tokens, sixteen waves splitting the hidden
-// size; the last workgroup then chooses for every token and makes the plan.
+// Logits of 16 experts for 16 tokens over one of `parts` pieces of the hidden
+// size (a router is small: with the whole of it to a workgroup, 64 tokens of
+// 4096 against 16 experts took 22 us); the last workgroup adds the pieces in
+// order, chooses for every token and makes the plan.
 template <bool BF>
 using RouteCore = Skinny<BF, 0, 1, 1, kRouteWaves, 1, true>;
 
@@ -238,41 +273,69 @@ template <bool BF, int PER>
 __global__ void __launch_bounds__(kRouteWaves * 64) moe_route_kernel(MoeArgs p)
 {
     extern __shared__ f32x4 lds[];
-    const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
+    const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16, part = blockIdx.z;
+    // pieces of whole steps
+    const int steps = (p.H + 127) >> 7;
+    const int k0 = part * steps / p.parts * 128;
     RouteCore<BF> c;
     c.W.w = p.router;
     c.row[0] = e0;
     c.rows[0] = p.E - e0;
-    c.K = p.H;
+    c.stride = p.H;
+    c.K = min((part + 1) * steps / p.parts * 128, p.H) - k0;
+    c.W.w += k0;
     c.M = min(16, p.T - t0);
-    c.begin((char *)lds, p.X + t0 * p.ldx, (uint32_t)((c.M - 1) * p.ldx + p.H) * 2u);
+    c.begin((char *)lds, p.X + t0 * p.ldx + k0, (uint32_t)((c.M - 1) * p.ldx + c.K) * 2u);
     c.run([&](int m) { return (uint32_t)(m * p.ldx) * 2u; });
+    float *logits = p.logits + (int64_t)part * p.T * p.E;
     c.join([&](int m, int n, const float(&v)[1]) {
         if (e0 + n < p.E)
-            put(p.logits + (t0 + m) * p.E + e0 + n, v[0]);
+            put(logits + (t0 + m) * p.E + e0 + n, v[0]);
     });
     __syncthreads();
     int *cnt = (int *)lds, *ids = cnt + MOE_MAX_EXPERTS;
-    if (!last_of(p.tickets, gridDim.x * gridDim.y, (uint32_t *)ids))
+    if (!last_of(p.tickets, gridDim.x * gridDim.y * gridDim.z, (uint32_t *)ids))
         return;
     __syncthreads();
-    // a wave's tokens, at most four, all their logits under way at once
+    // four of a wave's tokens at a time, all their logits under way at once
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    constexpr int kTokens = 64 / kRouteWaves;
-    float v[kTokens][PER];
+    constexpr int kTokens = PER == 1 ? 4 : PER == 4 ? 2 : 1;
+    for (int base = wave; base < p.T; base += kTokens * kRouteWaves) {
+        float v[kTokens][PER];
 #pragma unroll
-    for (int k = 0; k < kTokens; ++k)
+        for (int k = 0; k < kTokens; ++k)
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int t = wave + k * kRouteWaves, e = lane + 64 * i;
-            v[k][i] = t < p.T && e < p.E ? get(p.logits + t * p.E + e) : -__builtin_inff();
+            for (int i = 0; i < PER; ++i)
+                v[k][i] = 0.0f;
+        // these loads go past L2 and take 2 us: as many as fit at once
+        for (int q = 0; q < p.parts; q += 4) {
+            float g[4][kTokens][PER];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < kTokens; ++k)
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int t = base + k * kRouteWaves, e = lane + 64 * i;
+                        const bool in = q + j < p.parts && t < p.T && e < p.E;
+                        g[j][k][i] =
+                            get(p.logits + (in ? ((int64_t)(q + j) * p.T + t) * p.E + e : 0));
+                    }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < kTokens; ++k)
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        v[k][i] += q + j < p.parts ? g[j][k][i] : 0.0f;
         }
 #pragma unroll
-    for (int k = 0; k < kTokens; ++k) {
-        const int t = wave + k * kRouteWaves;
-        if (t < p.T)
-            choose<PER>(v[k], p.E, p.topk, p.renorm, p.ids + t * p.topk, p.weights + t * p.topk,
-                        ids + t * p.topk);
+        for (int k = 0; k < kTokens; ++k)
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                v[k][i] = lane + 64 * i < p.E ? v[k][i] : -__builtin_inff();
+        choose<PER, kTokens>(v, p, base, kRouteWaves, ids);
     }
     __syncthreads();
     if (p.plan)
@@ -305,13 +368,14 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
     const int blocks = (p.I + 15) / 16;
     const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
     const int s = wg / blocks, i0 = wg % blocks * 16;
-    if (s >= p.plan->active)
-        return;
-    const int64_t e = p.plan->act[s];
-    const int end = p.plan->off[s + 1];
-    for (int c0 = p.plan->off[s]; c0 < end; c0 += 16 * MB) {
-        const int count = min(16 * MB, end - c0);
-        const int *slot = p.plan->slot + c0;
+    const Plan::Item it = p.plan->item[s];
+    const int64_t e = it.expert;
+    for (int c0 = 0; c0 < it.count; c0 += 16 * MB) {
+        const int count = min(16 * MB, it.count - c0);
+        // a single row, the common case of few tokens, needs no further load
+        auto slot = [&](int m) {
+            return it.count == 1 ? it.slot : p.plan->slot[it.first + c0 + m];
+        };
         UpCore<BF, GS, MB> c;
         c.W = p.w13;
         c.row[0] = e * 2 * p.I + i0;
@@ -320,11 +384,11 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
         c.K = p.H;
         c.M = count;
         c.begin((char *)lds, p.X, (uint32_t)((p.T - 1) * p.ldx + p.H) * 2u);
-        c.run([&](int m) { return (uint32_t)(slot[m] / p.topk * p.ldx) * 2u; });
+        c.run([&](int m) { return (uint32_t)(slot(m) / p.topk * p.ldx) * 2u; });
         c.join([&](int m, int i, const float(&v)[2]) {
             if (i0 + i < p.I) {
                 const float act = v[0] / (1.0f + expf(-v[0]));
-                p.h[(int64_t)slot[m] * p.I + i0 + i] = from_float<BF>(act * v[1]);
+                p.h[(int64_t)slot(m) * p.I + i0 + i] = from_float<BF>(act * v[1]);
             }
         });
         __syncthreads();
@@ -341,15 +405,16 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_down_kern
     const int n = p.T * p.topk, blocks = (p.H + kDownRows<GS> - 1) / kDownRows<GS>;
     const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
     const int s = wg / blocks, block = wg % blocks, h0 = block * kDownRows<GS>;
-    const int active = p.plan->active;
-    if (s >= active && s > 0)
+    const Plan::Item it = p.plan->item[s];
+    if (it.count == 0 && s > 0)
         return;
-    if (s < active) {
-        const int64_t e = p.plan->act[s];
-        const int end = p.plan->off[s + 1];
-        for (int c0 = p.plan->off[s]; c0 < end; c0 += 16 * MB) {
-            const int count = min(16 * MB, end - c0);
-            const int *slot = p.plan->slot + c0;
+    if (it.count > 0) {
+        const int64_t e = it.expert;
+        for (int c0 = 0; c0 < it.count; c0 += 16 * MB) {
+            const int count = min(16 * MB, it.count - c0);
+            auto slot = [&](int m) {
+                return it.count == 1 ? it.slot : p.plan->slot[it.first + c0 + m];
+            };
             DownCore<BF, GS, MB> c;
             c.W = p.w2;
             c.row[0] = e * p.H + h0;
@@ -357,17 +422,17 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_down_kern
             c.K = p.I;
             c.M = count;
             c.begin((char *)lds, p.h, (uint32_t)n * (uint32_t)p.I * 2u);
-            c.run([&](int m) { return (uint32_t)slot[m] * (uint32_t)p.I * 2u; });
+            c.run([&](int m) { return (uint32_t)slot(m) * (uint32_t)p.I * 2u; });
             c.join([&](int m, int i, const float(&v)[2]) {
                 const int h = h0 + (i >> 4) * 32 + (i & 15);
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
                     if (h + 16 * r < p.H)
-                        put(p.y + (int64_t)slot[m] * p.H + h + 16 * r, v[r]);
+                        put(p.y + (int64_t)slot(m) * p.H + h + 16 * r, v[r]);
             });
             __syncthreads();
         }
-        if (!last_of(p.tickets + 1 + block, active, (uint32_t *)lds))
+        if (!last_of(p.tickets + 1 + block, p.plan->active, (uint32_t *)lds))
             return;
     }
     for (int i = threadIdx.x; i < p.T * kDownRows<GS>; i += kMoeWaves * 64) {
@@ -387,10 +452,10 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_down_kern
 template <bool BF, int PER>
 void launch_route_per(const MoeArgs &p, hipStream_t stream)
 {
-    const int act = RouteCore<BF>::lds_bytes(p.T < 16 ? p.T : 16, p.H);
+    const int act = RouteCore<BF>::lds_bytes(p.T < 16 ? p.T : 16, (int)cdiv(cdiv(p.H, 128), p.parts) * 128);
     const int last = (MOE_MAX_EXPERTS + kMoeSlots) * 4;
     hipLaunchKernelGGL((moe_route_kernel<BF, PER>),
-                       dim3((unsigned)cdiv(p.E, 16), (unsigned)cdiv(p.T, 16)),
+                       dim3((unsigned)cdiv(p.E, 16), (unsigned)cdiv(p.T, 16), (unsigned)p.parts),
                        dim3(kRouteWaves * 64), act > last ? act : last, stream, p);
 }
 

@@ -147,6 +147,7 @@ struct Skinny {
     int64_t row[NR];
     int rows[NR];
     int K, M;
+    int stride = 0;              // 16-bit weights: elements between rows, 0 for K
     f32x4 acc[RB][MB];
 
     char *lds;
@@ -200,13 +201,14 @@ struct Skinny {
         chunk = chunk_of(M, K);
         astride = chunk * 2 + 16;
         sstride = chunk / 128 * kGroups + 1;
-        const uint32_t row_bytes = GS ? (uint32_t)((K + 127) >> 7) * 64u : (uint32_t)K * 2u;
+        const uint32_t row_bytes =
+            GS ? (uint32_t)((K + 127) >> 7) * 64u : (uint32_t)(stride ? stride : K) * 2u;
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const int n = min(rows[i], kRows / NR);
             wr[i] = range(GS ? (const char *)W.q + row[i] * row_bytes
                              : (const char *)W.w + row[i] * row_bytes,
-                          n * row_bytes);
+                          GS ? n * row_bytes : n ? (n - 1) * row_bytes + K * 2u : 0);
             if constexpr (GS != 0) {
                 sr[i] = range(W.s + row[i] * G, n * G * 2);
                 zr[i] = range(W.z ? W.z + row[i] * G : nullptr, W.z ? n * G : 0);
