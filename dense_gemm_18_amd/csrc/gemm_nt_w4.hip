@@ -5,6 +5,8 @@
 
 namespace {
 
+typedef int16_t s16x2 __attribute__((ext_vector_type(2)));
+
 // 16 bytes at any 2-byte alignment (one global load on gfx950).
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 
@@ -22,66 +24,140 @@ __device__ __forceinline__ u32x4 load16_part(const uint16_t *p, int count)
     return v;
 }
 
+// A lane's place among the packed words of an N-row weight, and the step from
+// one to the next of its words: a division at the start only.
+struct WordWalk {
+    int64_t n;
+    int at;
+
+    __device__ __forceinline__ WordWalk(int words)
+    {
+        const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
+        n = i / words;
+        at = (int)(i - n * words);
+    }
+    __device__ __forceinline__ void next(int words, int64_t rows, int rest)
+    {
+        n += rows;
+        at += rest;
+        if (at >= words) {
+            at -= words;
+            ++n;
+        }
+    }
+};
+
+// rint(x / s) for 16-bit x and s, and `rs` = 1 / s within 2 ulp: x / s is a
+// half-integer or at least 2^-12 from one (both have at most 11 bits), and
+// fma(x, rs, 768) - 768 puts it on a grid of 2^-14, where the half-integers
+// are, less than 2^-18 from where it was.  Three instructions for a
+// correctly rounded division's ten and a rint.
+__device__ __forceinline__ float nearest(float x, float rs)
+{
+    return __builtin_rintf(__builtin_fmaf(x, rs, 768.0f) - 768.0f);
+}
+
 // Quantisation, eight consecutive elements of a row per lane: one 16-byte
 // load, one packed word.  Lanes follow K, so a group's 4, 8 or 16 lanes are
 // neighbours and its extremes take 2, 3 or 4 exchanges; a 64-byte block's
-// words leave permuted but together.  Bound by memory: 2.5 bytes and a few
-// ten instructions per element pair.
+// words leave permuted but together.  2.5 bytes and more per element.
 template <bool BF, int GS>
 __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restrict__ W,
                                                        uint32_t *__restrict__ Q,
                                                        uint16_t *__restrict__ S,
                                                        uint8_t *__restrict__ Z, int64_t N, int K,
-                                                       int64_t ldw)
+                                                       int64_t ldw, int64_t step_rows,
+                                                       int step_rest)
 {
     constexpr int kLanes = GS / 8;
     const int words = ((K + 127) >> 7) * 16, G = (K + GS - 1) / GS;
-    const int64_t total = N * words;
     // every lane of a group of 16 runs the same number of times: words and the
     // grid's lanes are multiples of 16
-    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * 256) {
-        const int64_t n = i / words;
-        const int at = (int)(i - n * words), k = at * 8;
-        const uint16_t *src = W + n * ldw + k;
+    auto fetch = [&](const WordWalk &w) {
+        const uint16_t *src = W + w.n * ldw + w.at * 8;
         u32x4 raw = {0, 0, 0, 0};
-        if (k + 8 <= K)
+        if (w.n < N && w.at * 8 + 8 <= K)
             raw = load16(src);
-        else if (k < K)
-            raw = load16_part(src, K - k);
-        float x[8], lo = 0.0f, hi = 0.0f;
-        bool odd = false;
+        else if (w.n < N && w.at * 8 < K)
+            raw = load16_part(src, K - w.at * 8);
+        return raw;
+    };
+    WordWalk w(words);
+    u32x4 ahead = fetch(w);
+    while (w.n < N) {
+        // the next word's elements are under way while this one's are worked
+        // on: 32 waves with one load each are 32 KB of a CU's 64 in flight
+        const int64_t n = w.n;
+        const int at = w.at, k = at * 8;
+        const u32x4 raw = ahead;
+        w.next(words, step_rows, step_rest);
+        ahead = fetch(w);
+        // The largest value and the largest magnitude of a negative one, at
+        // least 0, as bits: signed 16-bit integers order them, two at a time.
+        // An infinity or a NaN is the largest of either.
+        s16x2 up = {0, 0}, down = {0, 0};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = to_float<BF>((uint16_t)(raw[e >> 1] >> (16 * (e & 1))));
-            odd |= !(__builtin_fabsf(x[e]) < __builtin_inff());
-            lo = __builtin_fminf(lo, x[e]);
-            hi = __builtin_fmaxf(hi, x[e]);
+        for (int i = 0; i < 4; ++i) {
+            // (as elements of one vector the compiler dropped three of the four)
+            uint32_t pair = raw[i];
+            asm("" : "+v"(pair));
+            up = __builtin_elementwise_max(up, __builtin_bit_cast(s16x2, pair));
+            down = __builtin_elementwise_max(down,
+                                             __builtin_bit_cast(s16x2, pair ^ 0x80008000u));
         }
-        int any = odd;
-#pragma unroll
-        for (int d = 1; d < kLanes; d *= 2) {
-            lo = __builtin_fminf(lo, __shfl_xor(lo, d));
-            hi = __builtin_fmaxf(hi, __shfl_xor(hi, d));
-            any |= __shfl_xor(any, d);
-        }
+        // over the group's lanes: neighbours, pairs, halves of 8 and of 16
+        auto widest = [](s16x2 v) {
+            auto step = [&](auto ctrl) {
+                const int moved = __builtin_amdgcn_update_dpp(
+                    0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, false);
+                v = __builtin_elementwise_max(v, __builtin_bit_cast(s16x2, moved));
+            };
+            step(std::integral_constant<int, 0xb1>{});       // lane ^ 1
+            step(std::integral_constant<int, 0x4e>{});       // lane ^ 2
+            if constexpr (kLanes > 4)
+                step(std::integral_constant<int, 0x141>{});  // 7 - lane of 8
+            if constexpr (kLanes > 8)
+                step(std::integral_constant<int, 0x140>{});  // 15 - lane of 16
+            return (uint16_t)(v[0] > v[1] ? v[0] : v[1]);
+        };
+        const uint16_t up_bits = widest(up), down_bits = widest(down);
+        constexpr uint16_t kInf = BF ? 0x7f80 : 0x7c00;
+        const bool any = up_bits >= kInf || down_bits >= kInf;
+        const float hi = to_float<BF>(up_bits), lo = -to_float<BF>(down_bits);
         const uint16_t bits =
             from_float<BF>(Z ? (hi - lo) / 15.0f : __builtin_fmaxf(hi, -lo) / 7.0f);
         const float s = to_float<BF>(bits);
         const bool live = s > 0.0f && !any;
+        const float rs = live ? 1.0f / s : 0.0f;
         float z = 8.0f;
         if (Z && live)
             z = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(-lo / s), 0.0f), 15.0f);
+        auto x = [&](int e) { return to_float<BF>((uint16_t)(raw[e >> 1] >> (16 * (e & 1)))); };
+        float r[8];
+        if (__any(rs > 0x1p100f)) {          // 1 / s may have overflowed
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                r[e] = live ? __builtin_rintf(x(e) / s) : 0.0f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                r[e] = live ? nearest(x(e), rs) : 0.0f;
+        }
         uint32_t word = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float r = live ? __builtin_rintf(x[e] / s) : 0.0f;
+            float v;
             if (Z)
-                r = __builtin_fminf(__builtin_fmaxf(r + z, 0.0f), 15.0f);
+                v = __builtin_amdgcn_fmed3f(r[e] + z, 0.0f, 15.0f);
             else
-                r = __builtin_fminf(__builtin_fmaxf(r, -8.0f), 7.0f) + 8.0f;
-            const uint32_t q = k + e < K ? (uint32_t)r : 0u;
-            word |= q << (4 * (e >> 1) + 16 * (e & 1));
+                v = __builtin_amdgcn_fmed3f(r[e], -8.0f, 7.0f) + 8.0f;
+            word |= (uint32_t)v << (4 * (e >> 1) + 16 * (e & 1));
+        }
+        if (k + 8 > K) {                     // bits past the row's end are 0
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (k + e >= K)
+                    word &= ~(15u << (4 * (e >> 1) + 16 * (e & 1)));
         }
         const int j = (at >> 2) & 3, c = at & 3;
         Q[n * words + (at & ~15) + 4 * c + j] = word;
@@ -100,14 +176,13 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint32_t *__restr
                                                          const uint16_t *__restrict__ S,
                                                          const uint8_t *__restrict__ Z,
                                                          uint16_t *__restrict__ W, int64_t N,
-                                                         int K, int64_t ldw)
+                                                         int K, int64_t ldw, int64_t step_rows,
+                                                         int step_rest)
 {
     const int words = ((K + 127) >> 7) * 16, G = (K + GS - 1) / GS;
-    const int64_t total = N * words;
-    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * 256) {
-        const int64_t n = i / words;
-        const int at = (int)(i - n * words), k = at * 8;
+    for (WordWalk w(words); w.n < N; w.next(words, step_rows, step_rest)) {
+        const int64_t n = w.n;
+        const int at = w.at, k = at * 8;
         if (k >= K)
             continue;
         const int j = (at >> 2) & 3, c = at & 3;
@@ -163,11 +238,11 @@ void for_type(int dtype, F &&f)
         f(std::false_type{});
 }
 
-// Workgroups of 256 lanes for one lane per packed word, up to 16 per CU.
+// Workgroups of 256 lanes for one lane per packed word, up to 32 per CU.
 unsigned word_grid(int64_t N, int64_t K)
 {
     const int64_t wgs = cdiv(N * cdiv(K, 128) * 16, 256);
-    return (unsigned)(wgs < 4096 ? wgs : 4096);
+    return (unsigned)(wgs < 8192 ? wgs : 8192);
 }
 
 // Shared by the two directions; W is written where dequantize is set.
@@ -192,6 +267,9 @@ int convert(const void *W, const void *Q, const void *S, const void *Z, int64_t 
     if (N == 0 || K == 0)
         return GEMM_OK;
     const dim3 grid(word_grid(N, K));
+    const int64_t words = cdiv(K, 128) * 16, stride = (int64_t)grid.x * 256;
+    const int64_t step_rows = stride / words;
+    const int step_rest = (int)(stride % words);
     for_type(dtype, [&](auto bf) {
         with_group(group, [&](auto gs) {
             constexpr bool BF = decltype(bf)::value;
@@ -199,11 +277,11 @@ int convert(const void *W, const void *Q, const void *S, const void *Z, int64_t 
             if (dequantize)
                 hipLaunchKernelGGL((dequantize_kernel<BF, GS>), grid, dim3(256), 0, stream,
                                    (const uint32_t *)Q, (const uint16_t *)S, (const uint8_t *)Z,
-                                   (uint16_t *)W, N, (int)K, ldw);
+                                   (uint16_t *)W, N, (int)K, ldw, step_rows, step_rest);
             else
                 hipLaunchKernelGGL((quantize_kernel<BF, GS>), grid, dim3(256), 0, stream,
                                    (const uint16_t *)W, (uint32_t *)Q, (uint16_t *)S,
-                                   (uint8_t *)Z, N, (int)K, ldw);
+                                   (uint8_t *)Z, N, (int)K, ldw, step_rows, step_rest);
         });
     });
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ELAUNCH;

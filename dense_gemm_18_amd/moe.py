@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 
 from . import binding
-from .w4 import W4Weight, check_out, dtype_code, launch, row_stride
+from .w4 import W4Weight, check_out, dtype_code, launch, row_stride, stream_of
 
 
 class MoeLayer:
@@ -63,16 +63,16 @@ class MoeLayer:
         self._workspaces = {}
 
     def _workspace(self, stream):
-        """The address of a zero-filled workspace for calls on ``stream``."""
-        import torch
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        ws = self._workspaces.get(s.cuda_stream)
+        """(address of a zero-filled workspace for calls on ``stream``, the stream)."""
+        handle = stream_of(self.device, stream)
+        ws = self._workspaces.get(handle)
         if ws is None:
-            with torch.cuda.stream(s):
+            import torch
+            with torch.cuda.stream(stream), torch.cuda.device(self.device):
                 ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
                 if not torch.cuda.is_current_stream_capturing():
-                    self._workspaces[s.cuda_stream] = ws
-        return s, ws
+                    self._workspaces[handle] = ws
+        return ws.data_ptr(), handle
 
     def _check(self, X):
         if X.dim() != 2 or X.shape[1] != self.hidden:
@@ -84,10 +84,8 @@ class MoeLayer:
         return row_stride(X, "X")
 
     def _out(self, X, out):
-        import torch
         if out is None:
-            return torch.empty((X.shape[0], self.hidden), dtype=X.dtype, device=X.device), \
-                self.hidden
+            return X.new_empty(X.shape), self.hidden
         check_out(out, X.shape, X.dtype, X.device)
         return out, row_stride(out, "out")
 
@@ -104,20 +102,20 @@ class MoeLayer:
         ldx = self._check(X)
         out, ldd = self._out(X, out)
         ids, weights = self._slots(X)
-        s, ws = self._workspace(stream)
-        launch("moe_nt_layer", self.device, s,
+        ws, handle = self._workspace(stream)
+        launch("moe_nt_layer", self.device,
                (self._ref, X.data_ptr(), out.data_ptr(), ids.data_ptr(), weights.data_ptr(),
-                X.shape[0], ldx, ldd, self.topk, self._flags, ws.data_ptr(), self._ws_bytes))
+                X.shape[0], ldx, ldd, self.topk, self._flags, ws, self._ws_bytes, handle))
         return out, ids, weights
 
     def route(self, X, stream=None):
         """(ids, weights) of the tokens X, as the layer's call returns them."""
         ldx = self._check(X)
         ids, weights = self._slots(X)
-        s, ws = self._workspace(stream)
-        launch("moe_nt_route", self.device, s,
+        ws, handle = self._workspace(stream)
+        launch("moe_nt_route", self.device,
                (self._ref, X.data_ptr(), ids.data_ptr(), weights.data_ptr(), X.shape[0], ldx,
-                self.topk, self._flags, ws.data_ptr(), self._ws_bytes))
+                self.topk, self._flags, ws, self._ws_bytes, handle))
         return ids, weights
 
     def experts(self, X, ids, weights, out=None, stream=None):
@@ -131,8 +129,8 @@ class MoeLayer:
                 raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape "
                                  f"{(X.shape[0], self.topk)} on X's device")
         out, ldd = self._out(X, out)
-        s, ws = self._workspace(stream)
-        launch("moe_nt_experts", self.device, s,
+        ws, handle = self._workspace(stream)
+        launch("moe_nt_experts", self.device,
                (self._ref, X.data_ptr(), ids.data_ptr(), weights.data_ptr(), out.data_ptr(),
-                X.shape[0], ldx, ldd, self.topk, ws.data_ptr(), self._ws_bytes))
+                X.shape[0], ldx, ldd, self.topk, ws, self._ws_bytes, handle))
         return out

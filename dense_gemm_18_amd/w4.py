@@ -6,6 +6,8 @@ current stream of the tensors' device).
 """
 from __future__ import annotations
 
+import math
+
 from . import binding
 from .binding import GEMM_OK, GemmError
 
@@ -24,17 +26,25 @@ def dtype_code(dtype) -> int:
         raise TypeError(f"unsupported dtype {dtype}: float16 or bfloat16") from None
 
 
-def launch(name: str, device, stream, args) -> None:
-    """The raw entry point ``name`` with ``args`` and the stream, on ``device``."""
+def stream_of(device, stream) -> int:
+    """The raw handle of ``stream``, or of the device's current stream."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if stream is not None:
+        return stream.cuda_stream
+    # torch.cuda.current_stream would build an object around it: 2 us
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def launch(name: str, device, args) -> None:
+    """The raw entry point ``name`` with ``args`` on ``device``."""
+    import torch
     fn = getattr(binding.lib(), name)
     if device.index == torch.cuda.current_device():
-        rc = fn(*args, s.cuda_stream)
+        rc = fn(*args)
     else:
         # the library launches on the current device: make it the operands' one
         with torch.cuda.device(device):
-            rc = fn(*args, s.cuda_stream)
+            rc = fn(*args)
     if rc != GEMM_OK:
         raise GemmError(rc, name)
 
@@ -42,6 +52,8 @@ def launch(name: str, device, stream, args) -> None:
 def row_stride(x, what: str) -> int:
     """Elements between the rows of a 2-D tensor whose rows are dense."""
     rows, cols = x.shape
+    if x.is_contiguous():
+        return cols
     if cols > 1 and x.stride(1) != 1:
         raise ValueError(f"{what} must have dense rows")
     ld = x.stride(0) if rows > 1 else cols
@@ -71,7 +83,7 @@ class W4Weight:
         if len(shape) < 2:
             raise ValueError(f"shape {shape} is not [..., N, K]")
         K = shape[-1]
-        self.code = dtype_code(scales.dtype)
+        dtype_code(scales.dtype)
         want = {"q": (q, torch.int32, -(-K // 128) * 16),
                 "scales": (scales, scales.dtype, -(-K // group))}
         if zeros is not None:
@@ -82,12 +94,14 @@ class W4Weight:
                                  f"{shape[:-1] + (last,)}, not {x.dtype} {tuple(x.shape)}")
             if not x.is_contiguous() or not x.is_cuda or x.device != q.device:
                 raise ValueError(f"{name} must be contiguous, on the GPU of q")
+        self._hold(q, scales, zeros, shape, group)
+
+    def _hold(self, q, scales, zeros, shape, group):
         self.q, self.scales, self.zeros = q, scales, zeros
         self.shape, self.group = shape, group
         self.dtype, self.device = scales.dtype, q.device
-        self.N, self.K = 1, K
-        for n in shape[:-1]:
-            self.N *= n
+        self.code = dtype_code(scales.dtype)
+        self.N, self.K = math.prod(shape[:-1]), shape[-1]
         self.pointers = (q.data_ptr(), scales.data_ptr(),
                          zeros.data_ptr() if zeros is not None else None)
 
@@ -106,32 +120,33 @@ def quantize_w4(W, group: int = 128, zeros: bool = False, stream=None) -> W4Weig
         raise ValueError("W must be contiguous")
     if group not in (32, 64, 128):
         raise ValueError(f"group {group} is not 32, 64 or 128")
-    K = W.shape[-1]
-    ldw = row_stride(W, "W") if W.dim() == 2 else K
-    lead = tuple(W.shape[:-1])
-    w = W4Weight(torch.empty(lead + (-(-K // 128) * 16,), dtype=torch.int32, device=W.device),
-                 torch.empty(lead + (-(-K // group),), dtype=W.dtype, device=W.device),
-                 torch.empty(lead + (-(-K // group),), dtype=torch.uint8, device=W.device)
-                 if zeros else None, shape=W.shape, group=group)
+    shape = tuple(W.shape)
+    K, lead, device = shape[-1], shape[:-1], W.device
+    ldw = row_stride(W, "W") if len(shape) == 2 else K
+    groups = lead + (-(-K // group),)
+    w = W4Weight.__new__(W4Weight)
+    w._hold(torch.empty(lead + (-(-K // 128) * 16,), dtype=torch.int32, device=device),
+            W.new_empty(groups),
+            torch.empty(groups, dtype=torch.uint8, device=device) if zeros else None,
+            shape, group)
     q, s, z = w.pointers
-    launch("gemm_w4_quantize", W.device, stream,
-           (W.data_ptr(), q, s, z, w.N, K, ldw, group, code))
+    launch("gemm_w4_quantize", device, (W.data_ptr(), q, s, z, w.N, K, ldw, group, code,
+                                        stream_of(device, stream)))
     return w
 
 
 def dequantize_w4(w: W4Weight, out=None, stream=None):
     """The values of ``w``, rounded to its 16-bit type, in its shape.  ``out``
     (optional): 2-D with a row stride, or contiguous."""
-    import torch
     if out is None:
-        out = torch.empty(w.shape, dtype=w.dtype, device=w.device)
+        out = w.scales.new_empty(w.shape)
     else:
         check_out(out, w.shape, w.dtype, w.device)
         if out.dim() > 2 and not out.is_contiguous():
             raise ValueError("out must be contiguous")
     ldw = row_stride(out, "out") if out.dim() == 2 else w.K
-    launch("gemm_w4_dequantize", w.device, stream,
-           (*w.pointers, out.data_ptr(), w.N, w.K, ldw, w.group, w.code))
+    launch("gemm_w4_dequantize", w.device, (*w.pointers, out.data_ptr(), w.N, w.K, ldw, w.group,
+                                            w.code, stream_of(w.device, stream)))
     return out
 
 
@@ -142,29 +157,30 @@ def gemm_nt_w4(A, w: W4Weight, out=None, stream=None, workspace=None):
     a contiguous uint8 tensor for the unpacked weight of large M, allocated here where
     it is needed and none is given."""
     import torch
-    if len(w.shape) != 2 or A.dim() != 2 or A.shape[1] != w.K:
+    N, K, device = w.N, w.K, w.device
+    if len(w.shape) != 2 or A.dim() != 2 or A.shape[1] != K:
         raise ValueError(f"shapes {tuple(A.shape)} and {w.shape} are not [M, K] and [N, K]")
     if A.dtype != w.dtype:
         raise TypeError(f"A is {A.dtype}, the weight's scales are {w.dtype}")
-    if A.device != w.device:
+    if A.device != device:
         raise ValueError("A and the weight must be on the same GPU")
-    M, N = A.shape[0], w.N
+    M = A.shape[0]
     lda = row_stride(A, "A")
     if out is None:
-        out = torch.empty((M, N), dtype=A.dtype, device=A.device)
-        ldd = N
+        out, ldd = A.new_empty((M, N)), N
     else:
-        check_out(out, (M, N), A.dtype, A.device)
+        check_out(out, (M, N), A.dtype, device)
         ldd = row_stride(out, "out")
+    ws = ws_bytes = 0
     if workspace is None:
-        need = binding.gemm_nt_w4_ws_size(M, N, w.K) if lda == w.K and ldd == N else 0
+        need = binding.lib().gemm_nt_w4_ws_size(M, N, K) if lda == K and ldd == N else 0
         if need:
             with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=A.device)
-    elif not workspace.is_cuda or workspace.device != A.device or not workspace.is_contiguous():
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on A's device")
-    ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
-        if workspace is not None else (None, 0)
-    launch("gemm_nt_w4", A.device, stream,
-           (A.data_ptr(), *w.pointers, out.data_ptr(), M, N, w.K, lda, ldd, w.group, w.code, *ws))
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    launch("gemm_nt_w4", device, (A.data_ptr(), *w.pointers, out.data_ptr(), M, N, K, lda, ldd,
+                                  w.group, w.code, ws, ws_bytes, stream_of(device, stream)))
     return out
