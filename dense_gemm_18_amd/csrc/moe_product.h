@@ -338,13 +338,14 @@ __global__ void __launch_bounds__(kRouteWaves * 64) moe_route_kernel(MoeArgs p)
         choose<PER, kTokens>(v, p, base, kRouteWaves, ids);
     }
     __syncthreads();
-    if (p.plan)
+    if (p.plan && p.T > 1)
         make_plan(p.plan, p.T * p.topk, p.E, cnt, [&](int i) { return ids[i]; });
 }
 
 // ---- experts ------------------------------------------------------------
 
 constexpr int kMoeWaves = 8;
+constexpr int64_t kOneLds = 96 * 1024;   // of the one-token down product, at most
 
 // Waves along K and blocks of 16 hidden rows to a wave of the down product,
 // whose K, the inner size, is short.
@@ -359,8 +360,8 @@ template <bool BF, int GS, int MB>
 using DownCore = Skinny<BF, GS, 2, MB, kDownWaves<GS>, kMoeWaves / kDownWaves<GS>, true>;
 
 // h = silu(gate) * up for 16 of an expert's inner rows and all its slots.
-// One workgroup takes the 16 gate rows and their 16 up rows, eight waves
-// split the hidden size.
+// One workgroup takes the 16 gate rows and their 16 up rows, its waves split
+// the hidden size.
 template <bool BF, int GS, int MB>
 __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel(MoeArgs p)
 {
@@ -368,7 +369,14 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
     const int blocks = (p.I + 15) / 16;
     const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
     const int s = wg / blocks, i0 = wg % blocks * 16;
-    const Plan::Item it = p.plan->item[s];
+    Plan::Item it;
+    if (p.T == 1) {              // a slot is an expert: no plan
+        it.expert = p.ids[s];
+        it.first = it.slot = s;
+        it.count = (uint32_t)it.expert < (uint32_t)p.E;
+    } else {
+        it = p.plan->item[s];
+    }
     const int64_t e = it.expert;
     for (int c0 = 0; c0 < it.count; c0 += 16 * MB) {
         const int count = min(16 * MB, it.count - c0);
@@ -449,6 +457,127 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_down_kern
     }
 }
 
+// One token: its slots' products are one long product, of the experts' rows
+// side by side with the gated rows end to end.  A workgroup takes 16 hidden
+// rows of every chosen expert, its waves share the (expert, piece of inner)
+// pairs, and the weighted sum is their join: nothing passes through memory.
+template <bool BF, int GS>
+using OneCore = Skinny<BF, GS, 1, 1, kMoeWaves, 1, true>;
+
+template <bool BF, int GS>
+__global__ void __launch_bounds__(kMoeWaves * 64, 4) moe_down_one_kernel(MoeArgs p)
+{
+    extern __shared__ f32x4 lds[];
+    using Core = OneCore<BF, GS>;
+    const int h0 = blockIdx.x * 16, steps = (p.I + 127) >> 7;
+    Core c;
+    c.W = p.w2;
+    c.K = p.I;
+    c.rows[0] = p.H - h0;
+    auto bind = [&](int j) {
+        const int e = p.ids[j];
+        c.row[0] = (int64_t)((uint32_t)e < (uint32_t)p.E ? e : 0) * p.H + h0;
+        c.M = 1;
+        c.begin((char *)lds, p.h, (uint32_t)p.topk * (uint32_t)p.I * 2u);
+        return (uint32_t)e < (uint32_t)p.E;
+    };
+    // the gated rows, then each expert's scales
+    bind(0);
+    c.M = p.topk;
+    c.chunk = steps * 128;
+    c.astride = c.chunk * 2 + 16;
+    c.sstride = steps * Core::kGroups + 1;
+    c.stage_acts(0, steps, [&](int m) { return (uint32_t)m * (uint32_t)p.I * 2u; });
+    uint32_t *scales = (uint32_t *)((char *)lds + p.topk * c.astride);
+    if constexpr (GS != 0) {
+        // 16 threads along the groups of a row, the rest along the rows of all
+        // experts; four rows' loads at once, from a valid place where there is
+        // nothing to load
+        const int G = (p.I + GS - 1) / GS, groups = steps * Core::kGroups;
+        for (int g0 = threadIdx.x & 15; g0 < groups; g0 += 16)
+            for (int n0 = threadIdx.x >> 4; n0 < p.topk * 16; n0 += 4 * 32) {
+                uint32_t s[4], z[4];
+                bool in[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n = n0 + 32 * i, e = n < p.topk * 16 ? p.ids[n >> 4] : -1;
+                    in[i] = (uint32_t)e < (uint32_t)p.E && g0 < G && h0 + (n & 15) < p.H;
+                    const int64_t at =
+                        in[i] ? ((int64_t)e * p.H + h0 + (n & 15)) * G + g0 : 0;
+                    s[i] = p.w2.s[at];
+                    z[i] = p.w2.z ? p.w2.z[at] & 15 : 8;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n0 + 32 * i < p.topk * 16)
+                        scales[(n0 + 32 * i) * c.sstride + g0] =
+                            (in[i] ? s[i] : 0) | ((BF ? 0x4300u : 0x6400u) + z[i]) << 16;
+            }
+    }
+    __syncthreads();
+
+    const int units = p.topk * p.parts;
+    f32x4 sum[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
+    for (int u = c.wave; u < units; u += kMoeWaves) {
+        const int j = u / p.parts, part = u % p.parts;
+        if (!bind(j))
+            continue;
+        c.astride = steps * 256 + 16;
+        c.sstride = steps * Core::kGroups + 1;
+        const char *acts = (const char *)lds + j * c.astride;
+        const uint32_t *sc = scales + j * 16 * c.sstride;
+        const int first = part * steps / p.parts, last = (part + 1) * steps / p.parts;
+        auto walk = [&](auto exact, f32x4 (&to)[1][1]) G18_INLINE {
+            typename Core::template Batch<Core::U> b;
+#pragma nounroll
+            for (int st = first; st < last; st += Core::U) {
+                c.load(b, st, last);
+#pragma unroll
+                for (int k = 0; k < Core::U; ++k)
+                    if (st + k < last)
+                        c.template consume<decltype(exact)::value>(b, k, st + k, 0, acts, sc, to);
+            }
+        };
+        walk(std::false_type{}, c.acc);
+        if constexpr (BF && GS != 0) {
+            // as Skinny::finish, for this wave alone
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                odd |= !Core::finite(c.acc[0][0][e]);
+            if (__any(odd)) {
+                f32x4 again[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
+                walk(std::true_type{}, again);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!Core::finite(c.acc[0][0][e]))
+                        c.acc[0][0][e] = again[0][0][e] * 0x1p12f;
+            }
+        }
+        const float w = p.weights[j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            sum[0][0][e] = __builtin_fmaf(w, c.acc[0][0][e], sum[0][0][e]);
+    }
+    c.M = 1;
+    c.acc[0][0] = sum[0][0];
+    c.join([&](int, int i, const float(&v)[1]) {
+        if (h0 + i < p.H)
+            p.D[h0 + i] = from_float<BF>(v[0]);
+    });
+}
+
+// LDS of that kernel, in bytes.
+template <bool BF, int GS>
+int64_t one_bytes(int topk, int I)
+{
+    const int64_t steps = cdiv(I, 128);
+    const int64_t need =
+        topk * (steps * 256 + 16 +
+                (GS ? 16 * 4 * (steps * OneCore<BF, GS>::kGroups + 1) : 0));
+    return need > kMoeWaves * 1024 ? need : kMoeWaves * 1024;
+}
+
 template <bool BF, int PER>
 void launch_route_per(const MoeArgs &p, hipStream_t stream)
 {
@@ -474,16 +603,31 @@ template <bool BF>
 void launch_experts(const MoeArgs &p, int group, bool planned, hipStream_t stream)
 {
     const int n = p.T * p.topk, most = p.E < n ? p.E : n;
-    if (!planned)
+    // workgroups for every item of the plan; one token has none, its slots may
+    // name an expert twice
+    const int slots = p.T == 1 ? n : most;
+    if (!planned && p.T > 1)
         hipLaunchKernelGGL((moe_plan_kernel<>), dim3(1), dim3(kMoeSlots), 0, stream, p);
     with_group(group, [&](auto gs) {
         constexpr int GS = decltype(gs)::value;
         auto go = [&](auto mbs) {
             constexpr int MB = decltype(mbs)::value;
             const int rows = n < 16 * MB ? n : 16 * MB;
-            hipLaunchKernelGGL((moe_up_kernel<BF, GS, MB>), tile_grid(most * cdiv(p.I, 16)),
-                               dim3(kMoeWaves * 64), (UpCore<BF, GS, MB>::lds_bytes(rows, p.H)),
-                               stream, p);
+            hipLaunchKernelGGL((moe_up_kernel<BF, GS, MB>), tile_grid(slots * cdiv(p.I, 16)),
+                               dim3(kMoeWaves * 64),
+                               (UpCore<BF, GS, MB>::lds_bytes(rows, p.H)), stream, p);
+            const int64_t one = one_bytes<BF, GS>(p.topk, p.I);
+            if (p.T == 1 && one <= kOneLds) {
+                // as many pairs as make all waves' work alike
+                MoeArgs q = p;
+                q.parts = p.topk % 8 == 0 ? 1 : p.topk % 4 == 0 ? 2 : p.topk % 2 == 0 ? 4 : 8;
+                hipLaunchKernelGGL((moe_down_one_kernel<BF, GS>),
+                                   dim3((unsigned)cdiv(p.H, 16)), dim3(kMoeWaves * 64), (int)one,
+                                   stream, q);
+                return;
+            }
+            if (p.T == 1)
+                hipLaunchKernelGGL((moe_plan_kernel<>), dim3(1), dim3(kMoeSlots), 0, stream, p);
             hipLaunchKernelGGL((moe_down_kernel<BF, GS, MB>),
                                tile_grid(most * cdiv(p.H, kDownRows<GS>)), dim3(kMoeWaves * 64),
                                (DownCore<BF, GS, MB>::lds_bytes(rows, p.I)), stream, p);
