@@ -564,18 +564,27 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
         uint32_t s[NS], z[NS];
     };
 
-    // What the thread stages of the chunk from k0 on (nothing from K on).
-    template <class F>
-    __device__ __forceinline__ void fetch(Next &x, int k0, F &&at) const
+    // The thread's pieces lie in one column, kRowStep rows apart: offsets into
+    // memory and LDS differ by constants.
+    static constexpr int kRowStep = kThreads / (CS * 16);
+    static_assert(kThreads % (CS * 16) == 0, "one column");
+    uint32_t row_bytes;             // between activation rows
+
+    __device__ __forceinline__ int column() const { return threadIdx.x % (CS * 16); }
+    __device__ __forceinline__ int first_row() const { return threadIdx.x / (CS * 16); }
+
+    // What the thread stages of the chunk from k0 on (nothing from K on; rows
+    // from M on are past the activations' range).
+    __device__ __forceinline__ void fetch(Next &x, int k0) const
     {
         const int K = this->K, G = this->G;
+        // all of the column's 8 elements, or what mend_chunk fetches
+        const bool in = k0 + column() * 8 + 8 <= K;
+        const uint32_t o =
+            in ? first_row() * row_bytes + (uint32_t)(k0 + column() * 8) * 2u : kOob;
 #pragma unroll
-        for (int i = 0; i < NA; ++i) {
-            const int idx = i * kThreads + threadIdx.x, m = idx / (CS * 16);
-            const int k = k0 + idx % (CS * 16) * 8;
-            x.a[i] = load_b128(this->ar,
-                               m < this->M && k + 8 <= K ? at(m) + 2u * (uint32_t)k : kOob);
-        }
+        for (int i = 0; i < NA; ++i)
+            x.a[i] = load_b128(this->ar, o + (uint32_t)(i * kRowStep) * row_bytes);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int idx = i * kThreads + threadIdx.x, n = idx / (CS * kGroups);
@@ -587,18 +596,12 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
         }
     }
 
-    template <class F>
-    __device__ __forceinline__ void store(const Next &x, int k0, char *buf, F &&at) const
+    __device__ __forceinline__ void store(const Next &x, int k0, char *buf) const
     {
-        const int K = this->K;
+        char *p = buf + first_row() * kStride + column() * 16;
 #pragma unroll
-        for (int i = 0; i < NA; ++i) {
-            const int idx = i * kThreads + threadIdx.x;
-            const int m = idx / (CS * 16), c = idx % (CS * 16), k = k0 + c * 8;
-            // the 8 elements that K ends among come below
-            if (k + 8 <= K || k >= K)
-                *(u32x4 *)(buf + m * kStride + c * 16) = x.a[i];
-        }
+        for (int i = 0; i < NA; ++i)
+            *(u32x4 *)(p + i * kRowStep * kStride) = x.a[i];
         uint32_t *scales = (uint32_t *)(buf + kActs);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
@@ -608,38 +611,41 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
                 scales[n * kScales + g] =
                     x.s[i] | ((BF ? 0x4300u : 0x6400u) + ((x.z[i] | this->zdef) & 15u)) << 16;
         }
+        // the 8 elements that K ends among, of which `fetch` left zeros
+        const int K = this->K;
         if ((K & 7) && k0 <= K && k0 + CS * 128 > K) {
+            __syncthreads();
             const int k = (K & ~7) + (threadIdx.x & 7);
             for (int m = threadIdx.x >> 3; m < 16 * MB; m += kThreads / 8)
                 *(uint16_t *)(buf + m * kStride + (k - k0) * 2) =
                     (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                        this->ar, m < this->M && k < K ? at(m) + 2u * k : kOob, 0, 0);
+                        this->ar, k < K ? m * row_bytes + 2u * k : kOob, 0, 0);
         }
     }
 
-    template <bool EXACT, class F>
-    __device__ __forceinline__ void walk(f32x4 (&to)[RB][MB], F &&at)
+    template <bool EXACT>
+    __device__ __forceinline__ void walk(f32x4 (&to)[RB][MB])
     {
         const int total = (this->K + 127) >> 7, mine = this->kw() * kSteps;
         typename Base::template Batch<kSteps> now, ahead;
         Next x;
         if (EXACT)
             __syncthreads();
-        fetch(x, 0, at);
+        fetch(x, 0);
         this->load(now, mine, total);
-        store(x, 0, this->lds, at);
+        store(x, 0, this->lds);
         __syncthreads();
         char *buf = this->lds, *other = this->lds + kBuffer;
 #pragma nounroll
         for (int s0 = 0; s0 < total; s0 += CS) {
-            fetch(x, (s0 + CS) * 128, at);
+            fetch(x, (s0 + CS) * 128);
             this->load(ahead, s0 + CS + mine, total);
 #pragma unroll
             for (int u = 0; u < kSteps; ++u)
                 if (s0 + mine + u < total)
                     this->template consume<EXACT>(now, u, mine + u, s0 * 128, buf,
                                                   (const uint32_t *)(buf + kActs), to);
-            store(x, (s0 + CS) * 128, other, at);
+            store(x, (s0 + CS) * 128, other);
             __syncthreads();
             char *t = buf;
             buf = other;
@@ -648,13 +654,15 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
         }
     }
 
+    // `at(m)` is m times at(1) here.
     template <class F>
     __device__ __forceinline__ void run(F &&at)
     {
+        row_bytes = at(1);
         this->astride = kStride;
         this->sstride = kScales;
         this->finish([&](auto exact, f32x4 (&to)[RB][MB])
-                         G18_INLINE { walk<decltype(exact)::value>(to, at); });
+                         G18_INLINE { walk<decltype(exact)::value>(to); });
     }
 };
 
