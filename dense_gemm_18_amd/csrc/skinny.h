@@ -578,7 +578,7 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
     __device__ __forceinline__ void fetch(Next &x, int k0) const
     {
         const int K = this->K, G = this->G;
-        // all of the column's 8 elements, or what mend_chunk fetches
+        // all of the column's 8 elements; `store` fetches those that K ends among
         const bool in = k0 + column() * 8 + 8 <= K;
         const uint32_t o =
             in ? first_row() * row_bytes + (uint32_t)(k0 + column() * 8) * 2u : kOob;
@@ -627,30 +627,34 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
     __device__ __forceinline__ void walk(f32x4 (&to)[RB][MB])
     {
         const int total = (this->K + 127) >> 7, mine = this->kw() * kSteps;
-        typename Base::template Batch<kSteps> now, ahead;
+        typename Base::template Batch<kSteps> even, odd;
         Next x;
         if (EXACT)
             __syncthreads();
         fetch(x, 0);
-        this->load(now, mine, total);
+        this->load(even, mine, total);
+        this->load(odd, CS + mine, total);
         store(x, 0, this->lds);
+        fetch(x, CS * 128);
         __syncthreads();
-        char *buf = this->lds, *other = this->lds + kBuffer;
-#pragma nounroll
-        for (int s0 = 0; s0 < total; s0 += CS) {
-            fetch(x, (s0 + CS) * 128);
-            this->load(ahead, s0 + CS + mine, total);
+        // The chunk from step s0 on, whose weights are in b and whose activations
+        // are in `buf`.  Two copies of this make the loop: a copy of registers
+        // that a load is still to fill would wait for it.
+        auto chunk = [&](auto &b, int s0, char *buf, char *other) G18_INLINE {
+            store(x, (s0 + CS) * 128, other);
+            fetch(x, (s0 + 2 * CS) * 128);
 #pragma unroll
             for (int u = 0; u < kSteps; ++u)
                 if (s0 + mine + u < total)
-                    this->template consume<EXACT>(now, u, mine + u, s0 * 128, buf,
+                    this->template consume<EXACT>(b, u, mine + u, s0 * 128, buf,
                                                   (const uint32_t *)(buf + kActs), to);
-            store(x, (s0 + CS) * 128, other);
+            this->load(b, s0 + 2 * CS + mine, total);
             __syncthreads();
-            char *t = buf;
-            buf = other;
-            other = t;
-            now = ahead;
+        };
+#pragma nounroll
+        for (int s0 = 0; s0 < total; s0 += 2 * CS) {
+            chunk(even, s0, this->lds, this->lds + kBuffer);
+            chunk(odd, s0 + CS, this->lds + kBuffer, this->lds);
         }
     }
 

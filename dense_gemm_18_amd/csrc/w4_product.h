@@ -75,31 +75,54 @@ void launch_w4_resident(const W4Args &a, hipStream_t stream)
     launch_w4_tile<BF, 1, Core>(a, Core::lds_bytes(a.M, a.K), stream);
 }
 
-template <bool BF, int GS, int RB, int MB, int KW, int CS>
+template <bool BF, int GS, int RB, int MB, int KW, int NW, int CS>
 void launch_w4_piped(const W4Args &a, hipStream_t stream)
 {
-    using Core = Piped<BF, GS, RB, MB, KW, kW4Waves / KW, CS>;
+    using Core = Piped<BF, GS, RB, MB, KW, NW, CS>;
     launch_w4_tile<BF, MB, Core>(a, Core::kLds, stream);
 }
 
+// Resident: activations within kActBytes, where no wave waits for another until
+// the end.  Otherwise the chunked core.  A tile's time hardly depends on how
+// many compute units have one, and larger tiles read the activations less
+// often: so each takes the largest tile that gives every compute unit one, and
+// the smallest if none does.  Measured at K = 8192, fp16, in us, by columns:
+//                         16384    8192    4096    1024
+//   16 rows, 16 x 64       17.5    15.4    15.0    13.4
+//            16 x 32       20.5    12.5    11.4    10.2
+//            16 x 16       26.5    14.9     9.6     8.1
+//   32 rows, 32 x 64       21.4    19.4    18.7
+//            32 x 32       25.3    17.8    14.9
+//   64 rows, 64 x 64       31.8    29.7    28.1    27.4
+//            32 x 64       35.1    21.6    19.5    17.9
+//            32 x 32       47.2    25.6    15.8    13.9
 template <bool BF>
 void launch_w4(const W4Args &a, int group, hipStream_t stream)
 {
+    const auto fills = [&](int rows, int columns) {
+        return cdiv(a.M, rows) * cdiv(a.N, columns) >= kCUs;
+    };
     with_group(group, [&](auto gs) {
         constexpr int GS = decltype(gs)::value ? decltype(gs)::value : 128;
         if (a.M <= 16 && (int64_t)a.M * (cdiv(a.K, 128) * 256 + 16) <= kActBytes) {
-            if (a.N >= 64 * kCUs)
+            if (fills(16, 64))
                 launch_w4_resident<BF, GS, 4>(a, stream);
-            else if (a.N >= 32 * kCUs)
+            else if (fills(16, 32))
                 launch_w4_resident<BF, GS, 2>(a, stream);
             else
                 launch_w4_resident<BF, GS, 1>(a, stream);
-        } else if (a.M <= 16) {
-            launch_w4_piped<BF, GS, 2, 1, 8, 8>(a, stream);
-        } else if (a.M <= 32) {
-            launch_w4_piped<BF, GS, 2, 2, 4, 4>(a, stream);
+        } else if (a.M <= 16 && fills(16, 64)) {
+            launch_w4_piped<BF, GS, 2, 1, 8, 2, 8>(a, stream);
+        } else if (a.M <= 16 && fills(16, 32)) {
+            launch_w4_piped<BF, GS, 2, 1, 8, 1, 8>(a, stream);
+        } else if (a.M > 32 && fills(64, 64)) {
+            launch_w4_piped<BF, GS, 2, 4, 4, 2, 4>(a, stream);
+        } else if (a.M > 16 && fills(32, 64)) {
+            launch_w4_piped<BF, GS, 2, 2, 4, 2, 4>(a, stream);
+        } else if (a.M > 16 && fills(32, 32)) {
+            launch_w4_piped<BF, GS, 1, 2, 4, 2, 4>(a, stream);
         } else {
-            launch_w4_piped<BF, GS, 2, 4, 4, 4>(a, stream);
+            launch_w4_piped<BF, GS, 1, 1, 8, 1, 8>(a, stream);
         }
     });
 }
