@@ -100,8 +100,11 @@ int gemm_nt_w4(const void *A, const void *Q, const void *S, const void *Z, void 
 
 #define GEMM_W4_MAX_LDA 16777215
 
-/* Rows up to which gemm_nt_w4 never uses a workspace. */
-#define GEMM_W4_DIRECT_M 256
+/* Rows up to which gemm_nt_w4 never uses a workspace.  Unpacking first took 206,
+ * 79 and 59 us at 384 rows and 16384, 8192 and 4096 columns of 8192 (fp16),
+ * unpacking on the way 181, 83 and 55; at 512 rows 201, 86 and 61 against 220,
+ * 110 and 55. */
+#define GEMM_W4_DIRECT_M 384
 
 /* Host-only: bytes of workspace gemm_nt_w4 can use for these sizes with
  * dense A and D (0: none, or sizes out of range). */

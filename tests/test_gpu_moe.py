@@ -295,3 +295,59 @@ def test_streams_and_graph_replays(group):
         torch.cuda.synchronize()
         assert torch.equal(bits(out), bits(eager[0])) and torch.equal(ids, eager[1]), i
         assert torch.equal(weights, eager[2]), i
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group", [0, 64])
+def test_one_token_with_left_out_and_repeated_slots(group, dtype):
+    note(f"moe one token, slots, group {group} {dtype}")
+    c = Case(5, 6, 4, 260, 140, dtype, group)
+    X = c.tokens(1)
+    weights = torch.randn((1, 4), generator=c.gen, device=device())
+    for slots in ([0, -1, 5, 6], [3, 3, 3, 3], [2 ** 31 - 1, 1, 1, -2 ** 31], [-1, 6, 100, -5]):
+        ids = torch.tensor([slots], dtype=torch.int32, device=device())
+        y = c.layer.experts(X, ids, weights)
+        c.check_y(X, ids, weights, y)
+        left = (ids < 0) | (ids >= 6)
+        odd = weights.masked_fill(left, float("nan"))
+        assert torch.equal(bits(c.layer.experts(X, ids, odd)), bits(y))
+        if bool(left.all()):
+            assert bool((bits(y) == 0).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,E,topk,H,I,group", [
+    (1, 16, 16, 70, 3100, 0), (1, 16, 16, 70, 3100, 128),       # rows of h past one LDS
+    (64, 2, 1, 4200, 70, 0), (64, 2, 1, 4200, 70, 32),          # activations in chunks
+    (40, 3, 2, 100, 2500, 0), (40, 3, 2, 100, 2500, 64),
+    (9, 2, 2, 4500, 3000, 0), (9, 2, 2, 4500, 3000, 128),
+    (12, 200, 7, 130, 40, 0), (12, 600, 12, 130, 40, 32)])
+def test_long_rows_and_many_experts(T, E, topk, H, I, group, dtype):
+    note(f"moe T{T} E{E} k{topk} H{H} I{I} group {group} {dtype}")
+    c = Case(T + E + H, E, topk, H, I, dtype, group, zeros=True)
+    X = c.tokens(T)
+    y, ids, weights = c.layer(X)
+    torch.cuda.synchronize()
+    c.check_route(X, ids, weights)
+    c.check_y(X, ids, weights, y)
+    assert torch.equal(bits(c.layer(X)[0]), bits(y))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("T", [1, 4, 40])
+def test_infinities_stay_in_their_token(T, group, dtype):
+    note(f"moe infinities T{T} group {group} {dtype}")
+    c = Case(7, 4, 2, 260, 140, dtype, group)
+    X = c.tokens(T)
+    ids = (torch.arange(2 * T, device=device()).view(T, 2) % 4).to(torch.int32)
+    weights = torch.rand((T, 2), generator=c.gen, device=device())
+    want = c.layer.experts(X, ids, weights)
+    for value in (float("inf"), float("-inf"), float("nan")):
+        B = X.clone()
+        B[T // 2, 137] = value
+        y = c.layer.experts(B, ids, weights)
+        other = torch.arange(T, device=device()) != T // 2
+        assert torch.equal(bits(y[other]), bits(want[other])), "another token changed"
+        # gates of both signs: silu has infinities and 0 * inf among its values
+        assert not bool(torch.isfinite(y[T // 2]).any())

@@ -301,3 +301,55 @@ def test_other_stream_and_graph_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, gemm_nt_w4(A, w)) and torch.equal(out_big, want_big), i
+
+
+# one shape for each tile that the product has, by the columns and rows that
+# choose it on 256 compute units; the rows' tails and the last columns are partial
+TILES = [(3, 16390, 300), (2, 8200, 333), (16, 16390, 2184), (13, 8200, 2700), (16, 4000, 4100),
+         (260, 1000, 515), (500, 1030, 387), (1030, 1000, 300)]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_every_tile(M, N, K, group, dtype):
+    note(f"w4 tiles {M}x{N}x{K} group {group} {dtype}")
+    for zeros in (False, True):
+        g = gen(M + N + K + group + zeros)
+        A = torch.randn((M, K), generator=g, device=device(), dtype=dtype)
+        Q, S, Z = w4_ref.random_weight(g, N, K, group, zeros, dtype)
+        # rows of D apart: many rows too are unpacked on the way
+        D = product(A, Q, S, Z, group, ldd_pad=2)
+        check(D, A, Q, S, Z, group)
+        if zeros:
+            continue
+        # an infinity, which bfloat16 takes through its second walk, stays in its row
+        B = A.clone()
+        B[M - 2, K - 3] = float("inf")
+        E = product(B, Q, S, Z, group, ldd_pad=2)
+        other = torch.arange(M, device=device()) != M - 2
+        assert torch.equal(bits(E[other]), bits(D[other])), "another row changed"
+        w = w4_ref.values(Q, S, Z, K, group)
+        ref = (B[M - 2].double() * w).sum(-1).to(dtype)
+        assert torch.equal(torch.isnan(E[M - 2]), torch.isnan(ref))
+        assert torch.equal(E[M - 2][torch.isinf(ref)], ref[torch.isinf(ref)])
+
+
+def test_quantize_ties_go_to_even():
+    # scales that are powers of two: W / s is an exact half-integer
+    for dtype in TYPES:
+        for zeros in (False, True):
+            note(f"quantize ties zeros {zeros} {dtype}")
+            halves = torch.arange(-14, 15, dtype=torch.float32) / 2         # -7 .. 7
+            W = torch.zeros((5, 64), dtype=dtype)
+            for i in range(5):
+                W[i, :29] = (halves * 2.0 ** (i - 3)).to(dtype)
+                W[i, 32] = (7.0 if not zeros else 15 - 7.0) * 2.0 ** (i - 3)
+            q, s, z = w4_ref.quantize(W, 64, zeros)
+            assert bool((s[:, 0].double() == 2.0 ** (torch.arange(5) - 3).double()).all())
+            w = quantize_w4(W.to(device()), group=64, zeros=zeros)
+            torch.cuda.synchronize()
+            assert torch.equal(w.scales.cpu(), s)
+            assert torch.equal(w4_ref.unpack(w.q.cpu(), 64), q)
+            if zeros:
+                assert torch.equal(w.zeros.cpu().to(torch.int64), z)

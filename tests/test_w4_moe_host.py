@@ -187,3 +187,20 @@ def test_limits_shared_with_the_headers():
     text = (root / "gemm_nt_w4.h").read_text() + (root / "moe_nt.h").read_text()
     for name in ("GEMM_T_F16", "GEMM_T_BF16", "MOE_RENORMALIZE"):
         assert f"#define {name} {getattr(binding, name)}" in text
+
+
+def test_row_lengths_past_the_limits_are_refused():
+    assert w4(M=0, A=0, D=0, lda=16777215) == OK
+    assert w4(M=0, A=0, D=0, lda=16777216) == BAD
+    assert w4(M=2, lda=16777216) == BAD
+    assert layer(T=0, ldx=16777215) == OK
+    assert layer(T=0, ldx=16777216) == BAD
+    assert layer(ldx=16777216) == BAD
+    assert layer(w=weights(inner=1048577)) == BAD
+    # (of 8 experts, the operands would overlap at these addresses)
+    assert layer(T=0, topk=1, w=weights(inner=1048576, experts=1)) == OK
+
+
+def test_workspace_of_the_product_starts_past_the_direct_rows():
+    assert binding.gemm_nt_w4_ws_size(384, 4096, 4096) == 0
+    assert binding.gemm_nt_w4_ws_size(385, 4096, 4096) == 4096 * 4096 * 2
