@@ -1625,6 +1625,7 @@ enum class Tile { kBig, kMid, kThin, kThinN, kThinM, kRect };
 // rather than 64 big ones, and 1024 x 1024 runs 256 thin tiles rather than
 // 64 mid ones (5.5 against 8.1 us at K = 1024).  The choice assumes operands
 // aligned to 16 bytes.
+//
 // thin_ok = false (FP8, whose 64 x 64 tile cost is not measured): the thin
 // tile only when M or N is at most 64.
 inline Tile choose_tile(int64_t M, int64_t N, int64_t K, bool thin_ok = true)

@@ -89,26 +89,23 @@ uint64_t scale_bytes(int64_t rows, int64_t cols, int group)
 }
 
 // What the two halves share: the activations, the workspace.
-int check_common(const moe_nt_weights *w, const void *X, int64_t T, int64_t ldx, int topk,
-                 const void *ws, int64_t ws_bytes, int64_t need)
+int check_common(const void *X, const void *ws, int64_t ws_bytes, int64_t need)
 {
-    if (ldx < w->hidden || ldx > MOE_MAX_LDX || !X || !aligned_to(X, 2))
-        return GEMM_EINVAL;
-    return !ws || !aligned_to(ws, 256) || ws_bytes < need ? GEMM_EINVAL : GEMM_OK;
+    return !X || !aligned_to(X, 2) || !ws || !aligned_to(ws, 256) || ws_bytes < need ? GEMM_EINVAL : GEMM_OK;
 }
 
 int check_route(const moe_nt_weights *w, const void *X, const int32_t *ids, const float *weights,
                 int64_t T, int64_t ldx, int topk, int flags, const void *ws, int64_t ws_bytes)
 {
-    if (!sizes_ok_moe(w, T, topk) || !inner_ok(w) || topk > w->experts || (flags & ~MOE_RENORMALIZE))
+    if (!sizes_ok_moe(w, T, topk) || !inner_ok(w) || topk > w->experts ||
+        (flags & ~MOE_RENORMALIZE) || ldx < w->hidden || ldx > MOE_MAX_LDX)
         return GEMM_EINVAL;
     if (T == 0)
         return GEMM_OK;
     if (!w->router || !aligned_to(w->router, 2) || !ids || !weights || !aligned_to(ids, 4) ||
         !aligned_to(weights, 4))
         return GEMM_EINVAL;
-    const int rc =
-        check_common(w, X, T, ldx, topk, ws, ws_bytes, layout_of(T, w, topk).bytes);
+    const int rc = check_common(X, ws, ws_bytes, layout_of(T, w, topk).bytes);
     if (rc != GEMM_OK)
         return rc;
     const uint64_t slots = (uint64_t)T * (uint64_t)topk * 4u;
@@ -123,12 +120,13 @@ int check_experts(const moe_nt_weights *w, const void *X, const int32_t *ids, co
                   const void *D, int64_t T, int64_t ldx, int64_t ldd, int topk, const void *ws,
                   int64_t ws_bytes)
 {
-    if (!sizes_ok_moe(w, T, topk) || !inner_ok(w))
+    if (!sizes_ok_moe(w, T, topk) || !inner_ok(w) || ldx < w->hidden || ldx > MOE_MAX_LDX ||
+        ldd < w->hidden || ldd > kMaxLd)
         return GEMM_EINVAL;
     if (T == 0)
         return GEMM_OK;
     if (!w->w13 || !w->w2 || !ids || !weights || !D || !aligned_to(D, 2) || !aligned_to(ids, 4) ||
-        !aligned_to(weights, 4) || ldd < w->hidden || ldd > kMaxLd)
+        !aligned_to(weights, 4))
         return GEMM_EINVAL;
     const uintptr_t wa = w->group ? 16 : 2;
     if (!aligned_to(w->w13, wa) || !aligned_to(w->w2, wa))
@@ -136,7 +134,7 @@ int check_experts(const moe_nt_weights *w, const void *X, const int32_t *ids, co
     if (w->group && (!w->w13_scales || !w->w2_scales || !aligned_to(w->w13_scales, 2) ||
                      !aligned_to(w->w2_scales, 2) || !w->w13_zeros != !w->w2_zeros))
         return GEMM_EINVAL;
-    const int rc = check_common(w, X, T, ldx, topk, ws, ws_bytes, moe_nt_ws_size(T, w, topk));
+    const int rc = check_common(X, ws, ws_bytes, moe_nt_ws_size(T, w, topk));
     if (rc != GEMM_OK)
         return rc;
     const int64_t n13 = w->experts * 2 * w->inner, n2 = w->experts * w->hidden;

@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 
 from . import binding
-from .w4 import W4Weight, check_out, dtype_code, launch, row_stride, stream_of
+from .w4 import W4Weight, check_out, dtype_code, launch, on_stream, row_stride, stream_of
 
 
 class MoeLayer:
@@ -18,9 +18,9 @@ class MoeLayer:
 
     Calls are enqueued on ``stream`` (default: the current stream of the weights'
     device).  The layer keeps one workspace for each stream it has been called on, so
-    calls on different streams may overlap.  A call that is being captured into a
-    graph on a stream that the layer has not run on takes a workspace of its own,
-    from the graph's memory."""
+    calls on different streams may overlap.  A call that is being captured takes a
+    workspace of its own from the graph's memory, and its zero fill becomes a part of
+    the graph: replays may run beside eager calls and other graphs."""
 
     def __init__(self, router, w13, w2, topk: int, renormalize: bool = True):
         packed = isinstance(w13, W4Weight)
@@ -62,17 +62,21 @@ class MoeLayer:
             raise ValueError(f"sizes E = {E}, H = {H}, I = {inner} are out of range")
         self._workspaces = {}
 
-    def _workspace(self, stream):
-        """(address of a zero-filled workspace for calls on ``stream``, the stream)."""
+    def _workspace(self, T, stream):
+        """(a zero-filled workspace for T tokens on ``stream``, its bytes, the stream).
+        The caller keeps the tensor until it has launched."""
+        import torch
         handle = stream_of(self.device, stream)
-        ws = self._workspaces.get(handle)
-        if ws is None:
-            import torch
-            with torch.cuda.stream(stream), torch.cuda.device(self.device):
-                ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
-                if not torch.cuda.is_current_stream_capturing():
-                    self._workspaces[handle] = ws
-        return ws.data_ptr(), handle
+        with on_stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                need = binding.moe_nt_ws_size(T, self._weights, self.topk)
+                return torch.zeros(need, dtype=torch.uint8, device=self.device), need, handle
+            ws = self._workspaces.get(handle)
+            if ws is None:
+                with torch.cuda.device(self.device):
+                    ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
+                self._workspaces[handle] = ws
+        return ws, self._ws_bytes, handle
 
     def _check(self, X):
         if X.dim() != 2 or X.shape[1] != self.hidden:
@@ -83,39 +87,41 @@ class MoeLayer:
             raise ValueError("X must be on the layer's GPU")
         return row_stride(X, "X")
 
-    def _out(self, X, out):
+    def _out(self, X, out, stream):
         if out is None:
-            return X.new_empty(X.shape), self.hidden
+            with on_stream(stream):
+                return X.new_empty(X.shape), self.hidden
         check_out(out, X.shape, X.dtype, X.device)
         return out, row_stride(out, "out")
 
-    def _slots(self, X):
+    def _slots(self, X, stream):
         import torch
         shape = (X.shape[0], self.topk)
-        return (torch.empty(shape, dtype=torch.int32, device=X.device),
-                torch.empty(shape, dtype=torch.float32, device=X.device))
+        with on_stream(stream):
+            return (torch.empty(shape, dtype=torch.int32, device=X.device),
+                    torch.empty(shape, dtype=torch.float32, device=X.device))
 
     def __call__(self, X, out=None, stream=None):
         """(y, ids, weights) for the tokens X [T, H]: y [T, H] in X's type, the chosen
         experts ids [T, topk] (int32) and their weights [T, topk] (float32).  X and
         ``out`` may have a row stride."""
         ldx = self._check(X)
-        out, ldd = self._out(X, out)
-        ids, weights = self._slots(X)
-        ws, handle = self._workspace(stream)
+        out, ldd = self._out(X, out, stream)
+        ids, weights = self._slots(X, stream)
+        ws, ws_bytes, handle = self._workspace(X.shape[0], stream)
         launch("moe_nt_layer", self.device,
                (self._ref, X.data_ptr(), out.data_ptr(), ids.data_ptr(), weights.data_ptr(),
-                X.shape[0], ldx, ldd, self.topk, self._flags, ws, self._ws_bytes, handle))
+                X.shape[0], ldx, ldd, self.topk, self._flags, ws.data_ptr(), ws_bytes, handle))
         return out, ids, weights
 
     def route(self, X, stream=None):
         """(ids, weights) of the tokens X, as the layer's call returns them."""
         ldx = self._check(X)
-        ids, weights = self._slots(X)
-        ws, handle = self._workspace(stream)
+        ids, weights = self._slots(X, stream)
+        ws, ws_bytes, handle = self._workspace(X.shape[0], stream)
         launch("moe_nt_route", self.device,
                (self._ref, X.data_ptr(), ids.data_ptr(), weights.data_ptr(), X.shape[0], ldx,
-                self.topk, self._flags, ws, self._ws_bytes, handle))
+                self.topk, self._flags, ws.data_ptr(), ws_bytes, handle))
         return ids, weights
 
     def experts(self, X, ids, weights, out=None, stream=None):
@@ -128,9 +134,9 @@ class MoeLayer:
                     or not x.is_contiguous() or x.device != X.device:
                 raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape "
                                  f"{(X.shape[0], self.topk)} on X's device")
-        out, ldd = self._out(X, out)
-        ws, handle = self._workspace(stream)
+        out, ldd = self._out(X, out, stream)
+        ws, ws_bytes, handle = self._workspace(X.shape[0], stream)
         launch("moe_nt_experts", self.device,
                (self._ref, X.data_ptr(), ids.data_ptr(), weights.data_ptr(), out.data_ptr(),
-                X.shape[0], ldx, ldd, self.topk, ws, self._ws_bytes, handle))
+                X.shape[0], ldx, ldd, self.topk, ws.data_ptr(), ws_bytes, handle))
         return out

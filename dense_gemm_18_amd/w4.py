@@ -2,11 +2,12 @@
 
 Over the C ABI of ``include/gemm_nt_w4.h``, which defines the packed layout,
 the rounding and the limits.  A call is enqueued on ``stream`` (default: the
-current stream of the tensors' device).
+current stream of the tensors' device); tensors that it makes are that stream's.
 """
 from __future__ import annotations
 
 import math
+from contextlib import nullcontext
 
 from . import binding
 from .binding import GEMM_OK, GemmError
@@ -33,6 +34,15 @@ def stream_of(device, stream) -> int:
         return stream.cuda_stream
     # torch.cuda.current_stream would build an object around it: 2 us
     return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def on_stream(stream):
+    """Allocations inside are ``stream``'s: the memory of a tensor made for another
+    stream may still be in use on this one."""
+    if stream is None:
+        return nullcontext()
+    import torch
+    return torch.cuda.stream(stream)
 
 
 def launch(name: str, device, args) -> None:
@@ -125,10 +135,11 @@ def quantize_w4(W, group: int = 128, zeros: bool = False, stream=None) -> W4Weig
     ldw = row_stride(W, "W") if len(shape) == 2 else K
     groups = lead + (-(-K // group),)
     w = W4Weight.__new__(W4Weight)
-    w._hold(torch.empty(lead + (-(-K // 128) * 16,), dtype=torch.int32, device=device),
-            W.new_empty(groups),
-            torch.empty(groups, dtype=torch.uint8, device=device) if zeros else None,
-            shape, group)
+    with on_stream(stream):
+        w._hold(torch.empty(lead + (-(-K // 128) * 16,), dtype=torch.int32, device=device),
+                W.new_empty(groups),
+                torch.empty(groups, dtype=torch.uint8, device=device) if zeros else None,
+                shape, group)
     q, s, z = w.pointers
     launch("gemm_w4_quantize", device, (W.data_ptr(), q, s, z, w.N, K, ldw, group, code,
                                         stream_of(device, stream)))
@@ -139,7 +150,8 @@ def dequantize_w4(w: W4Weight, out=None, stream=None):
     """The values of ``w``, rounded to its 16-bit type, in its shape.  ``out``
     (optional): 2-D with a row stride, or contiguous."""
     if out is None:
-        out = w.scales.new_empty(w.shape)
+        with on_stream(stream):
+            out = w.scales.new_empty(w.shape)
     else:
         check_out(out, w.shape, w.dtype, w.device)
         if out.dim() > 2 and not out.is_contiguous():
@@ -167,7 +179,8 @@ def gemm_nt_w4(A, w: W4Weight, out=None, stream=None, workspace=None):
     M = A.shape[0]
     lda = row_stride(A, "A")
     if out is None:
-        out, ldd = A.new_empty((M, N)), N
+        with on_stream(stream):
+            out, ldd = A.new_empty((M, N)), N
     else:
         check_out(out, (M, N), A.dtype, device)
         ldd = row_stride(out, "out")
@@ -175,7 +188,7 @@ def gemm_nt_w4(A, w: W4Weight, out=None, stream=None, workspace=None):
     if workspace is None:
         need = binding.lib().gemm_nt_w4_ws_size(M, N, K) if lda == K and ldd == N else 0
         if need:
-            with torch.cuda.stream(stream):
+            with on_stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on A's device")

@@ -51,12 +51,11 @@ typedef struct moe_nt_weights {
 
 /*
  * Router: ids[t*topk + j] (int32) and weights[t*topk + j] (fp32) of the T
- * rows of X, row t at X + t * ldx elements (hidden <= ldx <=
- * MOE_MAX_LDX).  The logits are
- * summed in fp32.  A row with a NaN logit, or whose largest is infinite, gets
- * NaN weights and topk distinct valid ids.  topk in [1, min(experts, MOE_MAX_TOPK)].
- * Of *w the sizes, group and dtype have to be valid, and router; w13, w2 and
- * their scales and zeros are not used.
+ * rows of X, row t at X + t * ldx elements (hidden <= ldx <= MOE_MAX_LDX).
+ * The logits are summed in fp32.  A row with a NaN logit, or whose largest is
+ * infinite, gets NaN weights and topk distinct valid ids.  topk in
+ * [1, min(experts, MOE_MAX_TOPK)].  Of *w the sizes, group, dtype and router
+ * have to be valid; w13, w2 and their scales and zeros are not used.
  *
  * workspace: device memory of moe_nt_ws_size(T, w, topk) bytes or more,
  * 256-byte aligned, zero-filled before its first use; every call leaves it
@@ -64,7 +63,7 @@ typedef struct moe_nt_weights {
  * not run at the same time (order them on one stream).
  *
  * Returns GEMM_OK, GEMM_EINVAL (a NULL w, sizes, topk, flags or types out of
- * range, ldx < hidden, a NULL or misaligned pointer to data with at least
+ * range, ldx or ldd too, a NULL or misaligned pointer to data with at least
  * one element, a workspace too small, or an output that overlaps an input,
  * the workspace or another output) or GEMM_ELAUNCH.  T == 0 is a no-op.
  */
@@ -84,7 +83,8 @@ int moe_nt_route(const moe_nt_weights *w, const void *X, int32_t *ids, float *we
  * infinite); y is rounded once, after the weighted sum over j in order, so
  * results do not depend on timing.  Tokens run in chunks of 64, or of
  * 512 / topk where that is less: within a chunk an expert's weights are read
- * once for each 64 of its rows.
+ * once for each 16 of its rows where there are 8 or fewer for each expert on
+ * average, else once for each 32.
  *
  * topk in [1, MOE_MAX_TOPK]; router may be NULL.  Workspace and errors as
  * moe_nt_route.

@@ -351,3 +351,37 @@ def test_infinities_stay_in_their_token(T, group, dtype):
         assert torch.equal(bits(y[other]), bits(want[other])), "another token changed"
         # gates of both signs: silu has infinities and 0 * inf among its values
         assert not bool(torch.isfinite(y[T // 2]).any())
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_replays_beside_eager_calls_and_another_graph(group):
+    # captured on a stream that the layer has run on, replayed on others: no
+    # workspace is shared
+    note(f"moe replays beside eager calls, group {group}")
+    c = Case(17, 16, 4, 512, 256, torch.bfloat16, group)
+    Xs = [c.tokens(t) for t in (9, 33, 20)]
+    want = [c.layer(X)[0].clone() for X in Xs]
+    home, away = torch.cuda.Stream(), torch.cuda.Stream()
+    home.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(home):
+        c.layer(Xs[0])
+    torch.cuda.synchronize()
+    graphs, outs = [], [torch.empty_like(X) for X in Xs]
+    for X, out in zip(Xs[:2], outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=home):
+            c.layer(X, out=out)
+            c.layer(X, out=out)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(away):
+            graphs[0].replay()
+        graphs[1].replay()
+        c.layer(Xs[2], out=outs[2], stream=home)
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(bits(o), bits(w))
