@@ -24,13 +24,14 @@ __device__ __forceinline__ u32x4 load16_part(const uint16_t *p, int count)
     return v;
 }
 
-// A lane's place among the packed words of an N-row weight, and the step from
-// one to the next of its words: a division at the start only.
-struct WordWalk {
+// A lane's place among the words (or units) of an N-row weight, `words` to a
+// row, and the step from one to the next of its own: a division at the start
+// only.
+struct Walk {
     int64_t n;
     int at;
 
-    __device__ __forceinline__ WordWalk(int words)
+    __device__ __forceinline__ Walk(int words)
     {
         const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
         n = i / words;
@@ -57,10 +58,16 @@ __device__ __forceinline__ float nearest(float x, float rs)
     return __builtin_rintf(__builtin_fmaf(x, rs, 768.0f) - 768.0f);
 }
 
-// Quantisation, eight consecutive elements of a row per lane: one 16-byte
-// load, one packed word.  Lanes follow K, so a group's 4, 8 or 16 lanes are
-// neighbours and its extremes take 2, 3 or 4 exchanges; a 64-byte block's
-// words leave permuted but together.  2.5 bytes and more per element.
+// Quantisation, 32 consecutive elements of a row per lane: four 16-byte loads,
+// four packed words.  Lanes follow K, so a group is one lane or 2 or 4
+// neighbours, whose extremes take an exchange or two; a 64-byte block's words
+// leave by four lanes together.  2.5 bytes and more per element bound it: 82 us
+// for 16384 x 8192 bf16 in groups of 32 with zero points, 4.2 TB/s.  With 8
+// elements per lane the group's arithmetic and the addresses, done by every
+// lane, were the bound (30 VALU instructions to an element, 115 us), though
+// 1024 x 1024 took 3.5 us instead of 4.2.  Elements past the last whole unit
+// are loaded when they are worked on: a second branch of `fetch` would wait
+// for the first one's loads.
 template <bool BF, int GS>
 __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restrict__ W,
                                                        uint32_t *__restrict__ Q,
@@ -69,55 +76,62 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restric
                                                        int64_t ldw, int64_t step_rows,
                                                        int step_rest)
 {
-    constexpr int kLanes = GS / 8;
-    const int words = ((K + 127) >> 7) * 16, G = (K + GS - 1) / GS;
-    // every lane of a group of 16 runs the same number of times: words and the
-    // grid's lanes are multiples of 16
-    auto fetch = [&](const WordWalk &w) {
-        const uint16_t *src = W + w.n * ldw + w.at * 8;
-        u32x4 raw = {0, 0, 0, 0};
-        if (w.n < N && w.at * 8 + 8 <= K)
-            raw = load16(src);
-        else if (w.n < N && w.at * 8 < K)
-            raw = load16_part(src, K - w.at * 8);
-        return raw;
+    constexpr int kLanes = GS / 32;
+    struct Unit {
+        u32x4 v[4];
     };
-    WordWalk w(words);
-    u32x4 ahead = fetch(w);
+    const int units = ((K + 127) >> 7) * 4, G = (K + GS - 1) / GS;
+    // every lane of a group of 4 runs the same number of times: units and the
+    // grid's lanes are multiples of 4
+    auto fetch = [&](const Walk &w) {
+        Unit x = {};
+        if (w.n < N && w.at * 32 + 32 <= K) {    // or when it is worked on
+            const uint16_t *src = W + w.n * ldw + w.at * 32;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x.v[i] = load16(src + 8 * i);
+        }
+        return x;
+    };
+    Walk w(units);
+    Unit ahead = fetch(w);
     while (w.n < N) {
-        // the next word's elements are under way while this one's are worked
-        // on: 32 waves with one load each are 32 KB of a CU's 64 in flight
+        // the next unit's elements are under way while this one's are worked on
         const int64_t n = w.n;
-        const int at = w.at, k = at * 8;
-        const u32x4 raw = ahead;
-        w.next(words, step_rows, step_rest);
+        const int at = w.at, k = at * 32;
+        Unit raw = ahead;
+        w.next(units, step_rows, step_rest);
         ahead = fetch(w);
+        if (k + 32 > K) {
+            const uint16_t *src = W + n * ldw + k;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                raw.v[i] = load16_part(src + 8 * i, K - k - 8 * i);
+        }
         // The largest value and the largest magnitude of a negative one, at
         // least 0, as bits: signed 16-bit integers order them, two at a time.
         // An infinity or a NaN is the largest of either.
         s16x2 up = {0, 0}, down = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // (as elements of one vector the compiler dropped three of the four)
-            uint32_t pair = raw[i];
+        for (int i = 0; i < 16; ++i) {
+            // (as elements of one vector the compiler dropped three of four)
+            uint32_t pair = raw.v[i >> 2][i & 3];
             asm("" : "+v"(pair));
             up = __builtin_elementwise_max(up, __builtin_bit_cast(s16x2, pair));
             down = __builtin_elementwise_max(down,
                                              __builtin_bit_cast(s16x2, pair ^ 0x80008000u));
         }
-        // over the group's lanes: neighbours, pairs, halves of 8 and of 16
+        // over the group's lanes
         auto widest = [](s16x2 v) {
             auto step = [&](auto ctrl) {
                 const int moved = __builtin_amdgcn_update_dpp(
                     0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, false);
                 v = __builtin_elementwise_max(v, __builtin_bit_cast(s16x2, moved));
             };
-            step(std::integral_constant<int, 0xb1>{});       // lane ^ 1
-            step(std::integral_constant<int, 0x4e>{});       // lane ^ 2
-            if constexpr (kLanes > 4)
-                step(std::integral_constant<int, 0x141>{});  // 7 - lane of 8
-            if constexpr (kLanes > 8)
-                step(std::integral_constant<int, 0x140>{});  // 15 - lane of 16
+            if constexpr (kLanes > 1)
+                step(std::integral_constant<int, 0xb1>{});       // lane ^ 1
+            if constexpr (kLanes > 2)
+                step(std::integral_constant<int, 0x4e>{});       // lane ^ 2
             return (uint16_t)(v[0] > v[1] ? v[0] : v[1]);
         };
         const uint16_t up_bits = widest(up), down_bits = widest(down);
@@ -129,38 +143,48 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restric
         const float s = to_float<BF>(bits);
         const bool live = s > 0.0f && !any;
         const float rs = live ? 1.0f / s : 0.0f;
-        float z = 8.0f;
+        // q is the nearest number between `least` and `most`, plus z: where the
+        // group is not live, all of them become z
+        float z = 8.0f, least = -8.0f, most = 7.0f;
         if (Z && live)
             z = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(-lo / s), 0.0f), 15.0f);
-        auto x = [&](int e) { return to_float<BF>((uint16_t)(raw[e >> 1] >> (16 * (e & 1)))); };
-        float r[8];
-        if (__any(rs > 0x1p100f)) {          // 1 / s may have overflowed
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                r[e] = live ? __builtin_rintf(x(e) / s) : 0.0f;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                r[e] = live ? nearest(x(e), rs) : 0.0f;
+        if (Z) {
+            least = -z;
+            most = 15.0f - z;
         }
-        uint32_t word = 0;
+        least = live ? least : 0.0f;
+        most = live ? most : 0.0f;
+        const bool slow = __any(rs > 0x1p100f);          // 1 / s may have overflowed
+        uint32_t *dst = Q + n * (units * 4) + (at & ~3) * 4 + (at & 3);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float v;
-            if (Z)
-                v = __builtin_amdgcn_fmed3f(r[e] + z, 0.0f, 15.0f);
-            else
-                v = __builtin_amdgcn_fmed3f(r[e], -8.0f, 7.0f) + 8.0f;
-            word |= (uint32_t)v << (4 * (e >> 1) + 16 * (e & 1));
-        }
-        if (k + 8 > K) {                     // bits past the row's end are 0
+        for (int i = 0; i < 4; ++i) {
+            auto x = [&](int e) {
+                return to_float<BF>((uint16_t)(raw.v[i][e >> 1] >> (16 * (e & 1))));
+            };
+            float r[8];
+            if (slow) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (k + e >= K)
-                    word &= ~(15u << (4 * (e >> 1) + 16 * (e & 1)));
+                for (int e = 0; e < 8; ++e)
+                    r[e] = __builtin_rintf(x(e) / s);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    r[e] = nearest(x(e), rs);
+            }
+            uint32_t word = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = __builtin_amdgcn_fmed3f(r[e], least, most) + z;
+                word |= (uint32_t)v << (4 * (e >> 1) + 16 * (e & 1));
+            }
+            if (k + 8 * i + 8 > K) {             // bits past the row's end are 0
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (k + 8 * i + e >= K)
+                        word &= ~(15u << (4 * (e >> 1) + 16 * (e & 1)));
+            }
+            dst[4 * i] = word;
         }
-        const int j = (at >> 2) & 3, c = at & 3;
-        Q[n * words + (at & ~15) + 4 * c + j] = word;
         if (at % kLanes == 0 && k < K) {
             const int64_t g = n * G + k / GS;
             S[g] = any ? (BF ? 0x7fc0 : 0x7e00) : bits;
@@ -180,7 +204,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint32_t *__restr
                                                          int step_rest)
 {
     const int words = ((K + 127) >> 7) * 16, G = (K + GS - 1) / GS;
-    for (WordWalk w(words); w.n < N; w.next(words, step_rows, step_rest)) {
+    for (Walk w(words); w.n < N; w.next(words, step_rows, step_rest)) {
         const int64_t n = w.n;
         const int at = w.at, k = at * 8;
         if (k >= K)
@@ -238,10 +262,10 @@ void for_type(int dtype, F &&f)
         f(std::false_type{});
 }
 
-// Workgroups of 256 lanes for one lane per packed word, up to 32 per CU.
-unsigned word_grid(int64_t N, int64_t K)
+// Workgroups of 256 lanes for `lanes` of them, up to 32 per CU.
+unsigned lane_grid(int64_t lanes)
 {
-    const int64_t wgs = cdiv(N * cdiv(K, 128) * 16, 256);
+    const int64_t wgs = cdiv(lanes, 256);
     return (unsigned)(wgs < 8192 ? wgs : 8192);
 }
 
@@ -266,8 +290,10 @@ int convert(const void *W, const void *Q, const void *S, const void *Z, int64_t 
                 return GEMM_EINVAL;
     if (N == 0 || K == 0)
         return GEMM_OK;
-    const dim3 grid(word_grid(N, K));
-    const int64_t words = cdiv(K, 128) * 16, stride = (int64_t)grid.x * 256;
+    // a lane has one word, or the four that it quantises
+    const int64_t words = cdiv(K, 128) * (dequantize ? 16 : 4);
+    const dim3 grid(lane_grid(N * words));
+    const int64_t stride = (int64_t)grid.x * 256;
     const int64_t step_rows = stride / words;
     const int step_rest = (int)(stride % words);
     for_type(dtype, [&](auto bf) {
