@@ -208,6 +208,7 @@ int run(const moe_nt_weights *w, MoeArgs p, int64_t T, bool route, bool experts,
         p.plan = nullptr;
     const MoeLaunch go = launches(w);
     for (int64_t done = 0; next_chunk(p, T, done);) {
+        p.late = route && experts && p.T == 1 && p.E <= 64;
         if (route)
             go.route(p, stream);
         if (experts)

@@ -41,6 +41,7 @@ struct MoeArgs {
     int64_t ldx, ldd;
     int T, E, H, I, topk, renorm;
     int parts;                     // pieces of H in the router
+    int late;                      // the experts' first kernel chooses, not the router
 };
 
 // One translation unit for each type.  Not exported from the library.
@@ -256,7 +257,8 @@ __device__ __forceinline__ void choose(const float (&v)[NT][PER], const MoeArgs 
             if (token < p.T && place[t][i] < p.topk) {
                 const int slot = token * p.topk + place[t][i];
                 p.ids[slot] = lane + 64 * i;
-                lds_ids[slot] = lane + 64 * i;
+                if (lds_ids)
+                    lds_ids[slot] = lane + 64 * i;
                 p.weights[slot] = w[i] / over;
             }
     }
@@ -265,7 +267,9 @@ __device__ __forceinline__ void choose(const float (&v)[NT][PER], const MoeArgs 
 // Logits of 16 experts for 16 tokens over one of `parts` pieces of the hidden
 // size (a router is small: with the whole of it to a workgroup, 64 tokens of
 // 4096 against 16 experts took 22 us); the last workgroup adds the pieces in
-// order, chooses for every token and makes the plan.
+// order, chooses for every token and makes the plan.  Or, for one token of a
+// layer with up to 64 experts, nobody does: every workgroup of the up kernel
+// chooses for itself.
 template <bool BF>
 using RouteCore = Skinny<BF, 0, 1, 1, kRouteWaves, 1, true>;
 
@@ -292,6 +296,8 @@ __global__ void __launch_bounds__(kRouteWaves * 64) moe_route_kernel(MoeArgs p)
         if (e0 + n < p.E)
             put(logits + (t0 + m) * p.E + e0 + n, v[0]);
     });
+    if (p.late)
+        return;
     __syncthreads();
     int *cnt = (int *)lds, *ids = cnt + MOE_MAX_EXPERTS;
     if (!last_of(p.tickets, gridDim.x * gridDim.y * gridDim.z, (uint32_t *)ids))
@@ -342,6 +348,40 @@ __global__ void __launch_bounds__(kRouteWaves * 64) moe_route_kernel(MoeArgs p)
         make_plan(p.plan, p.T * p.topk, p.E, cnt, [&](int i) { return ids[i]; });
 }
 
+// The expert of one token's slot s, by every wave for itself from the logits
+// that the launch before has left: the rounds of `choose` up to s.  `write`:
+// and all ids and weights, for the launches that follow.  A router that
+// chooses itself passes its logits through memory to the last workgroup to
+// end.  4096 x 64, 8 chosen, 1536 inner rows in 4 bits: router and up product
+// 12.2 + 19.2 us that way, 4.5 + 21.0 this way; 1024 x 8, 2 chosen: 8.1 + 5.7,
+// 3.5 + 6.2.
+__device__ __forceinline__ int choose_slot(const MoeArgs &p, int s, bool write)
+{
+    const int lane = threadIdx.x & 63;
+    float v[1][1] = {{0.0f}};
+    for (int q = 0; q < p.parts; q += 4) {
+        float g[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            g[j] = p.logits[q + j < p.parts && lane < p.E ? (q + j) * p.E + lane : 0];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[0][0] += q + j < p.parts ? g[j] : 0.0f;
+    }
+    v[0][0] = lane < p.E ? v[0][0] : -__builtin_inff();
+    if (write)
+        choose<1, 1>(v, p, 0, 1, nullptr);
+    uint32_t key = lane < p.E ? order_of(v[0][0]) + 1 : 0;
+    int expert = 0;
+    for (int j = 0; j <= s; ++j) {
+        const uint32_t most =
+            reduce_wave(key, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+        expert = __builtin_ctzll(__ballot(key == most));
+        key = lane == expert ? 0 : key;
+    }
+    return expert;
+}
+
 // ---- experts ------------------------------------------------------------
 
 constexpr int kMoeWaves = 8;
@@ -371,7 +411,7 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
     const int s = wg / blocks, i0 = wg % blocks * 16;
     Plan::Item it;
     if (p.T == 1) {              // a slot is an expert: no plan
-        it.expert = p.ids[s];
+        it.expert = p.late ? choose_slot(p, s, wg == 0 && threadIdx.x < 64) : p.ids[s];
         it.first = it.slot = s;
         it.count = (uint32_t)it.expert < (uint32_t)p.E;
     } else {
