@@ -24,6 +24,7 @@ struct Plan {
     } item[kMoeSlots];
     int active;                      // items in use
     int slot[kMoeSlots];
+    int token[kMoeSlots];        // slot[i] / topk
 };
 
 struct MoeArgs {
@@ -94,7 +95,8 @@ __device__ __forceinline__ bool last_of(uint32_t *counter, uint32_t count, uint3
 
 // By one workgroup.  cnt: MOE_MAX_EXPERTS ints of LDS.  ids(i): slot i's id.
 template <class F>
-__device__ __forceinline__ void make_plan(Plan *plan, int n, int E, int *cnt, F &&ids)
+__device__ __forceinline__ void make_plan(Plan *plan, int n, int topk, int E, int *cnt,
+                                          F &&ids)
 {
     for (int e = threadIdx.x; e < E; e += blockDim.x)
         cnt[e] = 0;
@@ -139,6 +141,7 @@ __device__ __forceinline__ void make_plan(Plan *plan, int n, int E, int *cnt, F 
     if (id >= 0) {
         const int place = atomicAdd(&cnt[id], 1 << 16);
         plan->slot[place >> 16] = threadIdx.x;
+        plan->token[place >> 16] = threadIdx.x / topk;
     }
     __syncthreads();
     // the first slots, now that all are in place
@@ -152,7 +155,7 @@ template <int = 0>
 __global__ void __launch_bounds__(kMoeSlots) moe_plan_kernel(MoeArgs p)
 {
     __shared__ int cnt[MOE_MAX_EXPERTS];
-    make_plan(p.plan, p.T * p.topk, p.E, cnt, [&](int i) { return p.ids[i]; });
+    make_plan(p.plan, p.T * p.topk, p.topk, p.E, cnt, [&](int i) { return p.ids[i]; });
 }
 
 // ---- router -------------------------------------------------------------
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kRouteWaves * 64) moe_route_kernel(MoeArgs p)
     }
     __syncthreads();
     if (p.plan && p.T > 1)
-        make_plan(p.plan, p.T * p.topk, p.E, cnt, [&](int i) { return ids[i]; });
+        make_plan(p.plan, p.T * p.topk, p.topk, p.E, cnt, [&](int i) { return ids[i]; });
 }
 
 // The expert of one token's slot s, by every wave for itself from the logits
@@ -432,7 +435,10 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
         c.K = p.H;
         c.M = count;
         c.begin((char *)lds, p.X, (uint32_t)((p.T - 1) * p.ldx + p.H) * 2u);
-        c.run([&](int m) { return (uint32_t)(slot(m) / p.topk * p.ldx) * 2u; });
+        c.run([&](int m) {
+            const int t = it.count == 1 ? it.slot / p.topk : p.plan->token[it.first + c0 + m];
+            return (uint32_t)(t * p.ldx) * 2u;
+        });
         c.join([&](int m, int i, const float(&v)[2]) {
             if (i0 + i < p.I) {
                 const float act = v[0] / (1.0f + expf(-v[0]));

@@ -249,36 +249,51 @@ struct Skinny {
     }
 
     // Activations k0 .. k0 + 128 * steps - 1 of every row, zero from K on.
-    // `at(m)`: the byte of `ar` where row m starts.
+    // `at(m)`: the byte of `ar` where row m starts.  Pieces of all the rows a
+    // thread has to do with are under way at once: each wait is for memory.
     template <class F>
     __device__ __forceinline__ void stage_acts(int k0, int steps, F &&at) const
     {
         // a power of two of threads along a row, the rest along the rows
         const int per_row = steps * 16;
-        int shift = 31 - __builtin_clz(kThreads);
+        constexpr int kLog = 31 - __builtin_clz(kThreads);
+        int shift = kLog;
         while (shift > 4 && (1 << (shift - 1)) >= per_row)
             --shift;
         const int c0 = threadIdx.x & ((1 << shift) - 1), dc = 1 << shift;
         const int m0 = threadIdx.x >> shift, dm = kThreads >> shift;
-        constexpr int kBatch = 4;
-        for (int m = m0; m < M; m += dm) {
-            const uint32_t src = at(m) + (uint32_t)k0 * 2u;
-            char *dst = lds + m * astride;
-            for (int c = c0; c < per_row; c += dc * kBatch) {
-                u32x4 v[kBatch];
+        const int total = ((per_row + dc - 1) >> shift) * ((M + dm - 1) >> (kLog - shift));
+        int c = 0, m = 0;
+        auto batch = [&](auto count) G18_INLINE {
+            constexpr int kBatch = decltype(count)::value;
+            u32x4 v[kBatch];
+            int dst[kBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int k = (c + i * dc) * 8;
-                    v[i] = load_b128(ar, k0 + k + 8 <= K ? src + 2u * k : kOob);
-                }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int k = (c + i * dc) * 8;
-                    // the 8 elements that K ends among come below
-                    if (c + i * dc < per_row && (k0 + k + 8 <= K || k0 + k >= K))
-                        *(u32x4 *)(dst + k * 2) = v[i];
+            for (int i = 0; i < kBatch; ++i) {
+                const int k = (c0 + c) * 8, row = m0 + m;
+                const bool in = c0 + c < per_row && row < M, whole = k0 + k + 8 <= K;
+                const uint32_t src = at(min(row, M - 1)) + (uint32_t)(k0 + k) * 2u;
+                v[i] = load_b128(ar, in && whole ? src : kOob);
+                // the 8 elements that K ends among come below
+                dst[i] = in && (whole || k0 + k >= K) ? row * astride + k * 2 : -1;
+                c += dc;
+                if (c >= per_row) {
+                    c = 0;
+                    m += dm;
                 }
             }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (dst[i] >= 0)
+                    *(u32x4 *)(lds + dst[i]) = v[i];
+        };
+        for (int left = total; left > 0; left -= 4) {
+            if (left > 2)
+                batch(std::integral_constant<int, 4>{});
+            else if (left == 2)
+                batch(std::integral_constant<int, 2>{});
+            else
+                batch(std::integral_constant<int, 1>{});
         }
         if ((K & 7) && k0 + steps * 128 > K) {
             const int k = (K & ~7) + (threadIdx.x & 7);
@@ -296,27 +311,30 @@ struct Skinny {
     {
         uint32_t *dst = (uint32_t *)(lds + act_bytes(M, chunk));
         const int g0 = k0 / (GS ? GS : 1), groups = steps * kGroups;
-        constexpr int kBatch = 4;
+        // the waves' halves take the two blocks of rows, where there are two;
+        // 16 threads or more along the groups of a row
+        constexpr int kBatch = 4, kPart = kThreads / NR, kEach = kRows / NR;
+        constexpr int kAlong = kPart / kEach > 16 ? kPart / kEach : 16;
+        const int i = NR == 1 ? 0 : wave / (kPart / 64), t = threadIdx.x % kPart;
+        const auto scales = NR > 1 && i ? sr[NR - 1] : sr[0];
+        const auto zeros = NR > 1 && i ? zr[NR - 1] : zr[0];
+        for (int n = t / kAlong; n < kEach; n += kPart / kAlong) {
+            uint32_t *to = dst + (i * kEach + n) * sstride;
+            for (int g = t % kAlong; g < groups; g += kAlong * kBatch) {
+                uint32_t s[kBatch], z[kBatch];
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            for (int n = threadIdx.x >> 4; n < kRows / NR; n += kThreads / 16) {
-                uint32_t *to = dst + (i * 16 + n) * sstride;
-                for (int g = threadIdx.x & 15; g < groups; g += 16 * kBatch) {
-                    uint32_t s[kBatch], z[kBatch];
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        const int gg = g0 + g + 16 * k;
-                        const uint32_t o = gg < G ? (uint32_t)(n * G + gg) : kOob;
-                        s[k] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                            sr[i], 2 * o + (o & kOob), 0, 0);
-                        z[k] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zr[i], o, 0, 0);
-                    }
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k)
-                        if (g + 16 * k < groups)
-                            to[g + 16 * k] =
-                                s[k] | ((BF ? 0x4300u : 0x6400u) + ((z[k] | zdef) & 15u)) << 16;
+                for (int k = 0; k < kBatch; ++k) {
+                    const int gg = g0 + g + kAlong * k;
+                    const uint32_t o = gg < G ? (uint32_t)(n * G + gg) : kOob;
+                    s[k] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scales,
+                                                                          2 * o + (o & kOob), 0, 0);
+                    z[k] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zeros, o, 0, 0);
                 }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    if (g + kAlong * k < groups)
+                        to[g + kAlong * k] =
+                            s[k] | ((BF ? 0x4300u : 0x6400u) + ((z[k] | zdef) & 15u)) << 16;
             }
         }
     }
