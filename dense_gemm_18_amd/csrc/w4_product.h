@@ -25,7 +25,10 @@ __attribute__((visibility("hidden"))) void gemm18_w4_bf16(const W4Args &a, int g
 namespace {
 
 // One workgroup's tile of D, 16 * MB rows and as many columns as Core has
-// weight rows.
+// weight rows.  Few rows are bound by reading the weights: 1 x 16384 x 8192 with
+// zero points, 70 MB, takes 17 us (4.1 TB/s; 14 us from HBM and 10 from the
+// last-level cache for the reading alone), of which the launch, the first
+// loads and the join are 4, all that 1 x 1024 x 1024 has.
 template <bool BF, int MB, class Core>
 __global__ void __launch_bounds__(Core::kThreads, 2) gemm_w4_kernel(W4Args p)
 {
