@@ -6,6 +6,7 @@
 namespace {
 
 typedef int16_t s16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 // 16 bytes at any 2-byte alignment (one global load on gfx950).
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
@@ -48,7 +49,7 @@ struct Walk {
     }
 };
 
-// rint(x / s) for 16-bit x and s, and `rs` = 1 / s within 2 ulp: x / s is a
+// rint(x / s) for 16-bit x and s, and `rs` = 1 / s within 1 ulp: x / s is a
 // half-integer or at least 2^-12 from one (both have at most 11 bits), and
 // fma(x, rs, 768) - 768 puts it on a grid of 2^-14, where the half-integers
 // are, less than 2^-18 from where it was.  Three instructions for a
@@ -61,8 +62,8 @@ __device__ __forceinline__ float nearest(float x, float rs)
 // Quantisation, 32 consecutive elements of a row per lane: four 16-byte loads,
 // four packed words.  Lanes follow K, so a group is one lane or 2 or 4
 // neighbours, whose extremes take an exchange or two; a 64-byte block's words
-// leave by four lanes together.  2.5 bytes and more per element bound it: 82 us
-// for 16384 x 8192 bf16 in groups of 32 with zero points, 4.2 TB/s.  With 8
+// leave by four lanes together.  2.5 bytes and more per element bound it: 81 us
+// for 16384 x 8192 bf16 in groups of 32 with zero points, 4.3 TB/s.  With 8
 // elements per lane the group's arithmetic and the addresses, done by every
 // lane, were the bound (30 VALU instructions to an element, 115 us), though
 // 1024 x 1024 took 3.5 us instead of 4.2.  Elements past the last whole unit
@@ -108,25 +109,26 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restric
             for (int i = 0; i < 4; ++i)
                 raw.v[i] = load16_part(src + 8 * i, K - k - 8 * i);
         }
-        // The largest value and the largest magnitude of a negative one, at
-        // least 0, as bits: signed 16-bit integers order them, two at a time.
-        // An infinity or a NaN is the largest of either.
-        s16x2 up = {0, 0}, down = {0, 0};
+        // The largest value, at least 0, and the negative one of the largest
+        // magnitude, as bits, two at a time: signed 16-bit integers have the one
+        // as their maximum, unsigned ones the other (or a number below 2^15
+        // where none is negative).  An infinity or a NaN is the largest of either.
+        s16x2 up = {0, 0};
+        u16x2 down = {0, 0};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             // (as elements of one vector the compiler dropped three of four)
             uint32_t pair = raw.v[i >> 2][i & 3];
             asm("" : "+v"(pair));
             up = __builtin_elementwise_max(up, __builtin_bit_cast(s16x2, pair));
-            down = __builtin_elementwise_max(down,
-                                             __builtin_bit_cast(s16x2, pair ^ 0x80008000u));
+            down = __builtin_elementwise_max(down, __builtin_bit_cast(u16x2, pair));
         }
         // over the group's lanes
-        auto widest = [](s16x2 v) {
+        auto widest = [](auto v) {
             auto step = [&](auto ctrl) {
                 const int moved = __builtin_amdgcn_update_dpp(
                     0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, false);
-                v = __builtin_elementwise_max(v, __builtin_bit_cast(s16x2, moved));
+                v = __builtin_elementwise_max(v, __builtin_bit_cast(decltype(v), moved));
             };
             if constexpr (kLanes > 1)
                 step(std::integral_constant<int, 0xb1>{});       // lane ^ 1
@@ -134,7 +136,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restric
                 step(std::integral_constant<int, 0x4e>{});       // lane ^ 2
             return (uint16_t)(v[0] > v[1] ? v[0] : v[1]);
         };
-        const uint16_t up_bits = widest(up), down_bits = widest(down);
+        const uint16_t up_bits = widest(up), lowest = widest(down);
+        const uint16_t down_bits = lowest & 0x8000 ? lowest & 0x7fff : 0;
         constexpr uint16_t kInf = BF ? 0x7f80 : 0x7c00;
         const bool any = up_bits >= kInf || down_bits >= kInf;
         const float hi = to_float<BF>(up_bits), lo = -to_float<BF>(down_bits);
@@ -142,19 +145,19 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restric
             from_float<BF>(Z ? (hi - lo) / 15.0f : __builtin_fmaxf(hi, -lo) / 7.0f);
         const float s = to_float<BF>(bits);
         const bool live = s > 0.0f && !any;
-        const float rs = live ? 1.0f / s : 0.0f;
+        const float rs = live ? __builtin_amdgcn_rcpf(s) : 0.0f;
+        const bool slow = __any(rs > 0x1p100f);          // 1 / s may have overflowed
         // q is the nearest number between `least` and `most`, plus z: where the
         // group is not live, all of them become z
         float z = 8.0f, least = -8.0f, most = 7.0f;
-        if (Z && live)
-            z = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(-lo / s), 0.0f), 15.0f);
         if (Z) {
+            const float r = slow ? __builtin_rintf(-lo / s) : nearest(-lo, rs);
+            z = live ? __builtin_fminf(r, 15.0f) : 8.0f;
             least = -z;
             most = 15.0f - z;
         }
         least = live ? least : 0.0f;
         most = live ? most : 0.0f;
-        const bool slow = __any(rs > 0x1p100f);          // 1 / s may have overflowed
         uint32_t *dst = Q + n * (units * 4) + (at & ~3) * 4 + (at & 3);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -171,12 +174,18 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restric
                 for (int e = 0; e < 8; ++e)
                     r[e] = nearest(x(e), rs);
             }
-            uint32_t word = 0;
+            // the digits of two numbers to the base 16, exact in fp32
+            float half[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float v = __builtin_amdgcn_fmed3f(r[e], least, most) + z;
-                word |= (uint32_t)v << (4 * (e >> 1) + 16 * (e & 1));
+            for (int h = 0; h < 2; ++h) {
+                half[h] = z * 4369.0f;
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    half[h] = __builtin_fmaf(
+                        __builtin_amdgcn_fmed3f(r[2 * d + h], least, most),
+                        (float)(1 << (4 * d)), half[h]);
             }
+            uint32_t word = (uint32_t)half[0] | (uint32_t)half[1] << 16;
             if (k + 8 * i + 8 > K) {             // bits past the row's end are 0
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
