@@ -562,13 +562,14 @@ struct Skinny {
 // each other.
 // 64 x 16384 x 8192, fp16, groups of 128, one workgroup to a CU: 31 us, of
 // which reading the weights alone takes 14.  By counters the matrix units are
-// busy for 22 % of it, the VALU (unpacking, 195 instructions for a step's 32
-// matrix instructions) for 33 %, the LDS for 36 %, and with two waves to a SIMD
+// busy for 25 % of it, the VALU (unpacking, 195 instructions for a step's 32
+// matrix instructions) for 37 %, the LDS for 41 %, and with two waves to a SIMD
 // these follow each other more than they overlap: without consuming it takes
-// 18 us, without fetching activations 30 of then 37.  Wider rows in LDS
-// (fewer bank conflicts), scheduling groups and unconditional steps changed
-// nothing; four waves to a SIMD need 128 registers, which this tile does not
-// have.
+// 18 us, without fetching activations 30 of then 37.  Wider rows in LDS (fewer
+// bank conflicts), scheduling groups and unconditional steps changed nothing;
+// the waves' halves one phase apart, one reading LDS while the other multiplies,
+// took 35 us (bfloat16 33 instead of 35, smaller tiles more); four waves to a
+// SIMD need 128 registers, which this tile does not have.
 template <bool BF, int GS, int RB, int MB, int KW, int NW, int CS>
 struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
     using Base = Skinny<BF, GS, RB, MB, KW, NW, true>;
