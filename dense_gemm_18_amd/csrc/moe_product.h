@@ -498,10 +498,23 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_down_kern
         if (h >= p.H)
             continue;
         float sum = 0.0f;
-        for (int j = 0; j < p.topk; ++j) {
-            const int slot = t * p.topk + j;
-            if ((uint32_t)p.ids[slot] < (uint32_t)p.E)
-                sum = __builtin_fmaf(p.weights[slot], get(p.y + (int64_t)slot * p.H + h), sum);
+        // four slots' loads under way at once, those of slots that are left out
+        // or past the last without use
+        for (int j0 = 0; j0 < p.topk; j0 += 4) {
+            float y[4], weight[4];
+            int id[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int slot = t * p.topk + min(j0 + j, p.topk - 1);
+                id[j] = j0 + j < p.topk ? p.ids[slot] : -1;
+                weight[j] = p.weights[slot];
+                y[j] = get(p.y + (int64_t)slot * p.H + h);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if ((uint32_t)id[j] < (uint32_t)p.E)
+                    sum = __builtin_fmaf(weight[j], y[j], sum);
         }
         p.D[t * p.ldd + h] = from_float<BF>(sum);
     }
