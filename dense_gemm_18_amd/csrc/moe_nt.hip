@@ -32,7 +32,7 @@ Layout layout_of(int64_t T, const moe_nt_weights *w, int topk)
     // a ticket for each 16 hidden rows is more than any block size needs
     l.plan = up(4 * (1 + cdiv(w->hidden, 16)));
     l.logits = l.plan + up(sizeof(Plan));
-    l.h = l.logits + up(route_parts(w->hidden) * chunk * w->experts * 4);
+    l.h = l.logits + up(route_parts(w->hidden, w->experts, chunk) * chunk * w->experts * 4);
     l.y = l.h + up(slots * w->inner * 2);
     l.bytes = l.y + up(slots * w->hidden * 4);
     return l;
@@ -176,7 +176,6 @@ MoeArgs common_args(const moe_nt_weights *w, const void *X, const int32_t *ids,
     p.H = (int)w->hidden;
     p.I = (int)w->inner;
     p.topk = topk;
-    p.parts = route_parts(w->hidden);
     return p;
 }
 
@@ -208,6 +207,7 @@ int run(const moe_nt_weights *w, MoeArgs p, int64_t T, bool route, bool experts,
         p.plan = nullptr;
     const MoeLaunch go = launches(w);
     for (int64_t done = 0; next_chunk(p, T, done);) {
+        p.parts = route_parts(p.H, p.E, p.T);       // no more than the workspace has
         p.late = route && experts && p.T == 1 && p.E <= 64;
         if (route)
             go.route(p, stream);

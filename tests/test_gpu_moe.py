@@ -385,3 +385,19 @@ def test_replays_beside_eager_calls_and_another_graph(group):
         torch.cuda.synchronize()
         for o, w in zip(outs, want):
             assert torch.equal(bits(o), bits(w))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,E,topk,H", [(1, 16, 4, 2048), (16, 16, 16, 2048), (3, 1, 1, 2047),
+                                        (16, 5, 2, 1500), (16, 16, 3, 2050), (17, 16, 3, 2048),
+                                        (16, 17, 3, 2048), (2, 9, 9, 700)])
+def test_router_around_one_workgroup(T, E, topk, H, dtype):
+    note(f"moe router T{T} E{E} k{topk} H{H} {dtype}")
+    c = Case(T + E + H, E, topk, H, 24, dtype, renorm=False)
+    X = c.tokens(T)
+    ids, weights = c.layer.route(X)
+    c.check_route(X, ids, weights)
+    y, ids2, weights2 = c.layer(X)
+    assert torch.equal(ids, ids2)
+    assert bool(((weights - weights2).abs() <= 1e-5 * weights).all())
+    c.check_y(X, ids2, weights2, y)
