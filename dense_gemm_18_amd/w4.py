@@ -13,6 +13,7 @@ from . import binding
 from .binding import GEMM_OK, GemmError
 
 _DTYPES = None
+_HERE = nullcontext()
 
 
 def dtype_code(dtype) -> int:
@@ -40,7 +41,7 @@ def on_stream(stream):
     """Allocations inside are ``stream``'s: the memory of a tensor made for another
     stream may still be in use on this one."""
     if stream is None:
-        return nullcontext()
+        return _HERE
     import torch
     return torch.cuda.stream(stream)
 
