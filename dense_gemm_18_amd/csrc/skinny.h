@@ -568,8 +568,8 @@ struct Skinny {
 // 18 us, without fetching activations 30 of then 37.  Wider rows in LDS (fewer
 // bank conflicts), scheduling groups and unconditional steps changed nothing;
 // the waves' halves one phase apart, one reading LDS while the other multiplies,
-// took 35 us (bfloat16 33 instead of 35, smaller tiles more); four waves to a
-// SIMD need 128 registers, which this tile does not have.
+// took 32 to 36 us by where the fetches stood (smaller tiles more); four waves
+// to a SIMD need 128 registers, which this tile does not have.
 template <bool BF, int GS, int RB, int MB, int KW, int NW, int CS>
 struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
     using Base = Skinny<BF, GS, RB, MB, KW, NW, true>;
