@@ -44,6 +44,7 @@ struct MoeArgs {
     int parts;                     // pieces of H in the router
     int late;                      // the experts' first kernel chooses, not the router
 };
+constexpr int kLateExperts = 256;
 
 // One translation unit for each type.  Not exported from the library.
 struct MoeLaunch {
@@ -279,7 +280,7 @@ __device__ __forceinline__ void choose(const float (&v)[NT][PER], const MoeArgs 
 // size (a router is small: with the whole of it to a workgroup, 64 tokens of
 // 4096 against 16 experts took 22 us); the last workgroup adds the pieces in
 // order, chooses for every token and makes the plan.  Or, for one token of a
-// layer with up to 64 experts, nobody does: every workgroup of the up kernel
+// layer with up to kLateExperts, nobody does: every workgroup of the up kernel
 // chooses for itself.
 template <bool BF>
 using RouteCore = Skinny<BF, 0, 1, 1, kRouteWaves, 1, true>;
@@ -369,30 +370,52 @@ __global__ void __launch_bounds__(kRouteWaves * 64) moe_route_kernel(MoeArgs p)
 // chooses itself passes its logits through memory to the last workgroup to
 // end.  4096 x 64, 8 chosen, 1536 inner rows in 4 bits: router and up product
 // 12.2 + 19.2 us that way, 4.5 + 21.0 this way; 1024 x 8, 2 chosen: 8.1 + 5.7,
-// 3.5 + 6.2.
+// 3.5 + 6.2; the whole layer of 4096 x 256, 8 chosen: 41.4 and 38.1.
+template <int PER>
 __device__ __forceinline__ int choose_slot(const MoeArgs &p, int s, bool write)
 {
     const int lane = threadIdx.x & 63;
-    float v[1][1] = {{0.0f}};
+    float v[1][PER] = {};
     for (int q = 0; q < p.parts; q += 4) {
-        float g[4];
+        float g[4][PER];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            g[j] = p.logits[q + j < p.parts && lane < p.E ? (q + j) * p.E + lane : 0];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int e = lane + 64 * i;
+                g[j][i] = p.logits[q + j < p.parts && e < p.E ? (q + j) * p.E + e : 0];
+            }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            v[0][0] += q + j < p.parts ? g[j] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                v[0][i] += q + j < p.parts ? g[j][i] : 0.0f;
     }
-    v[0][0] = lane < p.E ? v[0][0] : -__builtin_inff();
+    uint32_t key[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool in = lane + 64 * i < p.E;
+        v[0][i] = in ? v[0][i] : -__builtin_inff();
+        key[i] = in ? order_of(v[0][i]) + 1 : 0;
+    }
     if (write)
-        choose<1, 1>(v, p, 0, 1, nullptr);
-    uint32_t key = lane < p.E ? order_of(v[0][0]) + 1 : 0;
+        choose<PER, 1>(v, p, 0, 1, nullptr);
     int expert = 0;
     for (int j = 0; j <= s; ++j) {
-        const uint32_t most =
-            reduce_wave(key, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
-        expert = __builtin_ctzll(__ballot(key == most));
-        key = lane == expert ? 0 : key;
+        auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            most = larger(most, key[i]);
+        most = reduce_wave(most, 0u, larger);
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) {
+            const uint64_t who = __ballot(key[i] == most);
+            expert = who ? __builtin_ctzll(who) + 64 * i : expert;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            key[i] = lane + 64 * i == expert ? 0 : key[i];
     }
     return expert;
 }
@@ -429,7 +452,11 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
     const int s = wg / blocks, i0 = wg % blocks * 16;
     Plan::Item it;
     if (p.T == 1) {              // a slot is an expert: no plan
-        it.expert = p.late ? choose_slot(p, s, wg == 0 && threadIdx.x < 64) : p.ids[s];
+        const bool write = wg == 0 && threadIdx.x < 64;
+        // (with more rows than 8 for each expert nothing is late)
+        it.expert = MB > 1 || !p.late ? p.ids[s]
+                    : p.E <= 64       ? choose_slot<1>(p, s, write)
+                                      : choose_slot<kLateExperts / 64>(p, s, write);
         it.first = it.slot = s;
         it.count = (uint32_t)it.expert < (uint32_t)p.E;
     } else {

@@ -401,3 +401,21 @@ def test_router_around_one_workgroup(T, E, topk, H, dtype):
     assert torch.equal(ids, ids2)
     assert bool(((weights - weights2).abs() <= 1e-5 * weights).all())
     c.check_y(X, ids2, weights2, y)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,topk,H,group", [(64, 16, 1100, 0), (65, 8, 300, 0), (200, 7, 2100, 64),
+                                            (256, 8, 4100, 128), (257, 8, 300, 0),
+                                            (256, 16, 64, 32)])
+def test_one_token_of_many_experts(E, topk, H, group, dtype):
+    note(f"moe one token E{E} k{topk} H{H} group {group} {dtype}")
+    c = Case(E + H, E, topk, H, 40, dtype, group, zeros=True)
+    for round in range(2):
+        X = c.tokens(1)
+        if round:                             # equal logits, by rising index
+            c.router[3:] = c.router[2]
+        y, ids, weights = c.layer(X)
+        ids2, weights2 = c.layer.route(X)
+        assert torch.equal(ids, ids2) and torch.equal(weights, weights2)
+        c.check_route(X, ids, weights)
+        c.check_y(X, ids, weights, y)
