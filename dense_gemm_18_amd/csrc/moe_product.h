@@ -450,6 +450,8 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
     const int blocks = (p.I + 15) / 16;
     const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
     const int s = wg / blocks, i0 = wg % blocks * 16;
+    if (s >= (p.T == 1 ? p.topk : min(p.E, p.T * p.topk)))
+        return;                  // past the end of a grid with a second dimension
     Plan::Item it;
     if (p.T == 1) {              // a slot is an expert: no plan
         const bool write = wg == 0 && threadIdx.x < 64;
@@ -502,6 +504,8 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_down_kern
     const int n = p.T * p.topk, blocks = (p.H + kDownRows<GS> - 1) / kDownRows<GS>;
     const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
     const int s = wg / blocks, block = wg % blocks, h0 = block * kDownRows<GS>;
+    if (s >= min(p.E, n))
+        return;                  // past the end of a grid with a second dimension
     const Plan::Item it = p.plan->item[s];
     if (it.count == 0 && s > 0)
         return;

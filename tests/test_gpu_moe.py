@@ -419,3 +419,31 @@ def test_one_token_of_many_experts(E, topk, H, group, dtype):
         assert torch.equal(ids, ids2) and torch.equal(weights, weights2)
         c.check_route(X, ids, weights)
         c.check_y(X, ids, weights, y)
+
+
+@pytest.mark.parametrize("H,I", [(1, 140000), (270000, 3)])
+def test_more_workgroups_than_one_dimension_of_a_grid(H, I):
+    # 512 experts or slots times 8750 or 8438 blocks: the second dimension's last
+    # row goes past the end
+    E, T, topk = 512, 64, 8
+    note(f"moe large grid H{H} I{I}")
+    g = gen(H)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device=device(), dtype=torch.float16)
+    w13, w2 = normal(E, 2 * I, H), normal(E, H, I)
+    w13 /= math.sqrt(H)
+    w2 /= math.sqrt(I)
+    layer = MoeLayer(normal(E, H), w13, w2, topk=topk)
+    X = normal(T, H)
+    ids = torch.randint(0, E, (T, topk), generator=g, device=device(), dtype=torch.int32)
+    weights = torch.rand((T, topk), generator=g, device=device())
+    y = layer.experts(X, ids, weights)
+    assert torch.equal(bits(layer.experts(X, ids, weights)), bits(y))
+    want = torch.zeros((T, H), dtype=torch.float64, device=device())
+    for e in sorted(set(ids.flatten().tolist())):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        gu = X[t].double() @ w13[e].double().T
+        h = torch.sigmoid(gu[:, :I]) * gu[:, :I] * gu[:, I:]
+        want.index_add_(0, t, (h @ w2[e].double().T) * weights[t, j].double().unsqueeze(-1))
+    assert w4_ref.rel(y, want) <= 2 * half_step(torch.float16)
