@@ -447,3 +447,41 @@ def test_more_workgroups_than_one_dimension_of_a_grid(H, I):
         h = torch.sigmoid(gu[:, :I]) * gu[:, :I] * gu[:, I:]
         want.index_add_(0, t, (h @ w2[e].double().T) * weights[t, j].double().unsqueeze(-1))
     assert w4_ref.rel(y, want) <= 2 * half_step(torch.float16)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,E,topk,H,group", [(2, 1, 1, 100, 0), (2, 2, 2, 300, 64), (8, 8, 8, 500, 0),
+                                              (8, 16, 16, 2100, 32), (8, 256, 16, 1100, 0),
+                                              (7, 65, 9, 4100, 128), (3, 256, 4, 260, 64),
+                                              (9, 64, 6, 520, 0), (4, 257, 8, 520, 64),
+                                              (72, 40, 2, 130, 0)])
+def test_a_few_tokens_of_few_and_many_experts(T, E, topk, H, group, dtype):
+    note(f"moe few tokens T{T} E{E} k{topk} H{H} group {group} {dtype}")
+    c = Case(T * E + H, E, topk, H, 56, dtype, group, zeros=True)
+    for alike in (False, True):
+        X = c.tokens(T)
+        if alike:                             # every token with the same experts
+            X[:] = X[0] + X * 0.01
+            if E > 2:
+                c.router[2:] = c.router[1]    # and equal logits, by rising index
+        y, ids, weights = c.layer(X)
+        ids2, weights2 = c.layer.route(X)
+        assert torch.equal(ids, ids2) and torch.equal(weights, weights2)
+        c.check_route(X, ids, weights)
+        c.check_y(X, ids, weights, y)
+        assert torch.equal(bits(c.layer.experts(X, ids, weights)), bits(y))
+        assert torch.equal(bits(c.layer(X)[0]), bits(y))
+
+
+def test_a_nan_token_among_a_few():
+    c = Case(6, 12, 3, 260, 40, torch.bfloat16)
+    note("moe few tokens, NaN")
+    X = c.tokens(5)
+    want = c.layer(X)
+    B = X.clone()
+    B[2, 7] = float("nan")
+    y, ids, weights = c.layer(B)
+    keep = [0, 1, 3, 4]
+    assert torch.equal(ids[keep], want[1][keep]) and torch.equal(weights[keep], want[2][keep])
+    assert torch.equal(bits(y[keep]), bits(want[0][keep]))
+    assert bool(torch.isnan(weights[2]).all()) and len(set(ids[2].tolist())) == 3
