@@ -432,24 +432,24 @@ constexpr int kDownWaves = GS ? 4 : 8;
 template <int GS>
 constexpr int kDownRows = 16 * 2 * (kMoeWaves / kDownWaves<GS>);
 
-template <bool BF, int GS, int MB>
-using UpCore = Skinny<BF, GS, 2, MB, kMoeWaves, 1, false>;
+template <bool BF, int GS, int RB, int MB>
+using UpCore = Skinny<BF, GS, RB, MB, kMoeWaves, 1, false>;
 template <bool BF, int GS, int MB>
 using DownCore = Skinny<BF, GS, 2, MB, kDownWaves<GS>, kMoeWaves / kDownWaves<GS>, true>;
 
-// h = silu(gate) * up for 16 of an expert's inner rows and all its slots.
-// One workgroup takes the 16 gate rows and their 16 up rows, its waves split
+// h = silu(gate) * up for some of an expert's inner rows and all its slots.
+// One workgroup takes 8 * RB gate rows and their 8 * RB up rows, its waves split
 // the hidden size.  Bound by reading w13: 64 tokens, 2 of 16 experts, 4096 x
 // 4096 bf16, 203 us for 1.07 GB (5.3 TB/s); 16 tokens, 6 of 64, 2048 x 1024,
 // 73 us for the 50 experts or so that any token chose (5.7 TB/s); one token,
 // 8 of 64, 4096 x 1536 in 4 bits, 20 us for 50 MB, of which 17 are the loads.
-template <bool BF, int GS, int MB>
+template <bool BF, int GS, int RB, int MB>
 __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel(MoeArgs p)
 {
     extern __shared__ f32x4 lds[];
-    const int blocks = (p.I + 15) / 16;
+    const int blocks = (p.I + 8 * RB - 1) / (8 * RB);
     const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
-    const int s = wg / blocks, i0 = wg % blocks * 16;
+    const int s = wg / blocks, i0 = wg % blocks * (8 * RB);
     if (s >= (p.T == 1 ? p.topk : min(p.E, p.T * p.topk)))
         return;                  // past the end of a grid with a second dimension
     Plan::Item it;
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
         auto slot = [&](int m) {
             return it.count == 1 ? it.slot : p.plan->slot[it.first + c0 + m];
         };
-        UpCore<BF, GS, MB> c;
+        UpCore<BF, GS, RB, MB> c;
         c.W = p.w13;
         c.row[0] = e * 2 * p.I + i0;
         c.row[1] = c.row[0] + p.I;
@@ -483,10 +483,14 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
             const int t = it.count == 1 ? it.slot / p.topk : p.plan->token[it.first + c0 + m];
             return (uint32_t)(t * p.ldx) * 2u;
         });
-        c.join([&](int m, int i, const float(&v)[2]) {
-            if (i0 + i < p.I) {
-                const float act = v[0] / (1.0f + expf(-v[0]));
-                p.h[(int64_t)slot(m) * p.I + i0 + i] = from_float<BF>(act * v[1]);
+        c.join([&](int m, int n, const float(&v)[RB]) {
+#pragma unroll
+            for (int r = 0; r < RB / 2; ++r) {
+                const int i = i0 + 16 * r + n;
+                if (i < p.I) {
+                    const float act = v[r] / (1.0f + expf(-v[r]));
+                    p.h[(int64_t)slot(m) * p.I + i] = from_float<BF>(act * v[RB / 2 + r]);
+                }
             }
         });
         __syncthreads();
@@ -721,9 +725,22 @@ void launch_experts(const MoeArgs &p, int group, bool planned, hipStream_t strea
         auto go = [&](auto mbs) {
             constexpr int MB = decltype(mbs)::value;
             const int rows = n < 16 * MB ? n : 16 * MB;
-            hipLaunchKernelGGL((moe_up_kernel<BF, GS, MB>), tile_grid(slots * cdiv(p.I, 16)),
-                               dim3(kMoeWaves * 64),
-                               (UpCore<BF, GS, MB>::lds_bytes(rows, p.H)), stream, p);
+            auto up = [&](auto rbs) {
+                constexpr int RB = decltype(rbs)::value;
+                hipLaunchKernelGGL((moe_up_kernel<BF, GS, RB, MB>),
+                                   tile_grid(slots * cdiv(p.I, 8 * RB)), dim3(kMoeWaves * 64),
+                                   (UpCore<BF, GS, RB, MB>::lds_bytes(rows, p.H)), stream, p);
+            };
+            // Packed weights, 32 inner rows to a workgroup where rows are long
+            // and that leaves four for each CU: 8 KB of a wave's loads are then
+            // a smaller part of its work.  Layers in us, bf16, groups of 128: 8
+            // tokens, 2 of 16 experts of 8192 x 2048 107 -> 97, 2 of 8, 4096 x
+            // 8192, 156 -> 144; 2 tokens (256 and 1024 workgroups) 42 -> 45 and 62
+            // -> 64; 2048 x 768, 8 of 256, 85 -> 88.
+            if (GS && p.H >= 4096 && slots * cdiv(p.I, 32) >= 4 * kCUs)
+                up(std::integral_constant<int, GS ? 4 : 2>{});
+            else
+                up(std::integral_constant<int, 2>{});
             const int64_t one = one_bytes<BF, GS>(p.topk, p.I);
             if (p.T == 1 && one <= kOneLds) {
                 // as many pairs as make all waves' work alike

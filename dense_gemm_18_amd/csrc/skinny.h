@@ -128,8 +128,8 @@ constexpr int kActBytes = 66 * 1024;
 constexpr int kScaleBytes = 32 * 1024;
 
 // One workgroup's product.  GS: 0 for 16-bit weights, else the group.
-// JOINED: the workgroup's weight rows follow each other; else (RB == 2,
-// NW == 1) block 0 and block 1 start at rows of their own.
+// JOINED: the workgroup's weight rows follow each other; else (RB even, NW == 1)
+// each half of the blocks starts at a row of its own.
 template <bool BF, int GS, int RB, int MB, int KW, int NW, bool JOINED>
 struct Skinny {
     using x8 = typename Elem<BF>::x8;
@@ -217,7 +217,7 @@ struct Skinny {
         zdef = W.z ? 0 : 8;
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
-            const int at = JOINED ? (nw() * RB + r) * 16 : 0;
+            const int at = JOINED ? (nw() * RB + r) * 16 : r % (RB / NR) * 16;
             woff[r] = (at + (lane() & 15)) * row_bytes + (lane() >> 4) * 16;
 #pragma unroll
             for (int m = 0; m < MB; ++m)
@@ -244,7 +244,7 @@ struct Skinny {
                     woff[r] + (st + u < end ? (uint32_t)(st + u) * (GS ? 64u : 256u) : kOob);
 #pragma unroll
                 for (int j = 0; j < (GS ? 1 : 4); ++j)
-                    b.v[u][r][j] = load_b128(wr[r % NR], o + 64u * j);
+                    b.v[u][r][j] = load_b128(wr[r / (RB / NR)], o + 64u * j);
             }
     }
 
@@ -376,7 +376,7 @@ struct Skinny {
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
                     const uint32_t end = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                        wr[r % NR], woff[r] - 16u * c + (uint32_t)(K - 1) * 2u, 0, 0);
+                        wr[r / (RB / NR)], woff[r] - 16u * c + (uint32_t)(K - 1) * 2u, 0, 0);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         b.v[u][r][j] = mend(b.v[u][r][j], left - 32 * j, end);

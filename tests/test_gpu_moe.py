@@ -485,3 +485,23 @@ def test_a_nan_token_among_a_few():
     assert torch.equal(ids[keep], want[1][keep]) and torch.equal(weights[keep], want[2][keep])
     assert torch.equal(bits(y[keep]), bits(want[0][keep]))
     assert bool(torch.isnan(weights[2]).all()) and len(set(ids[2].tolist())) == 3
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,E,topk,H,I,group", [(8, 64, 8, 4100, 530, 128), (40, 8, 2, 4130, 4090, 64),
+                                                (20, 33, 4, 4096, 1000, 32)])
+def test_long_packed_rows(T, E, topk, H, I, group, dtype):
+    note(f"moe long packed rows T{T} E{E} k{topk} H{H} I{I} group {group} {dtype}")
+    c = Case(T + E + I, E, topk, H, I, dtype, group, zeros=True)
+    X = c.tokens(T)
+    y, ids, weights = c.layer(X)
+    torch.cuda.synchronize()
+    c.check_route(X, ids, weights)
+    c.check_y(X, ids, weights, y)
+    # an infinity stays in its token
+    B = X.clone()
+    B[T // 2, 137] = float("inf")
+    z = c.layer.experts(B, ids, weights)
+    other = torch.arange(T, device=device()) != T // 2
+    assert torch.equal(bits(z[other]), bits(y[other]))
+    assert not bool(torch.isfinite(z[T // 2]).any())
