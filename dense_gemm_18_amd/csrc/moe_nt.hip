@@ -19,7 +19,12 @@ bool inner_ok(const moe_nt_weights *w)
 }
 
 // Workspace: tickets (kept at zero between calls), the plan, and a chunk's
-// logits, gated rows and their products.
+// logits, gated rows and their products.  The tickets are as many as the
+// longest hidden size needs, one for the router and one for each 32 hidden rows
+// (the fewest that a workgroup of the down product takes), 512 KB: a call of
+// other sizes then never finds there what this one leaves behind them.
+constexpr int64_t kTicketBytes = 4 * (1 + (GEMM_MAX_K + 31) / 32);
+
 struct Layout {
     int64_t plan, logits, h, y, bytes;
 };
@@ -29,8 +34,7 @@ Layout layout_of(int64_t T, const moe_nt_weights *w, int topk)
     auto up = [](int64_t n) { return cdiv(n, 256) * 256; };
     const int64_t chunk = moe_chunk(T, topk), slots = chunk * topk;
     Layout l;
-    // a ticket for each 16 hidden rows is more than any block size needs
-    l.plan = up(4 * (1 + cdiv(w->hidden, 16)));
+    l.plan = up(kTicketBytes);
     l.logits = l.plan + up(sizeof(Plan));
     l.h = l.logits + up(route_parts(w->hidden, w->experts, chunk) * chunk * w->experts * 4);
     l.y = l.h + up(slots * w->inner * 2);

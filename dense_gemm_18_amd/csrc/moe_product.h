@@ -431,6 +431,7 @@ template <int GS>
 constexpr int kDownWaves = GS ? 4 : 8;
 template <int GS>
 constexpr int kDownRows = 16 * 2 * (kMoeWaves / kDownWaves<GS>);
+static_assert(kDownRows<0> >= 32 && kDownRows<128> >= 32, "a ticket for each 32 hidden rows");
 
 template <bool BF, int GS, int RB, int MB>
 using UpCore = Skinny<BF, GS, RB, MB, kMoeWaves, 1, false>;
