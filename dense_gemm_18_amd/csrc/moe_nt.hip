@@ -210,6 +210,7 @@ int run(const moe_nt_weights *w, MoeArgs p, int64_t T, bool route, bool experts,
     if (!experts)
         p.plan = nullptr;
     const MoeLaunch go = launches(w);
+    const std::lock_guard<std::mutex> whole(launch_lock(p.tickets));
     for (int64_t done = 0; next_chunk(p, T, done);) {
         p.parts = route_parts(p.H, p.E, p.T);       // no more than the workspace has
         p.late = route && experts && p.T == 1 && p.E <= kLateExperts;

@@ -21,6 +21,8 @@
 // (2, 3 or 4 deep) was slower than eight waves that each wait for their batch.
 #pragma once
 
+#include <mutex>
+
 #include "gemm_types.h"
 #include "moe_nt.h"
 
@@ -697,6 +699,15 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
                          G18_INLINE { walk<decltype(exact)::value>(to); });
     }
 };
+
+// Held while a call enqueues launches that hand each other results in
+// `workspace`: those of another host thread's call on the same stream come before
+// or after all of them.  Calls with other workspaces seldom meet.
+inline std::mutex &launch_lock(const void *workspace)
+{
+    static std::mutex locks[64];
+    return locks[(((uintptr_t)workspace >> 8) * 0x9e3779b97f4a7c15ull) >> 58];
+}
 
 inline bool overlap(const void *p, uint64_t pn, const void *q, uint64_t qn)
 {

@@ -18,9 +18,10 @@ class MoeLayer:
 
     Calls are enqueued on ``stream`` (default: the current stream of the weights'
     device).  The layer keeps one workspace for each stream it has been called on, so
-    calls on different streams may overlap.  A call that is being captured takes a
-    workspace of its own from the graph's memory, and its zero fill becomes a part of
-    the graph: replays may run beside eager calls and other graphs."""
+    calls on different streams may overlap; host threads may call it on one stream or
+    on several.  A call that is being captured takes a workspace of its own from the
+    graph's memory, and its zero fill becomes a part of the graph: replays may run beside
+    eager calls and other graphs."""
 
     def __init__(self, router, w13, w2, topk: int, renormalize: bool = True):
         packed = isinstance(w13, W4Weight)
@@ -75,7 +76,8 @@ class MoeLayer:
             if ws is None:
                 with torch.cuda.device(self.device):
                     ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
-                self._workspaces[handle] = ws
+                # another thread may have been here: one of the two for both
+                ws = self._workspaces.setdefault(handle, ws)
         return ws, self._ws_bytes, handle
 
     def _check(self, X):

@@ -60,7 +60,9 @@ typedef struct moe_nt_weights {
  * workspace: device memory of moe_nt_ws_size(T, w, topk) bytes or more,
  * 256-byte aligned, zero-filled before its first use; every call leaves it
  * ready for the next, whatever its sizes.  Calls that share a workspace must
- * not run at the same time (order them on one stream).
+ * not run at the same time: they go on one stream, or are ordered by events.
+ * Several host threads may make them on that stream, each call's launches are
+ * enqueued side by side.
  *
  * Returns GEMM_OK, GEMM_EINVAL (a NULL w, sizes, topk, flags or types out of
  * range, ldx or ldd too, a NULL or misaligned pointer to data with at least

@@ -32,3 +32,51 @@ def test_counters_lie_apart_from_what_calls_of_other_sizes_write(tmp_path, group
     for x in launch_recorder.run(tmp_path, LAYOUTS.replace("GROUP", str(group))):
         assert x["inside"][0] == 0, x
         assert x["inside"][1] >= most, x
+
+
+THREADS = """
+pause_us.value = 1000
+WS = 0x5000000000
+w = weights()
+need = binding.moe_nt_ws_size(64, w, 2)
+
+def call(kind, T, at):
+    x, y = 0x8000000000 + at, 0x9000000000 + at
+    ids, wts = 0xa000000000 + at, 0xb000000000 + at
+    if kind == "layer":
+        return binding.moe_nt_layer(w, x, y, ids, wts, T, 256, 256, 2, 0, WS, need)
+    return binding.moe_nt_experts(w, x, ids, wts, y, T, 256, 256, 2, WS, need)
+
+calls = [("layer", 5), ("experts", 9), ("layer", 130), ("layer", 1)]
+alone = []
+for kind, T in calls:
+    before = count.value
+    assert call(kind, T, 0) == binding.GEMM_OK
+    alone.append(count.value - before)
+before = count.value
+start = threading.Barrier(len(calls))
+
+def work(i):
+    start.wait()
+    for _ in range(4):
+        assert call(*calls[i], (i + 1) << 28) == binding.GEMM_OK
+
+threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+# which call's X a launch has; a chunk's lies a little further on
+result = [alone, [(x["arg"][0] - 0x8000000000 >> 28) - 1 for x in launches()[before:]]]
+"""
+
+
+def test_threads_that_share_a_workspace_enqueue_whole_calls(tmp_path):
+    """The launches of one call hand each other a plan, logits and products in the
+    workspace, so none of another call's may come between them on the stream."""
+    alone, order = launch_recorder.run(tmp_path, THREADS)
+    assert sorted(set(order)) == [0, 1, 2, 3] and len(order) == 4 * sum(alone)
+    while order:
+        n = alone[order[0]]
+        assert order[:n] == [order[0]] * n, order
+        order = order[n:]
