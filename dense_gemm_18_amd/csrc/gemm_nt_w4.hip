@@ -392,6 +392,7 @@ int gemm_nt_w4(const void *A, const void *Q, const void *S, const void *Z, void 
     }
     const int64_t need = gemm_nt_w4_ws_size(M, N, K);
     if (need && ws_bytes >= need && lda == K && ldd == N) {
+        const std::lock_guard<std::mutex> both(launch_lock(workspace));
         const int rc = gemm_w4_dequantize(Q, S, Z, workspace, N, K, K, group, dtype, stream);
         if (rc != GEMM_OK)
             return rc;

@@ -87,7 +87,8 @@ int gemm_w4_dequantize(const void *Q, const void *S, const void *Z, void *W, int
  * workspace: device memory of gemm_nt_w4_ws_size(M, N, K) bytes or more,
  * 256-byte aligned, overlapping no operand, or NULL with ws_bytes 0.  Its
  * contents mean nothing between calls; calls that may run at the same time
- * need one each.
+ * need one each.  Several host threads may share one on a stream: each call's
+ * launches are enqueued side by side.
  *
  * Returns GEMM_OK, GEMM_EINVAL (as gemm_nt_f16 and gemm_w4_quantize, lda < K,
  * ldd < N, D overlapping an operand, or a negative ws_bytes, a NULL or

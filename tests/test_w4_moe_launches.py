@@ -80,3 +80,38 @@ def test_threads_that_share_a_workspace_enqueue_whole_calls(tmp_path):
         n = alone[order[0]]
         assert order[:n] == [order[0]] * n, order
         order = order[n:]
+
+
+PRODUCTS = """
+pause_us.value = 1000
+M, N, K = 700, 512, 1024
+need = binding.gemm_nt_w4_ws_size(M, N, K)
+assert need > 0
+
+def call(at):
+    return binding.gemm_nt_w4(0x1000000000 + at, 0x2000000000 + at, 0x3000000000 + at, 0,
+                              0x4000000000 + at, M, N, K, K, N, 128, 0, 0x5000000000, need)
+
+assert call(0) == binding.GEMM_OK
+alone = count.value
+start = threading.Barrier(3)
+
+def work(i):
+    start.wait()
+    for _ in range(4):
+        assert call(i << 28) == binding.GEMM_OK
+
+threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+result = [alone, [x["thread"] for x in launches()[alone:]]]
+"""
+
+
+def test_threads_that_share_a_workspace_unpack_and_multiply_together(tmp_path):
+    alone, order = launch_recorder.run(tmp_path, PRODUCTS)
+    assert alone == 2 and len(order) == 3 * 4 * 2 and len(set(order)) == 3
+    for i in range(0, len(order), 2):
+        assert order[i] == order[i + 1], order
