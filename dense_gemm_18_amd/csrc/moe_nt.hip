@@ -92,6 +92,29 @@ uint64_t scale_bytes(int64_t rows, int64_t cols, int group)
     return group ? (uint64_t)rows * (uint64_t)cdiv(cols, group) * 2u : 0u;
 }
 
+uint64_t router_bytes(const moe_nt_weights *w)
+{
+    return (uint64_t)w->experts * (uint64_t)w->hidden * 2u;
+}
+
+// The experts' weights, scales and zero points.
+struct ExpertSpans {
+    Span part[6];
+
+    explicit ExpertSpans(const moe_nt_weights *w)
+    {
+        const int64_t n13 = w->experts * 2 * w->inner, n2 = w->experts * w->hidden;
+        const uint64_t s13 = scale_bytes(n13, w->hidden, w->group);
+        const uint64_t s2 = scale_bytes(n2, w->inner, w->group);
+        part[0] = {w->w13, weight_bytes(n13, w->hidden, w->group)};
+        part[1] = {w->w2, weight_bytes(n2, w->inner, w->group)};
+        part[2] = {w->w13_scales, s13};
+        part[3] = {w->w2_scales, s2};
+        part[4] = {w->w13_zeros, w->w13_zeros ? s13 / 2 : 0};
+        part[5] = {w->w2_zeros, w->w2_zeros ? s2 / 2 : 0};
+    }
+};
+
 // What the two halves share: the activations, the workspace.
 int check_common(const void *X, const void *ws, int64_t ws_bytes, int64_t need)
 {
@@ -115,7 +138,7 @@ int check_route(const moe_nt_weights *w, const void *X, const int32_t *ids, cons
     const uint64_t slots = (uint64_t)T * (uint64_t)topk * 4u;
     return apart<3, 2>({{ids, slots}, {weights, slots}, {ws, (uint64_t)ws_bytes}},
                        {{X, span_bytes(T, w->hidden, ldx)},
-                        {w->router, (uint64_t)w->experts * (uint64_t)w->hidden * 2u}})
+                        {w->router, router_bytes(w)}})
                ? GEMM_OK
                : GEMM_EINVAL;
 }
@@ -141,20 +164,26 @@ int check_experts(const moe_nt_weights *w, const void *X, const int32_t *ids, co
     const int rc = check_common(X, ws, ws_bytes, moe_nt_ws_size(T, w, topk));
     if (rc != GEMM_OK)
         return rc;
-    const int64_t n13 = w->experts * 2 * w->inner, n2 = w->experts * w->hidden;
-    const uint64_t s13 = scale_bytes(n13, w->hidden, w->group);
-    const uint64_t s2 = scale_bytes(n2, w->inner, w->group);
     const uint64_t slots = (uint64_t)T * (uint64_t)topk * 4u;
-    return apart<2, 9>({{D, span_bytes(T, w->hidden, ldd)}, {ws, (uint64_t)ws_bytes}},
-                       {{X, span_bytes(T, w->hidden, ldx)},
-                        {ids, slots},
-                        {weights, slots},
-                        {w->w13, weight_bytes(n13, w->hidden, w->group)},
-                        {w->w2, weight_bytes(n2, w->inner, w->group)},
-                        {w->w13_scales, s13},
-                        {w->w2_scales, s2},
-                        {w->w13_zeros, w->w13_zeros ? s13 / 2 : 0},
-                        {w->w2_zeros, w->w2_zeros ? s2 / 2 : 0}})
+    const ExpertSpans e(w);
+    return apart<2, 3>({{D, span_bytes(T, w->hidden, ldd)}, {ws, (uint64_t)ws_bytes}},
+                       {{X, span_bytes(T, w->hidden, ldx)}, {ids, slots}, {weights, slots}}) &&
+                   apart<2, 6>({{D, span_bytes(T, w->hidden, ldd)}, {ws, (uint64_t)ws_bytes}},
+                               e.part)
+               ? GEMM_OK
+               : GEMM_EINVAL;
+}
+
+// What the whole layer adds to its halves' checks: the outputs of the one
+// against the inputs of the other.
+int check_across(const moe_nt_weights *w, const int32_t *ids, const float *weights, const void *D,
+                 int64_t T, int64_t ldd, int topk)
+{
+    const uint64_t slots = (uint64_t)T * (uint64_t)topk * 4u;
+    const ExpertSpans e(w);
+    return apart<2, 6>({{ids, slots}, {weights, slots}}, e.part) &&
+                   apart<1, 1>({{D, span_bytes(T, w->hidden, ldd)}},
+                               {{w->router, router_bytes(w)}})
                ? GEMM_OK
                : GEMM_EINVAL;
 }
@@ -266,6 +295,8 @@ int moe_nt_layer(const moe_nt_weights *w, const void *X, void *D, int32_t *ids, 
     int rc = check_route(w, X, ids, weights, T, ldx, topk, flags, workspace, ws_bytes);
     if (rc == GEMM_OK)
         rc = check_experts(w, X, ids, weights, D, T, ldx, ldd, topk, workspace, ws_bytes);
+    if (rc == GEMM_OK)
+        rc = check_across(w, ids, weights, D, T, ldd, topk);
     if (rc != GEMM_OK || T == 0)
         return rc;
     MoeArgs p = common_args(w, X, ids, weights, T, ldx, topk, workspace);
