@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 
 from . import binding
-from .w4 import W4Weight, check_out, dtype_code, launch, on_stream, row_stride, stream_of
+from .w4 import W4Weight, check_out, dtype_code, launch, on_device, on_stream, row_stride, stream_of
 
 
 class MoeLayer:
@@ -68,14 +68,14 @@ class MoeLayer:
         The caller keeps the tensor until it has launched."""
         import torch
         handle = stream_of(self.device, stream)
-        with on_stream(stream):
+        # the current stream, of which torch knows whether it captures, is the device's
+        with on_stream(stream), on_device(self.device):
             if torch.cuda.is_current_stream_capturing():
                 need = binding.moe_nt_ws_size(T, self._weights, self.topk)
                 return torch.zeros(need, dtype=torch.uint8, device=self.device), need, handle
             ws = self._workspaces.get(handle)
             if ws is None:
-                with torch.cuda.device(self.device):
-                    ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
+                ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
                 # another thread may have been here: one of the two for both
                 ws = self._workspaces.setdefault(handle, ws)
         return ws, self._ws_bytes, handle

@@ -46,16 +46,18 @@ def on_stream(stream):
     return torch.cuda.stream(stream)
 
 
+def on_device(device):
+    """``device`` is the current one inside."""
+    import torch
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
 def launch(name: str, device, args) -> None:
     """The raw entry point ``name`` with ``args`` on ``device``."""
-    import torch
     fn = getattr(binding.lib(), name)
-    if device.index == torch.cuda.current_device():
+    # the library launches on the current device: make it the operands' one
+    with on_device(device):
         rc = fn(*args)
-    else:
-        # the library launches on the current device: make it the operands' one
-        with torch.cuda.device(device):
-            rc = fn(*args)
     if rc != GEMM_OK:
         raise GemmError(rc, name)
 
