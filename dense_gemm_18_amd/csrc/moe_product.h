@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kMoeWaves * 64, 4) moe_down_one_kernel(MoeArgs
                 for (int i = 0; i < 4; ++i)
                     if (n0 + 32 * i < p.topk * 16)
                         scales[(n0 + 32 * i) * c.sstride + g0] =
-                            (in[i] ? s[i] : 0) | ((BF ? 0x4300u : 0x6400u) + z[i]) << 16;
+                            (in[i] ? s[i] : 0) | (0x6400u + z[i]) << 16;
             }
     }
     __syncthreads();
@@ -640,32 +640,14 @@ __global__ void __launch_bounds__(kMoeWaves * 64, 4) moe_down_one_kernel(MoeArgs
         const char *acts = (const char *)lds + j * c.astride;
         const uint32_t *sc = scales + j * 16 * c.sstride;
         const int first = part * steps / p.parts, last = (part + 1) * steps / p.parts;
-        auto walk = [&](auto exact, f32x4 (&to)[1][1]) G18_INLINE {
-            typename Core::template Batch<Core::U> b;
+        typename Core::template Batch<Core::U> b;
 #pragma nounroll
-            for (int st = first; st < last; st += Core::U) {
-                c.load(b, st, last);
+        for (int st = first; st < last; st += Core::U) {
+            c.load(b, st, last);
 #pragma unroll
-                for (int k = 0; k < Core::U; ++k)
-                    if (st + k < last)
-                        c.template consume<decltype(exact)::value>(b, k, st + k, 0, acts, sc, to);
-            }
-        };
-        walk(std::false_type{}, c.acc);
-        if constexpr (BF && GS != 0) {
-            // as Skinny::finish, for this wave alone
-            bool odd = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                odd |= !Core::finite(c.acc[0][0][e]);
-            if (__any(odd)) {
-                f32x4 again[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
-                walk(std::true_type{}, again);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (!Core::finite(c.acc[0][0][e]))
-                        c.acc[0][0][e] = again[0][0][e] * 0x1p12f;
-            }
+            for (int k = 0; k < Core::U; ++k)
+                if (st + k < last)
+                    c.consume(b, k, st + k, 0, acts, sc);
         }
         const float w = p.weights[j];
 #pragma unroll

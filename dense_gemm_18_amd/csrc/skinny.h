@@ -57,57 +57,65 @@ __device__ __forceinline__ uint16_t from_float(float v)
     return __builtin_bit_cast(uint16_t, (typename Elem<BF>::T)v);
 }
 
-// Eight 4-bit values of one packed word as 16-bit integers, exact.  A value
-// in the low bits of the mantissa of 1024 (fp16) or 128 (bfloat16) is that
-// number plus q: one mask-and-or for two of them.
+// What a product with packed bfloat16 weights has to be multiplied by: they go to
+// the matrix units times 2^-11 (still exact), so that a group's sum of at most 128
+// terms of 15 |A| stays in fp32's range wherever A does.  fp16's does anyway.
+template <bool BF, int GS>
+constexpr float kUnscale = BF && GS != 0 ? 0x1p11f : 1.0f;
+
+// Eight 4-bit values of one packed word less their zero point (bfloat16: times
+// 2^-11), exact in either type.  A value in the low bits of the mantissa of 1024 (fp16) is that number
+// plus q, one four bits up 1024 + 16 q: one mask-and-or makes two of them, and
+// one shift serves all.
 //
-// fp16 takes 1024 + z off both halves in one packed instruction, exactly,
-// leaving q - z; a value four bits up is 1024 + 16 q, and a packed fma with
-// 1/16 and 64 + z gives the same without a shift: 9 instructions for 8 weights.
-// bfloat16 has no packed arithmetic on gfx950: its 128 + q go to the matrix
-// unit as they are, and the caller takes (128 + z) * sum(A) off in fp32 (7
-// instructions; EXACT, which subtracts in fp32 and packs again, takes 35 and
-// leaves (q - z) * 2^-12).
-// sz: the number to take off, as 16 bits, in its upper half.
-template <bool BF, bool EXACT>
+// fp16 takes 1024 + z off both halves in one packed instruction, or has a packed
+// fma with 1/16 and 64 + z: 9 instructions for 8 weights.  bfloat16 has no packed
+// arithmetic on gfx950: a mixed fma reads each half as fp16 and leaves the
+// number in fp32, and one conversion packs two: 17 instructions.  (The matrix units could see
+// 128 + q, for 7, with (128 + z) times the activations' sum taken off afterwards.
+// Those sums are of terms up to 143 |A| where the result has 15 |A| or less, so an
+// activation that stands out left its rounding where its weight is 0.  Exact
+// numbers take 3 to 12 % longer up to 32 rows, 7 x 16384 x 8192 in groups of 128
+// 18.0 us for 16.7, and 3 to 8 % less from 64 rows on, whose matrix instructions for
+// the activations' sums they save.)
+// sz: 1024 + z in fp16, in its upper half.
+template <bool BF>
 __device__ __forceinline__ typename Elem<BF>::x8 unpack8(uint32_t w, uint32_t sz)
 {
     // the constants in registers: v_and_or_b32 takes no literals
-    uint32_t mask = 0x000f000fu, magic = BF ? 0x43004300u : 0x64006400u;
+    uint32_t mask = 0x000f000fu, mask4 = 0x00f000f0u, magic = 0x64006400u;
     asm("" : "+s"(mask));
+    asm("" : "+s"(mask4));
     asm("" : "+v"(magic));
+    const auto pair = [&](int t) G18_INLINE {
+        return __builtin_bit_cast(f16x2,
+                                  ((t < 2 ? w : w >> 8) & (t & 1 ? mask4 : mask)) | magic);
+    };
     u32x4 v;
     if constexpr (!BF) {
-        uint32_t mask4 = 0x00f000f0u, off = (sz >> 16) | (sz & 0xffff0000u);
-        asm("" : "+s"(mask4));
+        uint32_t off = (sz >> 16) | (sz & 0xffff0000u);
         asm("" : "+v"(off));      // seen as two equal halves it would be split up again
         const f16x2 z = __builtin_bit_cast(f16x2, off);
         const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
         // 64 + z, from 1024 + z
         const f16x2 z4 = z - f16x2{(_Float16)960.0f, (_Float16)960.0f};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const uint32_t x = t < 2 ? w : w >> 8;
-            const f16x2 q =
-                __builtin_bit_cast(f16x2, (x & (t & 1 ? mask4 : mask)) | magic);
+        for (int t = 0; t < 4; ++t)
             v[t] = __builtin_bit_cast(
-                uint32_t, t & 1 ? __builtin_elementwise_fma(q, sixteenth, -z4) : q - z);
-        }
+                uint32_t, t & 1 ? __builtin_elementwise_fma(pair(t), sixteenth, -z4) : pair(t) - z);
         return __builtin_bit_cast(f16x8, v);
     } else {
+        const float z = (float)__builtin_bit_cast(f16x2, sz)[1];
+        const float off = z * 0x1p-11f, off4 = (z - 960.0f) * 0x1p-11f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            v[t] = ((w >> (4 * t)) & mask) | magic;
-        if constexpr (EXACT) {
-            const float off = __builtin_bit_cast(float, sz & 0xffff0000u);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const float lo = (__builtin_bit_cast(float, v[t] << 16) - off) * 0x1p-12f;
-                const float hi =
-                    (__builtin_bit_cast(float, v[t] & 0xffff0000u) - off) * 0x1p-12f;
-                v[t] = (__builtin_bit_cast(uint32_t, lo) >> 16) |
-                       (__builtin_bit_cast(uint32_t, hi) & 0xffff0000u);
-            }
+        for (int t = 0; t < 4; ++t) {
+            const f16x2 q = pair(t);
+            const float by = t & 1 ? 0x1p-15f : 0x1p-11f, less = t & 1 ? off4 : off;
+            const float lo = __builtin_fmaf((float)q[0], by, -less);
+            const float hi = __builtin_fmaf((float)q[1], by, -less);
+            // exact: the upper halves are the numbers
+            v[t] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi),
+                                         __builtin_bit_cast(uint32_t, lo), 0x07060302u);
         }
         return __builtin_bit_cast(bf16x8, v);
     }
@@ -307,8 +315,7 @@ struct Skinny {
     }
 
     // Scale and zero point of each row's groups in one word: the scale's bits
-    // below, above them the 16-bit number that unpack8 takes off, 1024 + z or
-    // 128 + z.  Groups from G on, and rows past the end, have the scale 0.
+    // below, above them the fp16 number that unpack8 takes off, 1024 + z.  Groups from G on, and rows past the end, have the scale 0.
     __device__ __forceinline__ void stage_scales(int k0, int steps) const
     {
         uint32_t *dst = (uint32_t *)(lds + act_bytes(M, chunk));
@@ -336,7 +343,7 @@ struct Skinny {
                 for (int k = 0; k < kBatch; ++k)
                     if (g + kAlong * k < groups)
                         to[g + kAlong * k] =
-                            s[k] | ((BF ? 0x4300u : 0x6400u) + ((z[k] | zdef) & 15u)) << 16;
+                            s[k] | (0x6400u + ((z[k] | zdef) & 15u)) << 16;
             }
         }
     }
@@ -357,10 +364,9 @@ struct Skinny {
 
     // Step u of a batch, step `st` of the chunk that starts at k0 and whose
     // activations and scales are at `acts` and `scales`.
-    template <bool EXACT, int N>
+    template <int N>
     __device__ __forceinline__ void consume(Batch<N> &b, int u, int st, int k0,
-                                            const char *acts, const uint32_t *scales,
-                                            f32x4 (&to)[RB][MB]) const
+                                            const char *acts, const uint32_t *scales)
     {
         const int c = lane() >> 4;
         x8 a[MB][4];
@@ -390,39 +396,25 @@ struct Skinny {
                 for (int r = 0; r < RB; ++r)
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
-                        to[r][m] = mfma16<BF>(a[m][j], __builtin_bit_cast(x8, b.v[u][r][j]),
-                                              to[r][m]);
+                        acc[r][m] = mfma16<BF>(a[m][j], __builtin_bit_cast(x8, b.v[u][r][j]),
+                                               acc[r][m]);
         } else {
             constexpr int per = 4 / kGroups;       // matrix instructions per group
             const uint32_t *sp =
                 scales + ((JOINED ? nw() * RB * 16 : 0) + (lane() & 15)) * sstride + st * kGroups;
 #pragma unroll
             for (int k = 0; k < kGroups; ++k) {
-                f32x4 asum[MB];
-                if constexpr (BF && !EXACT) {
-                    // the activations' own sum, in every column
-                    const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-#pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        asum[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int i = 0; i < per; ++i)
-                            asum[m] = mfma16<BF>(a[m][k * per + i], __builtin_bit_cast(x8, one),
-                                                 asum[m]);
-                    }
-                }
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
                     const uint32_t sz = sp[r * 16 * sstride + k];
                     const float sc = to_float<BF>((uint16_t)sz);
-                    const float off = __builtin_bit_cast(float, sz & 0xffff0000u);   // BF
                     f32x4 sum[MB];
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
                         sum[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int i = 0; i < per; ++i) {
-                        const x8 f = unpack8<BF, EXACT>(b.v[u][r][0][k * per + i], sz);
+                        const x8 f = unpack8<BF>(b.v[u][r][0][k * per + i], sz);
 #pragma unroll
                         for (int m = 0; m < MB; ++m)
                             sum[m] = mfma16<BF>(a[m][k * per + i], f, sum[m]);
@@ -430,19 +422,17 @@ struct Skinny {
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float v = sum[m][e];
-                            if constexpr (BF && !EXACT)
-                                v = __builtin_fmaf(-off, asum[m][e], v);
-                            to[r][m][e] = __builtin_fmaf(sc, v, to[r][m][e]);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            acc[r][m][e] = __builtin_fmaf(sc, sum[m][e], acc[r][m][e]);
                 }
             }
         }
     }
 
-    template <bool EXACT, class F>
-    __device__ __forceinline__ void walk(f32x4 (&to)[RB][MB], F &&at)
+    // The product, each wave's part of it in `acc`.  `at(m)`: the byte of the
+    // activations where row m starts.
+    template <class F>
+    __device__ __forceinline__ void run(F &&at)
     {
         const int total = (K + 127) >> 7, per = chunk >> 7;
         for (int s0 = 0; s0 < total; s0 += per) {
@@ -451,7 +441,7 @@ struct Skinny {
             const int end = (kw() + 1) * steps / KW;
             Batch<U> b;
             load(b, s0 + st, s0 + end);
-            if (s0 > 0 || EXACT)
+            if (s0 > 0)
                 __syncthreads();          // the chunk before has been read
             stage_acts(s0 * 128, steps, at);
             if constexpr (GS != 0)
@@ -462,64 +452,11 @@ struct Skinny {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (st + u < end)
-                        consume<EXACT>(b, u, st + u, s0 * 128, lds,
-                                       (const uint32_t *)(lds + act_bytes(M, chunk)), to);
+                        consume(b, u, st + u, s0 * 128, lds,
+                                (const uint32_t *)(lds + act_bytes(M, chunk)));
                 st += U;
                 if (st < end)
                     load(b, s0 + st, s0 + end);
-            }
-        }
-    }
-
-    static __device__ __forceinline__ bool finite(float v)
-    {
-        return __builtin_fabsf(v) < __builtin_inff();
-    }
-
-    // The product, each wave's part of it in `acc`.  `at(m)`: the byte of the
-    // activations where row m starts.
-    template <class F>
-    __device__ __forceinline__ void run(F &&at)
-    {
-        finish([&](auto exact, f32x4 (&to)[RB][MB])
-                   G18_INLINE { walk<decltype(exact)::value>(to, at); });
-    }
-
-    // walk(false_type, acc), and what infinities need after it.
-    template <class W>
-    __device__ __forceinline__ void finish(W &&walk)
-    {
-        walk(std::false_type{}, acc);
-        if constexpr (BF && GS != 0) {
-            // An activation that is infinite, or so large that 128 times it
-            // overflows, leaves infinity minus infinity where q - z itself
-            // would not: such sums, and no others, are formed again with exact
-            // weights.  Those go in times 2^-12, so that a group's sum of at
-            // most 128 terms of 15 |A| cannot pass fp32 where A does not.
-            bool odd = false;
-#pragma unroll
-            for (int r = 0; r < RB; ++r)
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        odd |= !finite(acc[r][m][e]);
-            if (__syncthreads_or(odd)) {
-                f32x4 sum[RB][MB];
-#pragma unroll
-                for (int r = 0; r < RB; ++r)
-#pragma unroll
-                    for (int m = 0; m < MB; ++m)
-                        sum[r][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                walk(std::true_type{}, sum);
-#pragma unroll
-                for (int r = 0; r < RB; ++r)
-#pragma unroll
-                    for (int m = 0; m < MB; ++m)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!finite(acc[r][m][e]))
-                                acc[r][m][e] = sum[r][m][e] * 0x1p12f;
             }
         }
     }
@@ -549,6 +486,7 @@ struct Skinny {
 #pragma unroll
                     for (int w = 0; w < KW; ++w)
                         v[r] += p[w * RB * 256];
+                    v[r] *= kUnscale<BF, GS>;
                 }
                 if (16 * mb + m < M)
                     f(16 * mb + m, band * 16 + n, v);
@@ -639,7 +577,7 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
             const int n = idx / (CS * kGroups), g = idx % (CS * kGroups);
             if (n < kRows)
                 scales[n * kScales + g] =
-                    x.s[i] | ((BF ? 0x4300u : 0x6400u) + ((x.z[i] | this->zdef) & 15u)) << 16;
+                    x.s[i] | (0x6400u + ((x.z[i] | this->zdef) & 15u)) << 16;
         }
         // the 8 elements that K ends among, of which `fetch` left zeros
         const int K = this->K;
@@ -653,14 +591,16 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
         }
     }
 
-    template <bool EXACT>
-    __device__ __forceinline__ void walk(f32x4 (&to)[RB][MB])
+    // `at(m)` is m times at(1) here.
+    template <class F>
+    __device__ __forceinline__ void run(F &&at)
     {
+        row_bytes = at(1);
+        this->astride = kStride;
+        this->sstride = kScales;
         const int total = (this->K + 127) >> 7, mine = this->kw() * kSteps;
         typename Base::template Batch<kSteps> even, odd;
         Next x;
-        if (EXACT)
-            __syncthreads();
         fetch(x, 0);
         this->load(even, mine, total);
         this->load(odd, CS + mine, total);
@@ -676,8 +616,7 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
 #pragma unroll
             for (int u = 0; u < kSteps; ++u)
                 if (s0 + mine + u < total)
-                    this->template consume<EXACT>(b, u, mine + u, s0 * 128, buf,
-                                                  (const uint32_t *)(buf + kActs), to);
+                    this->consume(b, u, mine + u, s0 * 128, buf, (const uint32_t *)(buf + kActs));
             this->load(b, s0 + 2 * CS + mine, total);
             __syncthreads();
         };
@@ -686,17 +625,6 @@ struct Piped : Skinny<BF, GS, RB, MB, KW, NW, true> {
             chunk(even, s0, this->lds, this->lds + kBuffer);
             chunk(odd, s0 + CS, this->lds + kBuffer, this->lds);
         }
-    }
-
-    // `at(m)` is m times at(1) here.
-    template <class F>
-    __device__ __forceinline__ void run(F &&at)
-    {
-        row_bytes = at(1);
-        this->astride = kStride;
-        this->sstride = kScales;
-        this->finish([&](auto exact, f32x4 (&to)[RB][MB])
-                         G18_INLINE { walk<decltype(exact)::value>(to); });
     }
 };
 

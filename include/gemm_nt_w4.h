@@ -77,12 +77,10 @@ int gemm_w4_dequantize(const void *Q, const void *S, const void *Z, void *W, int
  * The sums are held in fp32 and rounded once.  A call with M up to
  * GEMM_W4_DIRECT_M rows, and any call without a workspace, unpacks the
  * weight on its way into the matrix units: there q - z is exact and s
- * multiplies each group's fp32 sum.  (For bfloat16 the units see 128 + q,
- * and (128 + z) times the group's sum of A, in fp32 too, is taken off.)  Above
- * that, where A and D are dense (lda == K, ldd == N) and the workspace is
- * large enough, the weight is unpacked once into the workspace, rounded to
- * the 16-bit type as gemm_w4_dequantize does, and the 16-bit product reads
- * it there.
+ * multiplies each group's fp32 sum.  Above that, where A and D are dense
+ * (lda == K, ldd == N) and the workspace is large enough, the weight is
+ * unpacked once into the workspace, rounded to the 16-bit type as
+ * gemm_w4_dequantize does, and the 16-bit product reads it there.
  *
  * workspace: device memory of gemm_nt_w4_ws_size(M, N, K) bytes or more,
  * 256-byte aligned, overlapping no operand, or NULL with ws_bytes 0.  Its
