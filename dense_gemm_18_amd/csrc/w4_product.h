@@ -99,6 +99,16 @@ void launch_w4_piped(const W4Args &a, hipStream_t stream)
 //   64 rows, 64 x 64       31.8    29.7    28.1    27.4
 //            32 x 64       35.1    21.6    19.5    17.9
 //            32 x 32       47.2    25.6    15.8    13.9
+// Of the 16 x 64 tile the resident form has half the waves and less LDS, and wins
+// where that lets two workgroups share a compute unit and the groups' scales are
+// few: one row, in us, resident and chunked, by columns x K:
+//                      16384 x 8192  16384 x 16384  32768 x 4096  65536 x 4096
+//   fp16, groups of 128   17.2 15.4      37.9 33.5     17.6 18.5     34.5 37.9
+//                    64   22.0 15.9      46.0 34.3     18.7 19.2     35.7 39.8
+//                    32   28.3 17.8      63.3 38.5     26.0 23.0     50.7 45.5
+//   bf16, groups of 128   21.2 17.8      42.3 36.1     20.6 22.0     38.9 43.3
+//                    64   25.2 19.1      48.8 38.6     21.7 22.7     40.3 45.2
+//                    32   31.3 21.4      69.0 42.0     29.0 25.7     58.1 52.3
 template <bool BF>
 void launch_w4(const W4Args &a, int group, hipStream_t stream)
 {
@@ -107,10 +117,13 @@ void launch_w4(const W4Args &a, int group, hipStream_t stream)
     };
     with_group(group, [&](auto gs) {
         constexpr int GS = decltype(gs)::value ? decltype(gs)::value : 128;
-        if (a.M <= 16 && (int64_t)a.M * (cdiv(a.K, 128) * 256 + 16) <= kActBytes) {
-            if (fills(16, 64))
-                launch_w4_resident<BF, GS, 4>(a, stream);
-            else if (fills(16, 32))
+        const bool whole =
+            a.M <= 16 && (int64_t)a.M * (cdiv(a.K, 128) * 256 + 16) <= kActBytes;
+        if constexpr (GS > 32)
+            if (whole && cdiv(a.N, 64) >= 2 * kCUs)
+                return launch_w4_resident<BF, GS, 4>(a, stream);
+        if (whole && !fills(16, 64)) {
+            if (fills(16, 32))
                 launch_w4_resident<BF, GS, 2>(a, stream);
             else
                 launch_w4_resident<BF, GS, 1>(a, stream);
