@@ -716,10 +716,13 @@ void launch_experts(const MoeArgs &p, int group, bool planned, hipStream_t strea
             };
             // Packed weights, 32 inner rows to a workgroup where rows are long
             // and that leaves four for each CU: 8 KB of a wave's loads are then
-            // a smaller part of its work.  Layers in us, bf16, groups of 128: 8
-            // tokens, 2 of 16 experts of 8192 x 2048 107 -> 97, 2 of 8, 4096 x
-            // 8192, 156 -> 144; 2 tokens (256 and 1024 workgroups) 42 -> 45 and 62
-            // -> 64; 2048 x 768, 8 of 256, 85 -> 88.
+            // a smaller part of its work.  Layers in us with 16 and with 32, bf16,
+            // groups of 128 and of 64: 2 of 8 experts of 4096 x 8192, 2 tokens
+            // (1024 workgroups) 78, 73 and 83, 79; 8 tokens (2048) 176, 152 and
+            // 180, 157; 64 tokens, 2 of 16, 4096 x 4096, 268, 230 and 276, 238;
+            // with 512 workgroups 51, 49 and 45, 45.  Groups of 32 win and lose a
+            // little (the same: 98, 103; 212, 212; 307, 284; 55, 60), and lose where
+            // rows are short (2048 x 1024, 6 of 64: 106, 126).
             if (GS && p.H >= 4096 && slots * cdiv(p.I, 32) >= 4 * kCUs)
                 up(std::integral_constant<int, GS ? 4 : 2>{});
             else
