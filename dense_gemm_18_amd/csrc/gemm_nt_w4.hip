@@ -117,9 +117,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restric
         u16x2 down = {0, 0};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            // (as elements of one vector the compiler dropped three of four)
-            uint32_t pair = raw.v[i >> 2][i & 3];
-            asm("" : "+v"(pair));
+            const uint32_t pair = raw.v[i >> 2][i & 3];
             up = __builtin_elementwise_max(up, __builtin_bit_cast(s16x2, pair));
             down = __builtin_elementwise_max(down, __builtin_bit_cast(u16x2, pair));
         }
