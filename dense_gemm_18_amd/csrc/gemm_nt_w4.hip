@@ -62,8 +62,8 @@ __device__ __forceinline__ float nearest(float x, float rs)
 // Quantisation, 32 consecutive elements of a row per lane: four 16-byte loads,
 // four packed words.  Lanes follow K, so a group is one lane or 2 or 4
 // neighbours, whose extremes take an exchange or two; a 64-byte block's words
-// leave by four lanes together.  2.5 bytes and more per element bound it: 81 us
-// for 16384 x 8192 bf16 in groups of 32 with zero points, 4.3 TB/s.  With 8
+// leave by four lanes together.  2.5 bytes and more per element bound it: 80 us
+// for 16384 x 8192 bf16 in groups of 32 with zero points, 4.4 TB/s.  With 8
 // elements per lane the group's arithmetic and the addresses, done by every
 // lane, were the bound (30 VALU instructions to an element, 115 us), though
 // 1024 x 1024 took 3.5 us instead of 4.2.  Elements past the last whole unit
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restric
 }
 
 // The reverse: one packed word, eight elements per lane.  Bound by writing:
-// 67 us for 16384 x 8192 bf16 in groups of 32, 5.3 TB/s in all.
+// 66 us for 16384 x 8192 bf16 in groups of 32, 5.4 TB/s in all.
 template <bool BF, int GS>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint32_t *__restrict__ Q,
                                                          const uint16_t *__restrict__ S,
@@ -390,6 +390,9 @@ int gemm_nt_w4(const void *A, const void *Q, const void *S, const void *Z, void 
     }
     const int64_t need = gemm_nt_w4_ws_size(M, N, K);
     if (need && ws_bytes >= need && lda == K && ldd == N) {
+        // one more rounding of the weights, to the type that the 16-bit product's
+        // matrix instructions take, and the weight unpacked once instead of for
+        // every 64 rows
         const std::lock_guard<std::mutex> both(launch_lock(workspace));
         const int rc = gemm_w4_dequantize(Q, S, Z, workspace, N, K, K, group, dtype, stream);
         if (rc != GEMM_OK)

@@ -441,9 +441,10 @@ using DownCore = Skinny<BF, GS, 2, MB, kDownWaves<GS>, kMoeWaves / kDownWaves<GS
 // h = silu(gate) * up for some of an expert's inner rows and all its slots.
 // One workgroup takes 8 * RB gate rows and their 8 * RB up rows, its waves split
 // the hidden size.  Bound by reading w13: 64 tokens, 2 of 16 experts, 4096 x
-// 4096 bf16, 203 us for 1.07 GB (5.3 TB/s); 16 tokens, 6 of 64, 2048 x 1024,
-// 73 us for the 50 experts or so that any token chose (5.7 TB/s); one token,
-// 8 of 64, 4096 x 1536 in 4 bits, 20 us for 50 MB, of which 17 are the loads.
+// 4096 bf16, 204 us for 1.07 GB (5.3 TB/s); 16 tokens, 6 of 64, 2048 x 1024,
+// 74 us for the 50 experts or so that any token chose (5.7 TB/s); one token,
+// 8 of 64, 4096 x 1536 in 4 bits, bf16, 22 us for 53 MB: a workgroup's first loads
+// wait for its expert, and unpacking takes the VALU for half of the time.
 template <bool BF, int GS, int RB, int MB>
 __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel(MoeArgs p)
 {
@@ -490,6 +491,7 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
                 const int i = i0 + 16 * r + n;
                 if (i < p.I) {
                     const float act = v[r] / (1.0f + expf(-v[r]));
+                    // in the type that the down product's matrix instructions take
                     p.h[(int64_t)slot(m) * p.I + i] = from_float<BF>(act * v[RB / 2 + r]);
                 }
             }
@@ -500,8 +502,8 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_up_kernel
 
 // y = W2 h for a block of an expert's hidden rows and all its slots, in fp32;
 // the last expert's workgroup of a block then forms each token's weighted
-// sum, over its slots in order.  As above, 125 us for 0.54 GB (4.3 TB/s) and 52
-// us (4.1 TB/s): K is short, so a workgroup's first loads and its end weigh more.
+// sum, over its slots in order.  As above, 121 us for 0.54 GB (4.5 TB/s) and 51
+// us (4.2 TB/s): K is short, so a workgroup's first loads and its end weigh more.
 template <bool BF, int GS, int MB>
 __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_down_kernel(MoeArgs p)
 {
@@ -571,7 +573,8 @@ __global__ void __launch_bounds__(kMoeWaves * 64, MB == 1 ? 4 : 2) moe_down_kern
 // One token: its slots' products are one long product, of the experts' rows
 // side by side with the gated rows end to end.  A workgroup takes 16 hidden
 // rows of every chosen expert, its waves share the (expert, piece of inner)
-// pairs, and the weighted sum is their join: nothing passes through memory.
+// pairs, and the weighted sum is their join, in the pairs' order: nothing passes
+// through memory.
 // 8 of 64 experts, 4096 x 1536 in 4 bits: 12 us, what its loads take; 2 of 8,
 // 1024 x 1024: 4.9 us, with the kernels for many tokens 7.2.
 template <bool BF, int GS>

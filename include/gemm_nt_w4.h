@@ -49,9 +49,11 @@ int64_t gemm_w4_packed_bytes(int64_t N, int64_t K);
  *        s = round16((hi - lo) / 15), z = clamp(rint(-lo / s), 0, 15),
  *        q = clamp(rint(w / s) + z, 0, 15).
  * round16 rounds to the 16-bit type, rint to the nearest even; the divisions
- * by s use the rounded s.  A group whose s rounds to 0 gets q = z = 8.  A
- * group that holds an infinity or a NaN gets s = NaN and q = z = 8, so its
- * products are NaN rather than wrong numbers.
+ * by s use the rounded s.  A group whose s rounds to 0 gets q = z = 8.  Where
+ * hi - lo passes fp32 (bfloat16 of both signs near its largest), s is
+ * infinite, q = z = 0 and the values are NaN: only symmetric groups take all
+ * of that type's range.  A group that holds an infinity or a NaN gets s = NaN
+ * and q = z = 8, so its products are NaN rather than wrong numbers.
  *
  * Returns GEMM_OK, GEMM_EINVAL (sizes out of range, ldw < K, an unknown group
  * or type, a NULL or misaligned pointer to data with at least one element, or
@@ -99,10 +101,17 @@ int gemm_nt_w4(const void *A, const void *Q, const void *S, const void *Z, void 
 
 #define GEMM_W4_MAX_LDA 16777215
 
-/* Rows up to which gemm_nt_w4 never uses a workspace.  Unpacking first took 206,
- * 79 and 59 us at 384 rows and 16384, 8192 and 4096 columns of 8192 (fp16),
- * unpacking on the way 181, 83 and 55; at 512 rows 201, 86 and 61 against 220,
- * 110 and 55. */
+/* Rows up to which gemm_nt_w4 never uses a workspace.  In us, K = 8192 in
+ * groups of 128 (32), unpacking on the way and unpacking first, by columns:
+ *                16384               8192               4096
+ *   256 fp16  112 (133) 179 (176)   57 (67)  77 (77)   30 (40) 41 (44)
+ *       bf16  123 (151) 178 (178)   63 (76)  74 (76)   33 (39) 40 (41)
+ *   384 fp16  166 (199) 207 (202)   84 (100) 77 (81)   57 (67) 59 (61)
+ *       bf16  184 (224) 207 (202)   93 (113) 76 (79)   62 (75) 60 (59)
+ *   512 fp16  221 (263) 209 (213)  111 (132) 89 (92)   57 (67) 62 (61)
+ *       bf16  244 (298) 209 (206)  123 (150) 83 (89)   63 (76) 61 (61)
+ * The rows alone decide, as they decide the rounding above: with 8192 columns
+ * unpacking first would win from 320 on, with 4096 and fp16 from about 600. */
 #define GEMM_W4_DIRECT_M 384
 
 /* Host-only: bytes of workspace gemm_nt_w4 can use for these sizes with

@@ -82,11 +82,13 @@ int moe_nt_route(const moe_nt_weights *w, const void *X, int32_t *ids, float *we
  *
  * All sums are held in fp32.  h_j is rounded to the 16-bit type (as a layer
  * that stores it between two products does; past the type's range it becomes
- * infinite); y is rounded once, after the weighted sum over j in order, so
- * results do not depend on timing.  Tokens run in chunks of 64, or of
- * 512 / topk where that is less: within a chunk an expert's weights are read
- * once for each 16 of its rows where there are 8 or fewer for each expert on
- * average, else once for each 32.
+ * infinite); y is rounded once, after the weighted sum.  That sum's order is
+ * fixed, so results do not depend on timing: over j where a chunk has two or
+ * more tokens; for one token over pieces of the products, each times its
+ * weight.  Tokens run in chunks of 64, or of 512 / topk where that is less:
+ * within a chunk an expert's weights are read once for each 16 of its rows
+ * where there are 8 or fewer for each expert on average, else once for each
+ * 32.
  *
  * topk in [1, MOE_MAX_TOPK]; router may be NULL.  Workspace and errors as
  * moe_nt_route.
