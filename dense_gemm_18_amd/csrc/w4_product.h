@@ -100,16 +100,22 @@ void launch_w4_piped(const W4Args &a, hipStream_t stream)
 //   64 rows, 64 x 64       31.8    29.7    28.1    27.4
 //            32 x 64       35.1    21.6    19.5    17.9
 //            32 x 32       47.2    25.6    15.8    13.9
-// Of the 16 x 64 tile the resident form has half the waves and less LDS, and wins
-// where that lets two workgroups share a compute unit and the groups' scales are
-// few: one row, in us, resident and chunked, by columns x K:
-//                      16384 x 8192  16384 x 16384  32768 x 4096  65536 x 4096
-//   fp16, groups of 128   17.2 15.4      37.9 33.5     17.6 18.5     34.5 37.9
-//                    64   22.0 15.9      46.0 34.3     18.7 19.2     35.7 39.8
-//                    32   28.3 17.8      63.3 38.5     26.0 23.0     50.7 45.5
-//   bf16, groups of 128   21.2 17.8      42.3 36.1     20.6 22.0     38.9 43.3
-//                    64   25.2 19.1      48.8 38.6     21.7 22.7     40.3 45.2
-//                    32   31.3 21.4      69.0 42.0     29.0 25.7     58.1 52.3
+// Of the 16 x 64 tile the chunked form has 16 waves and a compute unit to itself,
+// the resident one 8 waves and, with up to 80 KB of LDS, another beside it.  The
+// latter wins where there are more tiles than compute units and its scales, which
+// all have to be there before it starts, are few (64 groups).  Time of the chunked
+// form over the resident one's, one row, fp16 (bf16 is within 0.05 of it but for
+// groups of 64 at K = 8192, 0.91 to 0.96):
+//   K                     512   1024   2048   4096   8192  16384
+//   16384 columns, 256 tiles, one to a compute unit
+//     groups of 128      0.94   0.99   0.89   0.84   0.89   0.88
+//                32      1.00   0.96   0.91   0.70   0.65   0.61
+//   18000 to 65536 columns
+//     groups of 128      1.16+  1.19+  1.09+  1.04+  1.05+  0.89-0.96
+//                64      1.18+  1.18+  1.05+  1.02+  0.88-0.95  0.71+
+//                32      1.26+  1.20+  1.12+  0.83-0.91  0.62+  0.56+
+//   four rows, for which K = 8192 takes 82 KB and more
+//     groups of 128      1.16+  1.19+  1.08+  1.01+  0.85-0.90
 template <bool BF>
 void launch_w4(const W4Args &a, int group, hipStream_t stream)
 {
@@ -120,10 +126,10 @@ void launch_w4(const W4Args &a, int group, hipStream_t stream)
         constexpr int GS = decltype(gs)::value ? decltype(gs)::value : 128;
         const bool whole =
             a.M <= 16 && (int64_t)a.M * (cdiv(a.K, 128) * 256 + 16) <= kActBytes;
-        if constexpr (GS > 32)
-            if (whole && cdiv(a.N, 64) >= 2 * kCUs)
-                return launch_w4_resident<BF, GS, 4>(a, stream);
-        if (whole && !fills(16, 64)) {
+        const int beside = Skinny<BF, GS, 4, 1, kW4Waves, 1, true>::lds_bytes(a.M, a.K);
+        if (whole && cdiv(a.N, 64) > kCUs && cdiv(a.K, GS) <= 64 && beside <= 80 * 1024) {
+            launch_w4_resident<BF, GS, 4>(a, stream);
+        } else if (whole && !fills(16, 64)) {
             if (fills(16, 32))
                 launch_w4_resident<BF, GS, 2>(a, stream);
             else
