@@ -64,20 +64,20 @@ template <bool BF, int GS>
 constexpr float kUnscale = BF && GS != 0 ? 0x1p11f : 1.0f;
 
 // Eight 4-bit values of one packed word less their zero point (bfloat16: times
-// 2^-11), exact in either type.  A value in the low bits of the mantissa of 1024 (fp16) is that number
-// plus q, one four bits up 1024 + 16 q: one mask-and-or makes two of them, and
-// one shift serves all.
+// 2^-11), exact in either type.  A value in the low bits of the mantissa of 1024
+// (fp16) is that number plus q, one four bits up 1024 + 16 q: one mask-and-or makes
+// two of them, and one shift serves all.
 //
 // fp16 takes 1024 + z off both halves in one packed instruction, or has a packed
 // fma with 1/16 and 64 + z: 9 instructions for 8 weights.  bfloat16 has no packed
-// arithmetic on gfx950: a mixed fma reads each half as fp16 and leaves the
-// number in fp32, and one conversion packs two: 17 instructions.  (The matrix units could see
-// 128 + q, for 7, with (128 + z) times the activations' sum taken off afterwards.
-// Those sums are of terms up to 143 |A| where the result has 15 |A| or less, so an
-// activation that stands out left its rounding where its weight is 0.  Exact
-// numbers take 3 to 12 % longer up to 32 rows, 7 x 16384 x 8192 in groups of 128
-// 18.0 us for 16.7, and 3 to 8 % less from 64 rows on, whose matrix instructions for
-// the activations' sums they save.)
+// arithmetic on gfx950: a mixed fma reads each half as fp16 and leaves the number
+// in fp32, and the upper halves of two go together: 17 instructions.  (The matrix
+// units could see 128 + q, for 7, with (128 + z) times the activations' sum taken
+// off afterwards.  Those sums are of terms up to 143 |A| where the result has 15
+// |A| or less, so an activation that stands out left its rounding where its weight
+// is 0.  Exact numbers take 3 to 12 % longer up to 32 rows, 7 x 16384 x 8192 in
+// groups of 128 18.0 us for 16.7, up to 28 % in the resident tile, and 3 to 8 %
+// less from 64 rows on: matrix instructions for the activations' sums are saved.)
 // sz: 1024 + z in fp16, in its upper half.
 template <bool BF>
 __device__ __forceinline__ typename Elem<BF>::x8 unpack8(uint32_t w, uint32_t sz)
