@@ -1,5 +1,5 @@
 """Python binding of the C ABI in ``include/gemm_nt_f16.h``,
-``include/gemm_nt_w4.h`` and ``include/moe_nt.h``.
+``include/gemm_nt_w4.h``, ``include/moe_nt.h`` and ``include/rms_norm.h``.
 
 Argument marshalling only: every step of the GEMM runs in the HIP kernels of
 ``libgemm18.so``.  PyTorch supplies device memory and the current stream.
@@ -23,7 +23,10 @@ GEMM_FP8_E5M2 = 1
 
 GEMM_T_F16 = 0
 GEMM_T_BF16 = 1
+GEMM_T_F32 = 2
 MOE_RENORMALIZE = 1
+MOE_SOFTMAX = 0
+MOE_SIGMOID = 1
 
 # Every symbol the headers declare.
 EXPORTS = ("gemm_nt_f16", "gemm_nt_f16_strerror", "gemm_nt_f16_tile", "gemm_nt_f16_tile_coord",
@@ -32,7 +35,8 @@ EXPORTS = ("gemm_nt_f16", "gemm_nt_f16_strerror", "gemm_nt_f16_tile", "gemm_nt_f
            "gemm_nt_f16_kernel", "gemm_nt_f16_ws_noalloc", "gemm_nt_f16_acc16",
            "gemm_nt_f16_acc16_kernel", "gemm_w4_packed_bytes", "gemm_w4_quantize",
            "gemm_w4_dequantize", "gemm_nt_w4", "gemm_nt_w4_ws_size", "moe_nt_route",
-           "moe_nt_experts", "moe_nt_layer", "moe_nt_ws_size")
+           "moe_nt_experts", "moe_nt_layer", "moe_nt_ws_size", "moe_nt_choose",
+           "moe_nt_route_gated", "moe_nt_layer_gated", "rms_norm", "rms_norm_fp8")
 
 
 class moe_nt_weights(ctypes.Structure):
@@ -41,6 +45,13 @@ class moe_nt_weights(ctypes.Structure):
                                                "w2_scales", "w2_zeros")] + [
         (n, ctypes.c_int64) for n in ("experts", "hidden", "inner")] + [
         (n, ctypes.c_int32) for n in ("group", "dtype")]
+
+
+class moe_nt_gate(ctypes.Structure):
+    """``moe_nt_gate`` of include/moe_nt.h."""
+    _fields_ = [("bias", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("scoring", "groups", "topk_groups", "group_top")] + [
+        ("scale", ctypes.c_float)]
 
 
 class GemmError(RuntimeError):
@@ -129,6 +140,18 @@ def lib():
     L.moe_nt_layer.restype = ci
     L.moe_nt_ws_size.argtypes = [i64, mw, ci]
     L.moe_nt_ws_size.restype = i64
+    mg = ctypes.POINTER(moe_nt_gate)
+    L.moe_nt_choose.argtypes = [mg, vp, vp, vp, i64, i64, i64, ci, ci, ci, vp]
+    L.moe_nt_choose.restype = ci
+    L.moe_nt_route_gated.argtypes = [mw, mg, vp, vp, vp, i64, i64, ci, ci, vp, i64, vp]
+    L.moe_nt_route_gated.restype = ci
+    L.moe_nt_layer_gated.argtypes = [mw, mg, vp, vp, vp, vp, i64, i64, i64, ci, ci, vp, i64, vp]
+    L.moe_nt_layer_gated.restype = ci
+    cf = ctypes.c_float
+    L.rms_norm.argtypes = [vp] * 5 + [i64] * 6 + [cf, ci, vp]
+    L.rms_norm.restype = ci
+    L.rms_norm_fp8.argtypes = [vp] * 6 + [i64] * 6 + [cf, cf, ci, ci, vp]
+    L.rms_norm_fp8.restype = ci
     _lib = L
     return L
 
@@ -326,6 +349,47 @@ def moe_nt_layer(w: moe_nt_weights, X: int, D: int, ids: int, weights: int, T: i
 
 def moe_nt_ws_size(T: int, w: moe_nt_weights, topk: int) -> int:
     return lib().moe_nt_ws_size(T, w, topk)
+
+
+def moe_nt_choose(g: moe_nt_gate, logits: int, ids: int, weights: int, T: int, experts: int,
+                  ldl: int, topk: int, flags: int, dtype: int, stream: int = 0) -> int:
+    """Raw call of the choice from given logits; returns the C return code."""
+    return lib().moe_nt_choose(g, logits or None, ids or None, weights or None, T, experts, ldl,
+                               topk, flags, dtype, stream or None)
+
+
+def moe_nt_route_gated(w: moe_nt_weights, g: moe_nt_gate, X: int, ids: int, weights: int, T: int,
+                       ldx: int, topk: int, flags: int, workspace: int, ws_bytes: int,
+                       stream: int = 0) -> int:
+    """Raw call of the router with a gate; returns the C return code."""
+    return lib().moe_nt_route_gated(w, g, X or None, ids or None, weights or None, T, ldx, topk,
+                                    flags, workspace or None, ws_bytes, stream or None)
+
+
+def moe_nt_layer_gated(w: moe_nt_weights, g: moe_nt_gate, X: int, D: int, ids: int, weights: int,
+                       T: int, ldx: int, ldd: int, topk: int, flags: int, workspace: int,
+                       ws_bytes: int, stream: int = 0) -> int:
+    """Raw call of the whole layer with a gate; returns the C return code."""
+    return lib().moe_nt_layer_gated(w, g, X or None, D or None, ids or None, weights or None, T,
+                                    ldx, ldd, topk, flags, workspace or None, ws_bytes,
+                                    stream or None)
+
+
+def rms_norm(X: int, R: int, W: int, Y: int, S: int, T: int, H: int, ldx: int, ldr: int,
+             ldy: int, lds: int, eps: float, dtype: int, stream: int = 0) -> int:
+    """Raw call of the norm (R, W, S: 0 for none); returns the C return code."""
+    return lib().rms_norm(X or None, R or None, W or None, Y or None, S or None, T, H, ldx, ldr,
+                          ldy, lds, eps, dtype, stream or None)
+
+
+def rms_norm_fp8(X: int, R: int, W: int, Q: int, scales: int, S: int, T: int, H: int, ldx: int,
+                 ldr: int, ldq: int, lds: int, eps: float, scale: float, format: int, dtype: int,
+                 stream: int = 0) -> int:
+    """Raw call of the norm into FP8 (R, W, S: 0 for none; scales 0: by ``scale``); returns
+    the C return code."""
+    return lib().rms_norm_fp8(X or None, R or None, W or None, Q or None, scales or None,
+                              S or None, T, H, ldx, ldr, ldq, lds, eps, scale, format, dtype,
+                              stream or None)
 
 
 # ---- tensor-level convenience ----------------------------------------------

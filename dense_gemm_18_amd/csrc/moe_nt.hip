@@ -1,5 +1,6 @@
 // moe_nt.hip -- C entry points of the mixture-of-experts layer.  Kernels:
-// moe_product.h, skinny.h.
+// moe_product.h, skinny.h, moe_gate.h.
+#include "moe_gate.h"
 #include "moe_product.h"
 
 namespace {
@@ -188,6 +189,25 @@ int check_across(const moe_nt_weights *w, const int32_t *ids, const float *weigh
                : GEMM_EINVAL;
 }
 
+// Likewise of a gate: its values, and its bias against all that is written (D or NULL).
+int check_gate(const moe_nt_weights *w, const moe_nt_gate *g, const int32_t *ids,
+               const float *weights, const void *D, int64_t T, int64_t ldd, int topk,
+               const void *ws, int64_t ws_bytes)
+{
+    if (!gemm18_moe_gate_ok(g, w->experts, topk))
+        return GEMM_EINVAL;
+    const uint64_t slots = (uint64_t)T * (uint64_t)topk * 4u;
+    const Span bias{g->bias, g->bias ? (uint64_t)w->experts * 4u : 0u};
+    const Span out[4] = {{ids, slots},
+                         {weights, slots},
+                         {D, D ? span_bytes(T, w->hidden, ldd) : 0u},
+                         {ws, (uint64_t)ws_bytes}};
+    for (const Span &o : out)
+        if (overlap(o.p, o.n, bias.p, bias.n))
+            return GEMM_EINVAL;
+    return GEMM_OK;
+}
+
 MoeArgs common_args(const moe_nt_weights *w, const void *X, const int32_t *ids,
                     const float *weights, int64_t T, int64_t ldx, int topk, void *ws)
 {
@@ -232,9 +252,10 @@ MoeLaunch launches(const moe_nt_weights *w)
     return w->dtype == GEMM_T_BF16 ? gemm18_moe_bf16() : gemm18_moe_f16();
 }
 
-// The router, the experts or both, a chunk of tokens at a time.
+// The router, the experts or both, a chunk of tokens at a time.  With a gate the router
+// leaves its logits, as for a late choice, and a kernel of its own chooses.
 int run(const moe_nt_weights *w, MoeArgs p, int64_t T, bool route, bool experts,
-        hipStream_t stream)
+        hipStream_t stream, const GateArgs *gate = nullptr)
 {
     if (!experts)
         p.plan = nullptr;
@@ -243,10 +264,28 @@ int run(const moe_nt_weights *w, MoeArgs p, int64_t T, bool route, bool experts,
     for (int64_t done = 0; next_chunk(p, T, done);) {
         p.parts = route_parts(p.H, p.E, p.T);       // no more than the workspace has
         p.late = route && experts && p.T == 1 && p.E <= kLateExperts;
-        if (route)
+        if (gate) {
+            MoeArgs r = p;
+            r.late = 1;
+            go.route(r, stream);
+            GateArgs a = *gate;
+            a.logits = p.logits;
+            a.ids = p.ids;
+            a.weights = p.weights;
+            a.T = p.T;
+            a.E = p.E;
+            a.topk = p.topk;
+            a.dtype = GEMM_T_F32;
+            a.ldl = p.E;
+            a.parts = p.parts;
+            a.part_stride = (int64_t)p.T * p.E;
+            gemm18_moe_gate(a, stream);
+            p.late = 0;
+        } else if (route) {
             go.route(p, stream);
+        }
         if (experts)
-            go.experts(p, w->group, route, stream);
+            go.experts(p, w->group, route && !gate, stream);
     }
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ELAUNCH;
 }
@@ -304,6 +343,41 @@ int moe_nt_layer(const moe_nt_weights *w, const void *X, void *D, int32_t *ids, 
     p.D = (uint16_t *)D;
     p.ldd = ldd;
     return run(w, p, T, true, true, stream);
+}
+
+int moe_nt_route_gated(const moe_nt_weights *w, const moe_nt_gate *g, const void *X,
+                       int32_t *ids, float *weights, int64_t T, int64_t ldx, int topk, int flags,
+                       void *workspace, int64_t ws_bytes, hipStream_t stream)
+{
+    int rc = check_route(w, X, ids, weights, T, ldx, topk, flags, workspace, ws_bytes);
+    if (rc == GEMM_OK)
+        rc = check_gate(w, g, ids, weights, nullptr, T, 0, topk, workspace, ws_bytes);
+    if (rc != GEMM_OK || T == 0)
+        return rc;
+    const GateArgs gate = gemm18_moe_gate_args(g, flags);
+    return run(w, common_args(w, X, ids, weights, T, ldx, topk, workspace), T, true, false,
+               stream, &gate);
+}
+
+int moe_nt_layer_gated(const moe_nt_weights *w, const moe_nt_gate *g, const void *X, void *D,
+                       int32_t *ids, float *weights, int64_t T, int64_t ldx, int64_t ldd,
+                       int topk, int flags, void *workspace, int64_t ws_bytes,
+                       hipStream_t stream)
+{
+    int rc = check_route(w, X, ids, weights, T, ldx, topk, flags, workspace, ws_bytes);
+    if (rc == GEMM_OK)
+        rc = check_experts(w, X, ids, weights, D, T, ldx, ldd, topk, workspace, ws_bytes);
+    if (rc == GEMM_OK)
+        rc = check_across(w, ids, weights, D, T, ldd, topk);
+    if (rc == GEMM_OK)
+        rc = check_gate(w, g, ids, weights, D, T, ldd, topk, workspace, ws_bytes);
+    if (rc != GEMM_OK || T == 0)
+        return rc;
+    MoeArgs p = common_args(w, X, ids, weights, T, ldx, topk, workspace);
+    p.D = (uint16_t *)D;
+    p.ldd = ldd;
+    const GateArgs gate = gemm18_moe_gate_args(g, flags);
+    return run(w, p, T, true, true, stream, &gate);
 }
 
 } // extern "C"

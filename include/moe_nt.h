@@ -105,6 +105,61 @@ int moe_nt_layer(const moe_nt_weights *w, const void *X, void *D, int32_t *ids, 
 /* Host-only: bytes of workspace the calls above need (0: sizes out of range). */
 int64_t moe_nt_ws_size(int64_t T, const moe_nt_weights *w, int topk);
 
+/*
+ * Other ways from a token's logits to its experts, over E experts:
+ *
+ *   score[e] = softmax(logits)[e], or 1 / (1 + exp(-logits[e]))
+ *   choice[e] = score[e] + bias[e]
+ *   the experts fall into `groups` runs of E / groups; a group's value is the sum
+ *   of its group_top largest choices; the topk_groups groups with the largest
+ *   values stay, equal ones by rising index
+ *   e_0, e_1, ...: the topk experts of those groups with the largest choices, in
+ *   falling order, equal ones by rising index
+ *   w_j = scale * score[e_j], with MOE_RENORMALIZE over the sum of the chosen scores
+ *
+ * Without a bias and with group_top 1 the order of the choices is that of the
+ * logits; otherwise scores, choices and the groups' values are formed in 64 bits,
+ * so that which experts are chosen does not hang on a rounding.  Weights are
+ * formed in 64 bits and rounded to fp32 once; a softmax's sum over all experts is
+ * formed in fp32 where the choices are not.
+ *
+ * A row with a NaN logit, and with softmax one whose largest logit is infinite,
+ * gets NaN weights and topk distinct valid ids.  A NaN choice comes after every
+ * other.  Where the chosen scores' sum is 0, renormalised weights are 0.
+ */
+#define MOE_SOFTMAX 0
+#define MOE_SIGMOID 1
+#define MOE_MAX_GROUPS 64
+#define GEMM_T_F32 2      /* a type of logits only */
+
+typedef struct moe_nt_gate {
+    const float *bias;        /* one for each expert, in device memory, or NULL: 0 */
+    int32_t scoring;          /* MOE_SOFTMAX or MOE_SIGMOID */
+    int32_t groups;           /* in [1, MOE_MAX_GROUPS], a divisor of E */
+    int32_t topk_groups;      /* in [1, groups], with topk <= topk_groups * E / groups */
+    int32_t group_top;        /* 1 or 2, at most E / groups */
+    float scale;              /* finite */
+} moe_nt_gate;
+
+/*
+ * The choice from given logits: T rows of `experts` values of the type `dtype`
+ * (GEMM_T_F16, GEMM_T_BF16 or GEMM_T_F32), row t at logits + t * ldl elements
+ * (experts <= ldl).  Any number of rows; no workspace.  ids and weights as
+ * moe_nt_route, whose limits on experts, topk and flags hold; errors as there.
+ */
+int moe_nt_choose(const moe_nt_gate *g, const void *logits, int32_t *ids, float *weights,
+                  int64_t T, int64_t experts, int64_t ldl, int topk, int flags, int dtype,
+                  hipStream_t stream);
+
+/* moe_nt_route and moe_nt_layer with that choice; the logits are summed in fp32. */
+int moe_nt_route_gated(const moe_nt_weights *w, const moe_nt_gate *g, const void *X,
+                       int32_t *ids, float *weights, int64_t T, int64_t ldx, int topk, int flags,
+                       void *workspace, int64_t ws_bytes, hipStream_t stream);
+int moe_nt_layer_gated(const moe_nt_weights *w, const moe_nt_gate *g, const void *X, void *D,
+                       int32_t *ids, float *weights, int64_t T, int64_t ldx, int64_t ldd,
+                       int topk, int flags, void *workspace, int64_t ws_bytes,
+                       hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
