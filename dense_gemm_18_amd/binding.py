@@ -8,6 +8,7 @@ A missing library raises; there is no fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from pathlib import Path
 
 _LIB_PATH = Path(__file__).resolve().parent / "libgemm18.so"
@@ -31,7 +32,7 @@ MOE_SIGMOID = 1
 # Every symbol the headers declare.
 EXPORTS = ("gemm_nt_f16", "gemm_nt_f16_strerror", "gemm_nt_f16_tile", "gemm_nt_f16_tile_coord",
            "gemm_nt_bf16", "gemm_nt_f16_ex", "gemm_nt_f16_ws", "gemm_nt_f16_ws_size", "gemm_nt_f16_ws_tile",
-           "gemm_nt_f16_ws_items", "gemm_nt_fp8", "gemm_nt_fp8_cs", "gemm_nt_fp8_tile",
+           "gemm_nt_f16_ws_items", "gemm_nt_fp8", "gemm_nt_fp8_cs", "gemm_nt_fp8_rs", "gemm_nt_fp8_tile",
            "gemm_nt_f16_kernel", "gemm_nt_f16_ws_noalloc", "gemm_nt_f16_acc16",
            "gemm_nt_f16_acc16_kernel", "gemm_w4_packed_bytes", "gemm_w4_quantize",
            "gemm_w4_dequantize", "gemm_nt_w4", "gemm_nt_w4_ws_size", "moe_nt_route",
@@ -118,6 +119,9 @@ def lib():
     L.gemm_nt_fp8_cs.argtypes = [vp, vp, vp, i64, i64, i64, ctypes.c_float, vp, ctypes.c_int,
                                  ctypes.c_int, vp]
     L.gemm_nt_fp8_cs.restype = ctypes.c_int
+    L.gemm_nt_fp8_rs.argtypes = [vp, vp, vp, i64, i64, i64, ctypes.c_float, vp, vp, ctypes.c_int,
+                                 ctypes.c_int, ctypes.c_int, vp]
+    L.gemm_nt_fp8_rs.restype = ctypes.c_int
     L.gemm_nt_fp8_tile.argtypes = [i64, i64, i64, ctypes.c_int, ip, ip]
     L.gemm_nt_fp8_tile.restype = ctypes.c_int
     ci = ctypes.c_int
@@ -286,6 +290,16 @@ def gemm_nt_fp8_cs(A: int, B: int, D: int, M: int, N: int, K: int, a_scale: floa
                                 b_scale or None, a_format, b_format, stream or None)
 
 
+def gemm_nt_fp8_rs(A: int, B: int, D: int, M: int, N: int, K: int, scale: float, a_scale: int,
+                   b_scale: int, a_format: int = GEMM_FP8_E4M3, b_format: int = GEMM_FP8_E4M3,
+                   dtype: int = GEMM_T_F16, stream: int = 0) -> int:
+    """Raw call of the FP8 form with a scale for each row of A and of B (device addresses of
+    M and N fp32 values, 0: none) and D of the 16-bit type ``dtype``; returns the C return
+    code."""
+    return lib().gemm_nt_fp8_rs(A or None, B or None, D or None, M, N, K, scale, a_scale or None,
+                                b_scale or None, a_format, b_format, dtype, stream or None)
+
+
 def gemm_nt_fp8_tile(M: int, N: int, K: int, aligned16: bool = True):
     """(BM, BN) of the FP8 form's tile; (0, 0) for the plain kernel."""
     bm, bn = ctypes.c_int(), ctypes.c_int()
@@ -394,65 +408,93 @@ def rms_norm_fp8(X: int, R: int, W: int, Q: int, scales: int, S: int, T: int, H:
 
 # ---- tensor-level convenience ----------------------------------------------
 
-def gemm_nt(A, B, out=None, stream=None, scale: float = 1.0, b_scale=None):
+_FP8 = {}
+
+
+def _scale_of(x, n, what, device):
+    """The address of ``n`` contiguous float32 values on ``device``."""
+    import torch
+    if x.dtype != torch.float32 or x.numel() != n or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{what} must be a contiguous float32 tensor of {n} values on A's device")
+    return x.data_ptr()
+
+
+def gemm_nt(A, B, out=None, stream=None, scale: float = 1.0, b_scale=None, a_scale=None,
+            dtype=None):
     """D = A @ B.T for CUDA (HIP) tensors A [M, K] and B [N, K].
 
     float16 A and B call gemm_nt_f16 (D float16), bfloat16 call gemm_nt_bf16
     (D bfloat16); float8_e4m3fn / float8_e5m2 operands (the two may differ)
     call gemm_nt_fp8 with ``scale`` (D float16), or, given ``b_scale`` (a
     contiguous float32 tensor of N per-row scales of B on the same device),
-    gemm_nt_fp8_cs with a_scale = ``scale``.  ``out`` (optional) is a
+    gemm_nt_fp8_cs with a_scale = ``scale``.  Given ``a_scale`` (likewise M
+    per-row scales of A, as ``rms_norm_fp8`` returns them) or ``dtype``
+    (float16 or bfloat16, D's type), FP8 operands call gemm_nt_fp8_rs with all
+    three.  ``out`` (optional) is a
     contiguous [M, N] tensor of D's dtype on the same device.  The call is
     enqueued on ``stream`` (default: A's device's current stream; a stream
     given must belong to A's device), with A's device made current for it.
     """
     import torch
 
-    fp8 = {torch.float8_e4m3fn: GEMM_FP8_E4M3, torch.float8_e5m2: GEMM_FP8_E5M2}
-    if A.dtype in fp8 and B.dtype in fp8:
-        out_dtype = torch.float16
+    if not _FP8:
+        _FP8.update({torch.float8_e4m3fn: GEMM_FP8_E4M3, torch.float8_e5m2: GEMM_FP8_E5M2})
+    fp8 = A.dtype in _FP8 and B.dtype in _FP8
+    if fp8:
+        out_dtype = torch.float16 if dtype is None else dtype
+        if out_dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"unsupported dtype {out_dtype} of D: float16 or bfloat16")
     elif A.dtype == B.dtype and A.dtype in (torch.float16, torch.bfloat16):
         out_dtype = A.dtype
+        if b_scale is not None:
+            raise TypeError("b_scale applies to FP8 operands only")
+        if a_scale is not None or dtype not in (None, out_dtype):
+            raise TypeError("a_scale and another dtype of D apply to FP8 operands only")
     else:
         raise TypeError(f"unsupported operand dtypes {A.dtype} and {B.dtype}: both float16, "
                         "both bfloat16, or float8_e4m3fn / float8_e5m2")
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
         raise ValueError(f"shapes {tuple(A.shape)} and {tuple(B.shape)} are not [M,K] and [N,K]")
-    if not (A.is_cuda and B.is_cuda) or A.device != B.device:
+    device = A.device
+    if not (A.is_cuda and B.is_cuda) or device != B.device:
         raise ValueError("A and B must be on the same GPU")
     if not (A.is_contiguous() and B.is_contiguous()):
         raise ValueError("A and B must be contiguous row-major")
     M, K = A.shape
     N = B.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=A.device)
+        # the tensor is the call's stream's
+        with nullcontext() if stream is None else torch.cuda.stream(stream):
+            out = torch.empty((M, N), dtype=out_dtype, device=device)
     elif (out.dtype != out_dtype or tuple(out.shape) != (M, N) or not out.is_contiguous()
-          or out.device != A.device):
+          or out.device != device):
         raise ValueError(f"out must be a contiguous {out_dtype} [M, N] tensor on A's device")
-    s = stream if stream is not None else torch.cuda.current_stream(A.device)
+    # the raw handle: torch.cuda.current_stream would build an object around it
+    s = (stream.cuda_stream if stream is not None
+         else torch._C._cuda_getCurrentRawStream(device.index))
     pa, pb, pd = A.data_ptr(), B.data_ptr(), out.data_ptr()
-    if b_scale is not None:
-        if A.dtype not in fp8:
-            raise TypeError("b_scale applies to FP8 operands only")
-        if (b_scale.dtype != torch.float32 or b_scale.numel() != N or not b_scale.is_contiguous()
-                or b_scale.device != A.device):
-            raise ValueError("b_scale must be a contiguous float32 tensor of N values on A's device")
+    b_ptr = None if b_scale is None else _scale_of(b_scale, N, "b_scale", device)
     # the library launches on the current device: make it the operands' one
-    with torch.cuda.device(A.device):
-        if A.dtype in fp8 and b_scale is not None:
+    with (nullcontext() if device.index == torch.cuda.current_device()
+          else torch.cuda.device(device)):
+        if fp8 and (a_scale is not None or dtype is not None):
+            name = "gemm_nt_fp8_rs"
+            a_ptr = None if a_scale is None else _scale_of(a_scale, M, "a_scale", device)
+            rc = gemm_nt_fp8_rs(pa, pb, pd, M, N, K, scale, a_ptr, b_ptr, _FP8[A.dtype],
+                                _FP8[B.dtype],
+                                GEMM_T_BF16 if out_dtype == torch.bfloat16 else GEMM_T_F16, s)
+        elif fp8 and b_scale is not None:
             name = "gemm_nt_fp8_cs"
-            rc = gemm_nt_fp8_cs(pa, pb, pd, M, N, K, scale, b_scale.data_ptr(), fp8[A.dtype],
-                                fp8[B.dtype], s.cuda_stream)
-        elif A.dtype in fp8:
+            rc = gemm_nt_fp8_cs(pa, pb, pd, M, N, K, scale, b_ptr, _FP8[A.dtype], _FP8[B.dtype], s)
+        elif fp8:
             name = "gemm_nt_fp8"
-            rc = gemm_nt_fp8(pa, pb, pd, M, N, K, scale, fp8[A.dtype], fp8[B.dtype],
-                             s.cuda_stream)
+            rc = gemm_nt_fp8(pa, pb, pd, M, N, K, scale, _FP8[A.dtype], _FP8[B.dtype], s)
         elif A.dtype == torch.bfloat16:
             name = "gemm_nt_bf16"
-            rc = gemm_nt_bf16(pa, pb, pd, M, N, K, s.cuda_stream)
+            rc = gemm_nt_bf16(pa, pb, pd, M, N, K, s)
         else:
             name = "gemm_nt_f16"
-            rc = gemm_nt_f16(pa, pb, pd, M, N, K, s.cuda_stream)
+            rc = gemm_nt_f16(pa, pb, pd, M, N, K, s)
     if rc != GEMM_OK:
         raise GemmError(rc, name)
     return out

@@ -3,7 +3,8 @@
 //
 //   D[m,n] = scale * sum_k A[m,k] * B[n,k]     A, B: OCP E4M3 or E5M2 bytes,
 //                                               D: fp16, fp32 accumulation
-//   (or scale * col_scale[n] per column: per-channel weight scales)
+//   (or scale * col_scale[n] per column: per-channel weight scales; with per-row
+//   scales of A too, times row_scale[m], and D also in bfloat16)
 //
 // FP8 operands with a per-tensor scale kept in fp32 and applied in the
 // epilogue follow the GEMM-optimisation article at www.lqnn.cn (news/123226),
@@ -15,11 +16,26 @@
 
 #include "gemm_kernels.h"
 
+// What a product's sums are multiplied by, and D's type.
+struct Fp8Scales {
+    float scale;
+    const float *col, *row;    // may be null
+    bool bf;
+};
+
 // Launches the product for format pair F8 = 1 + fa + 2 * fb with fb = 1 (B in
 // E5M2); defined in gemm_nt_fp8_b5.hip.  Not exported from the library.
 __attribute__((visibility("hidden"))) void gemm18_fp8_launch_b5(
-    int f8, const void *A, const void *B, void *D, int64_t M, int64_t N, int64_t K, float scale,
-    const float *col_scale, hipStream_t s);
+    int f8, const void *A, const void *B, void *D, int64_t M, int64_t N, int64_t K,
+    const Fp8Scales &scales, hipStream_t s);
+// The same for F8 from 5 to 8, the pairs 1 to 4 with row scales; one translation unit for
+// each format of B.
+__attribute__((visibility("hidden"))) void gemm18_fp8_launch_rs(
+    int f8, const void *A, const void *B, void *D, int64_t M, int64_t N, int64_t K,
+    const Fp8Scales &scales, hipStream_t s);
+__attribute__((visibility("hidden"))) void gemm18_fp8_launch_rs_b5(
+    int f8, const void *A, const void *B, void *D, int64_t M, int64_t N, int64_t K,
+    const Fp8Scales &scales, hipStream_t s);
 
 namespace {
 
@@ -54,7 +70,13 @@ void launch_fp8_dma(const void *A, const void *B, void *D, int M, int N, int Kp,
     // As for 16-bit operands: an operand read once per call (one tile row:
     // B; one tile column: A) streams with the non-temporal policy.
     auto go_nt = [&](auto ktail) {
-        if constexpr (C::BM <= 128 && C::LB == 16) {
+        if constexpr (C::BM <= 128 && C::LB == 16 && F8 > 4) {
+            // with row scales, few rows against many columns only
+            if (tm == 1) {
+                go(ktail, std::integral_constant<int, 2>{});
+                return;
+            }
+        } else if constexpr (C::BM <= 128 && C::LB == 16) {
             switch ((tn == 1 ? 1 : 0) | (tm == 1 ? 2 : 0)) {
             case 1: go(ktail, std::integral_constant<int, 1>{}); return;
             case 2: go(ktail, std::integral_constant<int, 2>{}); return;
@@ -124,9 +146,9 @@ Tile fp8_tile(int64_t M, int64_t N, int64_t K, int lb)
 
 template <int F8>
 void launch_fp8(const void *A, const void *B, void *D, int64_t M, int64_t N, int64_t K,
-                float scale, const float *col_scale, hipStream_t s)
+                const Fp8Scales &x, hipStream_t s)
 {
-    const Epi epi{nullptr, nullptr, scale, 0.0f, col_scale};
+    const Epi epi{nullptr, nullptr, x.scale, 0.0f, x.col, x.row, x.bf};
     const int lb = fp8_load_bytes(A, B, M, N, K);
     const int vec = store_mode(D, N);
     const int m = (int)M, n = (int)N, kp = (int)(K / 2);

@@ -73,7 +73,9 @@ __device__ __forceinline__ f32x16 mfma32(typename Elem<BF>::x8 b, typename Elem<
 
 // FP8 operands (OCP E4M3 or E5M2, one format per operand): F8 = 1 + fa +
 // 2 * fb with fa, fb the formats of A and B (0: E4M3, 1: E5M2, the codes of
-// the f8f6f4 MFMA's format fields); F8 = 0 for 16-bit operands.  The MFMA is
+// the f8f6f4 MFMA's format fields), and 4 more for an epilogue with row scales,
+// kernels of their own because its registers made the 256 x 256 one without
+// spill; F8 = 0 for 16-bit operands.  The MFMA is
 // v_mfma_f32_16x16x128_f8f6f4 (32 bytes of K per lane and operand, no
 // block scales: the per-tensor scale is applied in the epilogue).  B is the
 // first operand as in mfma16; any assignment of K bytes to lanes gives the
@@ -81,7 +83,7 @@ __device__ __forceinline__ f32x16 mfma32(typename Elem<BF>::x8 b, typename Elem<
 template <int F8>
 __device__ __forceinline__ f32x4 mfma_f8(i32x8 b, i32x8 a, f32x4 c)
 {
-    constexpr int fa = (F8 - 1) & 1, fb = (F8 - 1) >> 1;
+    constexpr int fa = (F8 - 1) & 1, fb = (F8 - 1) >> 1 & 1;
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, fb, fa, 0, 0, 0, 0);
 }
 
@@ -164,6 +166,11 @@ struct Epi {
     // FP8 only: N per-column scales; column n is scaled by alpha * col_scale[n]
     // (formed in fp32) instead of alpha.  Null everywhere else.
     const float *col_scale;
+    // The kernels with row scales (F8 > 4) only: M of them; row m's sums are scaled by
+    // alpha * col_scale[n] (or by alpha) first and by row_scale[m] then.  Null: none.
+    // D holds bfloat16 if `bf` is set.
+    const float *row_scale;
+    int bf;
 };
 
 // Four values of row p at columns n .. n+3 as fp32; columns >= N read as 0
@@ -372,9 +379,10 @@ __device__ __forceinline__ f16x4 load4h(const _Float16 *p, int n, int N, int vec
 // or the bias is absent, which keeps their registers and code out (the FP8
 // kernels, whose epilogue is a scale alone).  COLS: e.col_scale is present
 // (FP8 with per-channel scales; the caller branches on it once, so that no
-// form computes the other's arithmetic).
+// form computes the other's arithmetic).  ROWS: the row form, whose row_scale and
+// col_scale may each be absent, and whose results are of either 16-bit type.
 template <int TM, int TN, class Get, bool WITH_C = true, bool COLS = false, bool WITH_BIAS = true,
-          bool STAGED = false>
+          bool STAGED = false, bool ROWS = false>
 __device__ __forceinline__ void store_blocks16_epi(Get get, _Float16 *__restrict__ D, int M,
                                                    int N, int mbase, int nbase, int lane,
                                                    int vec, const Epi &e, char *stage = nullptr)
@@ -389,8 +397,21 @@ __device__ __forceinline__ void store_blocks16_epi(Get get, _Float16 *__restrict
         for (int j = 0; j < TN; ++j) {
             const int n = nbase + 16 * j + 4 * fq;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                sv[j][r] = e.alpha * (n + r < N ? e.col_scale[n + r] : 0.0f);
+            for (int r = 0; r < 4; ++r) {
+                if constexpr (ROWS)
+                    sv[j][r] = e.col_scale && n + r < N ? e.alpha * e.col_scale[n + r] : e.alpha;
+                else
+                    sv[j][r] = e.alpha * (n + r < N ? e.col_scale[n + r] : 0.0f);
+            }
+        }
+    }
+    // the rows' factors, on their way together
+    float rv[ROWS ? TM : 1];
+    if constexpr (ROWS) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int m = mbase + 16 * i + frow;
+            rv[i] = e.row_scale && m < M ? e.row_scale[m] : 1.0f;
         }
     }
     if (has_bias) {
@@ -425,6 +446,8 @@ __device__ __forceinline__ void store_blocks16_epi(Get get, _Float16 *__restrict
                 u = v * sv[j];
             else
                 u = v * e.alpha;
+            if constexpr (ROWS)
+                u = u * rv[i];
             if (has_c) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
@@ -436,9 +459,17 @@ __device__ __forceinline__ void store_blocks16_epi(Get get, _Float16 *__restrict
                     u[r] = u[r] + (float)bv[j][r];
             }
             f16x4 h;
+            if (ROWS && e.bf) {
+                bf16x4 b;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                h[r] = (_Float16)u[r];
+                for (int r = 0; r < 4; ++r)
+                    b[r] = (__bf16)u[r];
+                h = __builtin_bit_cast(f16x4, b);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    h[r] = (_Float16)u[r];
+            }
             if constexpr (STAGED) {
                 *(u32x2 *)(stage + Stage16<TM, TN>::offset(16 * i + frow, 16 * j + 4 * fq)) =
                     __builtin_bit_cast(u32x2, h);
@@ -753,6 +784,7 @@ gemm_nt_dma_kernel(const typename Elem<BF>::T *__restrict__ A,
     // back to back, before the fp16 rounding).  The two slices of a step
     // then split the blocks by rows instead of the K-step by halves.
     constexpr bool WIDE = F8 != 0 || H16;
+    [[maybe_unused]] constexpr bool RS = F8 > 4;     // the epilogue with row scales
     using X8 = typename std::conditional<WIDE, i32x8, typename Elem<BF>::x8>::type;
     static_assert(!WIDE || (!BF && !SK && !C::SPLIT && C::MF == 16 && C::BK == 64 &&
                             C::SLICES == 2 && C::NSTAGE % 2 == 0 && C::TM % 2 == 0),
@@ -1204,7 +1236,11 @@ gemm_nt_dma_kernel(const typename Elem<BF>::T *__restrict__ A,
                 char *stage = smem + wave * St::BYTES;
                 auto get = [&](int i, int j) G18_INLINE { return accf(i, j); };
                 if constexpr (EPI) {     // FP8: the scale alone, or per-column scales
-                    if (epi.col_scale)
+                    if constexpr (RS)
+                        store_blocks16_epi<C::TM, C::TN, decltype(get), false, true, false, true,
+                                           true>(get, D, M, N, mb, nb, lane, vec_store, epi,
+                                                 stage);
+                    else if (epi.col_scale)
                         store_blocks16_epi<C::TM, C::TN, decltype(get), false, true, false, true>(
                             get, D, M, N, mb, nb, lane, vec_store, epi, stage);
                     else
@@ -1224,7 +1260,10 @@ gemm_nt_dma_kernel(const typename Elem<BF>::T *__restrict__ A,
                 store_blocks<C::TM, C::TN>(get, D, M, N, mb, nb, lane, vec_store,
                                            EpiFin{epi, N, vec_store});
             else if constexpr (F8 != 0) {
-                if (epi.col_scale)
+                if constexpr (RS)
+                    store_blocks16_epi<C::TM, C::TN, decltype(get), false, true, false, false,
+                                       true>(get, D, M, N, mb, nb, lane, vec_store, epi);
+                else if (epi.col_scale)
                     store_blocks16_epi<C::TM, C::TN, decltype(get), false, true, false>(
                         get, D, M, N, mb, nb, lane, vec_store, epi);
                 else
@@ -1517,7 +1556,7 @@ gemm_nt_dma_kernel(const typename Elem<BF>::T *__restrict__ A,
 }
 
 // K == 0 with the fused epilogue: D = alpha * (+0) + beta * C + bias (with FP8
-// column scales, alpha * col_scale[n] in place of alpha).
+// column scales, alpha * col_scale[n] in place of alpha; with row scales times row m's).
 [[maybe_unused]] __global__ void epilogue_only_kernel(_Float16 *__restrict__ D, Epi e, int64_t M, int64_t N)
 {
     const int64_t count = M * N;
@@ -1529,7 +1568,9 @@ gemm_nt_dma_kernel(const typename Elem<BF>::T *__restrict__ A,
             v = v + e.beta * (float)e.C[i];
         if (e.bias)
             v = v + (float)e.bias[i % N];
-        D[i] = (_Float16)v;
+        if (e.row_scale)
+            v = v * e.row_scale[i / N];
+        D[i] = e.bf ? __builtin_bit_cast(_Float16, (__bf16)v) : (_Float16)v;
     }
 }
 

@@ -137,10 +137,24 @@ __device__ __forceinline__ u32x4 load_b128(__amdgpu_buffer_rsrc_t rs, uint32_t o
 constexpr int kActBytes = 66 * 1024;
 constexpr int kScaleBytes = 32 * 1024;
 
+// The matrix instruction of pairs of 16-byte pieces of FP8 rows; F8 = 1 + fa + 2 * fb with
+// the formats of the activations and of the weights (0: E4M3, 1: E5M2).
+template <int F8>
+__device__ __forceinline__ f32x4 mfma_pair(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x4 c)
+{
+    constexpr int fa = (F8 - 1) & 1, fb = (F8 - 1) >> 1;
+    const auto both = [](u32x4 x, u32x4 y) G18_INLINE {
+        return __builtin_bit_cast(i32x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(both(a0, a1), both(b0, b1), c, fa, fb,
+                                                            0, 0, 0, 0);
+}
+
 // One workgroup's product.  GS: 0 for 16-bit weights, else the group.
 // JOINED: the workgroup's weight rows follow each other; else (RB even, NW == 1)
-// each half of the blocks starts at a row of its own.
-template <bool BF, int GS, int RB, int MB, int KW, int NW, bool JOINED>
+// each half of the blocks starts at a row of its own.  F8 (GS 0): activations and weights
+// are rows of pairs of FP8 bytes, K counts the pairs.
+template <bool BF, int GS, int RB, int MB, int KW, int NW, bool JOINED, int F8 = 0>
 struct Skinny {
     using x8 = typename Elem<BF>::x8;
     static constexpr int kThreads = KW * NW * 64;
@@ -389,6 +403,18 @@ struct Skinny {
                     for (int j = 0; j < 4; ++j)
                         b.v[u][r][j] = mend(b.v[u][r][j], left - 32 * j, end);
                 }
+            }
+            if constexpr (F8 != 0) {
+#pragma unroll
+                for (int j = 0; j < 4; j += 2)
+#pragma unroll
+                    for (int r = 0; r < RB; ++r)
+#pragma unroll
+                        for (int m = 0; m < MB; ++m)
+                            acc[r][m] = mfma_pair<F8>(__builtin_bit_cast(u32x4, a[m][j]),
+                                                      __builtin_bit_cast(u32x4, a[m][j + 1]),
+                                                      b.v[u][r][j], b.v[u][r][j + 1], acc[r][m]);
+                return;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)

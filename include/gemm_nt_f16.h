@@ -174,6 +174,23 @@ int gemm_nt_fp8_cs(const void *A, const void *B, void *D, int64_t M, int64_t N, 
                    hipStream_t stream);
 
 /*
+ * FP8 product with a scale for each row of both operands: activations with one
+ * for each token, as rms_norm_fp8 (rms_norm.h) makes them, weights with one for
+ * each output channel; D in fp16 or bfloat16:
+ *
+ *     D[m,n] = (scale * b_scale[n]) * sum_{k<K} A[m,k] * B[n,k] * a_scale[m]
+ *
+ * a_scale, b_scale: device pointers to M and N fp32 values, 4-byte aligned, read
+ *   only; NULL: 1 everywhere.  The factor scale * b_scale[n] is formed in fp32 and
+ *   multiplies the fp32 sum, then a_scale[m] does, and the result is rounded once
+ *   to D's type, `dtype` (GEMM_T_F16 or GEMM_T_BF16, gemm_nt_w4.h).
+ * Everything else as gemm_nt_fp8_cs; GEMM_EINVAL also for another dtype.
+ */
+int gemm_nt_fp8_rs(const void *A, const void *B, void *D, int64_t M, int64_t N, int64_t K,
+                   float scale, const float *a_scale, const float *b_scale, int a_format,
+                   int b_format, int dtype, hipStream_t stream);
+
+/*
  * Host-only: the output tile gemm_nt_fp8 uses for these sizes (aligned16:
  * whether A and B are 16-byte aligned; 4-byte alignment is assumed
  * otherwise), following the load paths above.
