@@ -2,6 +2,7 @@
 // with per-channel weight scales, and gemm_nt_fp8_rs with per-row scales of both
 // operands) and the launches with B in E4M3.  Kernels and helpers: gemm_kernels.h, gemm_fp8.h.
 #include "gemm_fp8.h"
+#include "gemm_fp8_few.h"
 #include "gemm_nt_w4.h"
 
 namespace {
@@ -43,6 +44,9 @@ int fp8_call(const void *A, const void *B, void *D, int64_t M, int64_t N, int64_
         hipLaunchKernelGGL(epilogue_only_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
                            (_Float16 *)D, epi, M, N);
     } else if (rows) {
+        if (gemm18_fp8_few({A, B, D, M, N, K, x.scale, x.col, x.row, x.bf,
+                            1 + a_format + 2 * b_format}, stream))
+            return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ELAUNCH;
         (b_format ? gemm18_fp8_launch_rs_b5 : gemm18_fp8_launch_rs)(
             5 + a_format + 2 * b_format, A, B, D, M, N, K, x, stream);
     } else {
