@@ -1,5 +1,6 @@
 """Python binding of the C ABI in ``include/gemm_nt_f16.h``,
-``include/gemm_nt_w4.h``, ``include/moe_nt.h`` and ``include/rms_norm.h``.
+``include/gemm_nt_w4.h``, ``include/moe_nt.h``, ``include/rms_norm.h`` and
+``include/lora_nt.h``.
 
 Argument marshalling only: every step of the GEMM runs in the HIP kernels of
 ``libgemm18.so``.  PyTorch supplies device memory and the current stream.
@@ -37,7 +38,8 @@ EXPORTS = ("gemm_nt_f16", "gemm_nt_f16_strerror", "gemm_nt_f16_tile", "gemm_nt_f
            "gemm_nt_f16_acc16_kernel", "gemm_w4_packed_bytes", "gemm_w4_quantize",
            "gemm_w4_dequantize", "gemm_nt_w4", "gemm_nt_w4_ws_size", "moe_nt_route",
            "moe_nt_experts", "moe_nt_layer", "moe_nt_ws_size", "moe_nt_choose",
-           "moe_nt_route_gated", "moe_nt_layer_gated", "rms_norm", "rms_norm_fp8")
+           "moe_nt_route_gated", "moe_nt_layer_gated", "rms_norm", "rms_norm_fp8",
+           "gemm_nt_lora", "gemm_nt_lora_ws_size")
 
 
 class moe_nt_weights(ctypes.Structure):
@@ -53,6 +55,12 @@ class moe_nt_gate(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p)] + [
         (n, ctypes.c_int32) for n in ("scoring", "groups", "topk_groups", "group_top")] + [
         ("scale", ctypes.c_float)]
+
+
+class lora_nt_adapters(ctypes.Structure):
+    """``lora_nt_adapters`` of include/lora_nt.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("A", "B", "s")] + [
+        (n, ctypes.c_int64) for n in ("count", "rank")]
 
 
 class GemmError(RuntimeError):
@@ -151,6 +159,12 @@ def lib():
     L.moe_nt_route_gated.restype = ci
     L.moe_nt_layer_gated.argtypes = [mw, mg, vp, vp, vp, vp, i64, i64, i64, ci, ci, vp, i64, vp]
     L.moe_nt_layer_gated.restype = ci
+    la = ctypes.POINTER(lora_nt_adapters)
+    L.gemm_nt_lora.argtypes = [vp, vp, vp, vp, la, vp, vp, i64, i64, i64, i64, i64, ci, ci, vp,
+                               i64, vp]
+    L.gemm_nt_lora.restype = ci
+    L.gemm_nt_lora_ws_size.argtypes = [i64, i64, i64, i64, ci]
+    L.gemm_nt_lora_ws_size.restype = i64
     cf = ctypes.c_float
     L.rms_norm.argtypes = [vp] * 5 + [i64] * 6 + [cf, ci, vp]
     L.rms_norm.restype = ci
@@ -387,6 +401,19 @@ def moe_nt_layer_gated(w: moe_nt_weights, g: moe_nt_gate, X: int, D: int, ids: i
     return lib().moe_nt_layer_gated(w, g, X or None, D or None, ids or None, weights or None, T,
                                     ldx, ldd, topk, flags, workspace or None, ws_bytes,
                                     stream or None)
+
+
+def gemm_nt_lora(X: int, W: int, S: int, Z: int, a: lora_nt_adapters, ids: int, D: int, M: int,
+                 N: int, K: int, ldx: int, ldd: int, group: int, dtype: int, workspace: int,
+                 ws_bytes: int, stream: int = 0) -> int:
+    """Raw call of the product with adapters; returns the C return code."""
+    return lib().gemm_nt_lora(X or None, W or None, S or None, Z or None, a, ids or None,
+                              D or None, M, N, K, ldx, ldd, group, dtype, workspace or None,
+                              ws_bytes, stream or None)
+
+
+def gemm_nt_lora_ws_size(M: int, N: int, K: int, rank: int, group: int = 0) -> int:
+    return lib().gemm_nt_lora_ws_size(M, N, K, rank, group)
 
 
 def rms_norm(X: int, R: int, W: int, Y: int, S: int, T: int, H: int, ldx: int, ldr: int,

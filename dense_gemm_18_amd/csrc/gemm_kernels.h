@@ -160,7 +160,7 @@ __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1
 // Columns >= N are never read.  vec: C and bias are 8-byte aligned and
 // N % 4 == 0 (the same condition as D's vector stores).
 struct Epi {
-    const _Float16 *C;
+    const _Float16 *C;         // of D's type, which may be bfloat16
     const _Float16 *bias;
     float alpha, beta;
     // FP8 only: N per-column scales; column n is scaled by alpha * col_scale[n]
@@ -176,11 +176,13 @@ struct Epi {
 // Four values of row p at columns n .. n+3 as fp32; columns >= N read as 0
 // and are never accessed.  vec: one 8-byte load (N % 4 == 0 and n % 4 == 0,
 // so the four columns are all valid or all past the end).
-__device__ __forceinline__ f32x4 load4(const _Float16 *p, int n, int N, int vec)
+template <class T>
+__device__ __forceinline__ f32x4 load4(const T *p, int n, int N, int vec)
 {
+    using X4 = typename Vec4<T>::type;
     f32x4 v;
     if (vec) {
-        const f16x4 h = n < N ? *(const f16x4 *)(p + n) : f16x4{};
+        const X4 h = n < N ? *(const X4 *)(p + n) : X4{};
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             v[r] = (float)h[r];
@@ -192,6 +194,7 @@ __device__ __forceinline__ f32x4 load4(const _Float16 *p, int n, int N, int vec)
     return v;
 }
 
+template <class T>
 struct EpiFin {
     Epi e;
     int N, vec;
@@ -199,9 +202,9 @@ struct EpiFin {
     {
         v = v * e.alpha;
         if (e.beta != 0.0f)
-            v = v + e.beta * load4(e.C + (int64_t)m * N, n, N, vec);
+            v = v + e.beta * load4((const T *)e.C + (int64_t)m * N, n, N, vec);
         if (e.bias)
-            v = v + load4(e.bias, n, N, vec);
+            v = v + load4((const T *)e.bias, n, N, vec);
         return v;
     }
 };
@@ -359,14 +362,16 @@ __device__ __forceinline__ void store_blocks16(Get get, T *__restrict__ D, int M
 
 // Four fp16 values of row p at columns n .. n+3 (columns >= N read as 0),
 // raw: one 8-byte load when vec, else element loads.
-__device__ __forceinline__ f16x4 load4h(const _Float16 *p, int n, int N, int vec)
+template <class T>
+__device__ __forceinline__ typename Vec4<T>::type load4h(const T *p, int n, int N, int vec)
 {
+    using X4 = typename Vec4<T>::type;
     if (vec)
-        return n < N ? *(const f16x4 *)(p + n) : f16x4{};
-    f16x4 h;
+        return n < N ? *(const X4 *)(p + n) : X4{};
+    X4 h;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        h[r] = n + r < N ? p[n + r] : (_Float16)0.0f;
+        h[r] = n + r < N ? p[n + r] : (T)0.0f;
     return h;
 }
 
@@ -382,14 +387,15 @@ __device__ __forceinline__ f16x4 load4h(const _Float16 *p, int n, int N, int vec
 // form computes the other's arithmetic).  ROWS: the row form, whose row_scale and
 // col_scale may each be absent, and whose results are of either 16-bit type.
 template <int TM, int TN, class Get, bool WITH_C = true, bool COLS = false, bool WITH_BIAS = true,
-          bool STAGED = false, bool ROWS = false>
-__device__ __forceinline__ void store_blocks16_epi(Get get, _Float16 *__restrict__ D, int M,
+          bool STAGED = false, bool ROWS = false, class T = _Float16>
+__device__ __forceinline__ void store_blocks16_epi(Get get, T *__restrict__ D, int M,
                                                    int N, int mbase, int nbase, int lane,
                                                    int vec, const Epi &e, char *stage = nullptr)
 {
+    using X4 = typename Vec4<T>::type;
     const int frow = lane & 15, fq = lane >> 4;
     const bool has_c = WITH_C && e.beta != 0.0f, has_bias = WITH_BIAS && e.bias != nullptr;
-    f16x4 cv[TM][TN], bv[TN];
+    X4 cv[TM][TN], bv[TN];
     // per-column factors alpha * col_scale[n .. n+3] (columns >= N not read)
     f32x4 sv[COLS ? TN : 1];
     if constexpr (COLS) {
@@ -417,7 +423,7 @@ __device__ __forceinline__ void store_blocks16_epi(Get get, _Float16 *__restrict
     if (has_bias) {
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-            bv[j] = load4h(e.bias, nbase + 16 * j + 4 * fq, N, vec);
+            bv[j] = load4h((const T *)e.bias, nbase + 16 * j + 4 * fq, N, vec);
     }
     if (has_c) {
 #pragma unroll
@@ -425,14 +431,14 @@ __device__ __forceinline__ void store_blocks16_epi(Get get, _Float16 *__restrict
             const int m = mbase + 16 * i + frow;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-                cv[i][j] = m < M ? load4h(e.C + (int64_t)m * N, nbase + 16 * j + 4 * fq, N, vec)
-                                 : f16x4{};
+                cv[i][j] = m < M ? load4h((const T *)e.C + (int64_t)m * N, nbase + 16 * j + 4 * fq, N, vec)
+                                 : X4{};
         }
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int m = mbase + 16 * i + frow;
-        _Float16 *drow = D + (int64_t)m * N;
+        T *drow = D + (int64_t)m * N;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const f32x4 v = get(i, j);
@@ -458,24 +464,24 @@ __device__ __forceinline__ void store_blocks16_epi(Get get, _Float16 *__restrict
                 for (int r = 0; r < 4; ++r)
                     u[r] = u[r] + (float)bv[j][r];
             }
-            f16x4 h;
+            X4 h;
             if (ROWS && e.bf) {
                 bf16x4 b;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     b[r] = (__bf16)u[r];
-                h = __builtin_bit_cast(f16x4, b);
+                h = __builtin_bit_cast(X4, b);
             } else {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    h[r] = (_Float16)u[r];
+                    h[r] = (T)u[r];
             }
             if constexpr (STAGED) {
                 *(u32x2 *)(stage + Stage16<TM, TN>::offset(16 * i + frow, 16 * j + 4 * fq)) =
                     __builtin_bit_cast(u32x2, h);
             } else if (vec) {
                 if (n < N)
-                    *(f16x4 *)(drow + n) = h;
+                    *(X4 *)(drow + n) = h;
             } else {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
@@ -1258,7 +1264,7 @@ gemm_nt_dma_kernel(const typename Elem<BF>::T *__restrict__ A,
             auto get = [&](int i, int j) G18_INLINE { return accf(i, j); };
             if constexpr (C::MF == 32)
                 store_blocks<C::TM, C::TN>(get, D, M, N, mb, nb, lane, vec_store,
-                                           EpiFin{epi, N, vec_store});
+                                           EpiFin<typename Elem<BF>::T>{epi, N, vec_store});
             else if constexpr (F8 != 0) {
                 if constexpr (RS)
                     store_blocks16_epi<C::TM, C::TN, decltype(get), false, true, false, false,
@@ -1270,7 +1276,9 @@ gemm_nt_dma_kernel(const typename Elem<BF>::T *__restrict__ A,
                     store_blocks16_epi<C::TM, C::TN, decltype(get), false, false, false>(
                         get, D, M, N, mb, nb, lane, vec_store, epi);
             } else {
-                store_blocks16_epi<C::TM, C::TN>(get, D, M, N, mb, nb, lane, vec_store, epi);
+                store_blocks16_epi<C::TM, C::TN, decltype(get), true, false, true, false, false,
+                                   typename Elem<BF>::T>(get, D, M, N, mb, nb, lane, vec_store,
+                                                         epi);
             }
         } else if constexpr (C::MF == 32) {
             store_acc<C::TM, C::TN>(acc, D, M, N, mb, nb, lane, vec_store);

@@ -24,14 +24,22 @@ __attribute__((visibility("hidden"))) void gemm18_w4_bf16(const W4Args &a, int g
 
 namespace {
 
+// What a kernel adds to a tile's sums before they are rounded: nothing.  Others have
+// `lds_at`, where their part of the LDS begins, bytes(rows) of it, stage(), which every
+// thread calls, and at(), the addend of the tile's row m in column n.
+struct NoPlus {
+    static constexpr bool kNone = true;
+    int bytes(int) const { return 0; }
+};
+
 // One workgroup's tile of D, 16 * MB rows and as many columns as Core has
 // weight rows.  Few rows are bound by reading the weights: 1 x 16384 x 8192 with
 // zero points, 70 MB, takes 15.4 us in fp16 (4.5 TB/s; 14 us from HBM and 10 from
 // the last-level cache for the reading alone) and 17.8 in bfloat16, whose
 // unpacking takes the VALU for 63 % of the time; the launch, the first loads and
 // the join are 4 of it, all that 1 x 1024 x 1024 has.
-template <bool BF, int MB, class Core>
-__global__ void __launch_bounds__(Core::kThreads, 2) gemm_w4_kernel(W4Args p)
+template <bool BF, int MB, class Core, class Plus = NoPlus>
+__global__ void __launch_bounds__(Core::kThreads, 2) gemm_w4_kernel(W4Args p, Plus plus)
 {
     extern __shared__ f32x4 lds[];
     // a grid of 2^32 work-items or more has a second dimension
@@ -49,41 +57,51 @@ __global__ void __launch_bounds__(Core::kThreads, 2) gemm_w4_kernel(W4Args p)
     c.begin((char *)lds, p.A + (int64_t)m0 * p.lda,
             (uint32_t)((c.M - 1) * p.lda + p.K) * 2u);
     c.run([&](int m) { return (uint32_t)(m * p.lda) * 2u; });
+    if constexpr (!Plus::kNone)
+        plus.stage((char *)lds, m0, c.M);
     uint16_t *D = p.D + (int64_t)m0 * p.ldd + n0;
     c.join([&](int m, int n, const auto &v) {
         constexpr int RB = sizeof(v) / sizeof(v[0]);
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
             const int nn = (n >> 4) * (16 * RB) + 16 * r + (n & 15);
-            if (n0 + nn < p.N)
-                D[m * p.ldd + nn] = from_float<BF>(v[r]);
+            if (n0 + nn < p.N) {
+                float d = v[r];
+                if constexpr (!Plus::kNone)
+                    d += plus.template at<BF>((const char *)lds, m, n0 + nn);
+                D[m * p.ldd + nn] = from_float<BF>(d);
+            }
         }
     });
 }
 
-template <bool BF, int MB, class Core>
-void launch_w4_tile(W4Args a, int lds, hipStream_t stream)
+template <bool BF, int MB, class Core, class Plus>
+void launch_w4_tile(W4Args a, int lds, hipStream_t stream, Plus plus)
 {
+    if constexpr (!Plus::kNone) {
+        plus.lds_at = lds;
+        lds += plus.bytes(a.M < 16 * MB ? a.M : 16 * MB);
+    }
     a.tiles_n = (uint32_t)cdiv(a.N, Core::kRows);
     a.tiles_m = (uint32_t)cdiv(a.M, 16 * MB);
-    hipLaunchKernelGGL((gemm_w4_kernel<BF, MB, Core>),
+    hipLaunchKernelGGL((gemm_w4_kernel<BF, MB, Core, Plus>),
                        tile_grid((int64_t)a.tiles_n * a.tiles_m), dim3(Core::kThreads), lds,
-                       stream, a);
+                       stream, a, plus);
 }
 
 // Activations that LDS holds whole: every wave walks its eighth of K freely.
-template <bool BF, int GS, int RB>
-void launch_w4_resident(const W4Args &a, hipStream_t stream)
+template <bool BF, int GS, int RB, class Plus>
+void launch_w4_resident(const W4Args &a, hipStream_t stream, const Plus &plus)
 {
     using Core = Skinny<BF, GS, RB, 1, kW4Waves, 1, true>;
-    launch_w4_tile<BF, 1, Core>(a, Core::lds_bytes(a.M, a.K), stream);
+    launch_w4_tile<BF, 1, Core>(a, Core::lds_bytes(a.M, a.K), stream, plus);
 }
 
-template <bool BF, int GS, int RB, int MB, int KW, int NW, int CS>
-void launch_w4_piped(const W4Args &a, hipStream_t stream)
+template <bool BF, int GS, int RB, int MB, int KW, int NW, int CS, class Plus>
+void launch_w4_piped(const W4Args &a, hipStream_t stream, const Plus &plus)
 {
     using Core = Piped<BF, GS, RB, MB, KW, NW, CS>;
-    launch_w4_tile<BF, MB, Core>(a, Core::kLds, stream);
+    launch_w4_tile<BF, MB, Core>(a, Core::kLds, stream, plus);
 }
 
 // Resident: activations within kActBytes, where no wave waits for another until
@@ -116,8 +134,10 @@ void launch_w4_piped(const W4Args &a, hipStream_t stream)
 //                32      1.26+  1.20+  1.12+  0.83-0.91  0.62+  0.56+
 //   four rows, for which K = 8192 takes 82 KB and more
 //     groups of 128      1.16+  1.19+  1.08+  1.01+  0.85-0.90
-template <bool BF>
-void launch_w4(const W4Args &a, int group, hipStream_t stream)
+// most: rows that a tile may have (16, 32 or 64).
+template <bool BF, class Plus = NoPlus>
+void launch_w4(const W4Args &a, int group, hipStream_t stream, const Plus &plus = Plus{},
+               int most = 64)
 {
     const auto fills = [&](int rows, int columns) {
         return cdiv(a.M, rows) * cdiv(a.N, columns) >= kCUs;
@@ -128,24 +148,24 @@ void launch_w4(const W4Args &a, int group, hipStream_t stream)
             a.M <= 16 && (int64_t)a.M * (cdiv(a.K, 128) * 256 + 16) <= kActBytes;
         const int beside = Skinny<BF, GS, 4, 1, kW4Waves, 1, true>::lds_bytes(a.M, a.K);
         if (whole && cdiv(a.N, 64) > kCUs && cdiv(a.K, GS) <= 64 && beside <= 80 * 1024) {
-            launch_w4_resident<BF, GS, 4>(a, stream);
+            launch_w4_resident<BF, GS, 4>(a, stream, plus);
         } else if (whole && !fills(16, 64)) {
             if (fills(16, 32))
-                launch_w4_resident<BF, GS, 2>(a, stream);
+                launch_w4_resident<BF, GS, 2>(a, stream, plus);
             else
-                launch_w4_resident<BF, GS, 1>(a, stream);
+                launch_w4_resident<BF, GS, 1>(a, stream, plus);
         } else if (a.M <= 16 && fills(16, 64)) {
-            launch_w4_piped<BF, GS, 2, 1, 8, 2, 8>(a, stream);
+            launch_w4_piped<BF, GS, 2, 1, 8, 2, 8>(a, stream, plus);
         } else if (a.M <= 16 && fills(16, 32)) {
-            launch_w4_piped<BF, GS, 2, 1, 8, 1, 8>(a, stream);
-        } else if (a.M > 32 && fills(64, 64)) {
-            launch_w4_piped<BF, GS, 2, 4, 4, 2, 4>(a, stream);
-        } else if (a.M > 16 && fills(32, 64)) {
-            launch_w4_piped<BF, GS, 2, 2, 4, 2, 4>(a, stream);
-        } else if (a.M > 16 && fills(32, 32)) {
-            launch_w4_piped<BF, GS, 1, 2, 4, 2, 4>(a, stream);
+            launch_w4_piped<BF, GS, 2, 1, 8, 1, 8>(a, stream, plus);
+        } else if (a.M > 32 && most >= 64 && fills(64, 64)) {
+            launch_w4_piped<BF, GS, 2, 4, 4, 2, 4>(a, stream, plus);
+        } else if (a.M > 16 && most >= 32 && fills(32, 64)) {
+            launch_w4_piped<BF, GS, 2, 2, 4, 2, 4>(a, stream, plus);
+        } else if (a.M > 16 && most >= 32 && fills(32, 32)) {
+            launch_w4_piped<BF, GS, 1, 2, 4, 2, 4>(a, stream, plus);
         } else {
-            launch_w4_piped<BF, GS, 1, 1, 8, 1, 8>(a, stream);
+            launch_w4_piped<BF, GS, 1, 1, 8, 1, 8>(a, stream, plus);
         }
     });
 }
