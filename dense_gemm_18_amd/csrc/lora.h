@@ -18,27 +18,28 @@ struct LoraArgs {
     uint16_t *D;
     int64_t ldx;
     int M, N, K, rank, count, parts;
-    int items, rblocks;            // of a tile: adapters at most, blocks of their rows
+    int items, rblocks;            // workgroups for a tile's adapters, blocks of their rows
+    int columns, split;            // of a workgroup of the second product; who share adapters
 };
 
-// Pieces of K in the first product, and with them of u: as many as give each compute unit
-// two workgroups, of 512 elements or more.
+// Pieces of K in the first product, and with them of u, at most: what the workspace has room
+// for.  Of 512 elements or more; the fewer the tiles of rows, the more of them.
 inline int lora_parts(int64_t M, int64_t K)
 {
     const int64_t tiles = cdiv(M, kLoraRows);
-    int64_t p = 2 * kCUs / tiles;
-    p = p > 8 ? 8 : p < 1 ? 1 : p;
+    int64_t p = tiles < 8 ? 8 : kCUs / tiles;
+    p = tiles >= 8 && p > 4 ? 4 : p < 1 ? 1 : p;
     return (int)(p < cdiv(K, 512) ? p : cdiv(K, 512));
 }
 
 // One translation unit for each type.  Not exported from the library.
 struct LoraLaunch {
     // u
-    void (*shrink)(LoraArgs, hipStream_t);
+    void (*shrink)(const LoraArgs &, hipStream_t);
     // D from the weight's tiles with the adapters' part added, for a group or 16-bit weights
     void (*fused)(const LoraArgs &, const W4Args &, int group, hipStream_t);
     // the adapters' part alone into dense rows of D
-    void (*expand)(const LoraArgs &, hipStream_t);
+    void (*expand)(LoraArgs, hipStream_t);
 };
 __attribute__((visibility("hidden"))) LoraLaunch gemm18_lora_f16();
 __attribute__((visibility("hidden"))) LoraLaunch gemm18_lora_bf16();
@@ -84,9 +85,9 @@ __device__ __forceinline__ uint64_t rows_of(int id, int item)
 }
 
 // u of one adapter's rows in a tile, for 16 * RB of its rank and one piece of K, on the
-// core of skinny.h with A's rows as the weight: each workgroup looks for its item among the
-// tile's ids and gathers its rows, so an adapter is read once for the rows that have it and
-// no row is multiplied with another's.
+// core of skinny.h with A's rows as the weight: each workgroup looks for its items among the
+// tile's ids and gathers their rows, so an adapter is read once for the rows that have it
+// and no row is multiplied with another's.
 template <bool BF, int RB, int MB>
 __device__ __forceinline__ void lora_item(const LoraArgs &p, char *lds, const int *list, int rows,
                                           int64_t m0, int a, int rb, int part)
@@ -118,29 +119,36 @@ __global__ void __launch_bounds__(512, 2) lora_shrink_kernel(LoraArgs p)
 {
     extern __shared__ f32x4 lds[];
     __shared__ int list[kLoraRows];
+    // Items vary slowest: those that find no adapter are then the last workgroups.  (Between
+    // the others, and dealt to the XCDs by turns, they left half of these idle: 34 us instead
+    // of 19 for 2048 rows of 8192, rank 64, with a second item to each tile.)
     int64_t wg = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
+    const int64_t tiles = (p.M + (int64_t)kLoraRows - 1) / kLoraRows;
     const int part = (int)(wg % p.parts);
     wg /= p.parts;
     const int rb = (int)(wg % p.rblocks);
     wg /= p.rblocks;
-    const int item = (int)(wg % p.items);
-    const int64_t m0 = wg / p.items * kLoraRows;
-    if (m0 >= p.M)
+    const int64_t m0 = wg % tiles * kLoraRows;
+    wg /= tiles;
+    if (wg >= p.items)
         return;
     const int lane = threadIdx.x & 63;
     const int id = lane < kLoraRows ? adapter_of(p, m0 + lane) : -1;
-    const uint64_t mask = rows_of(id, item);
-    if (!mask)
-        return;
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(mask));
-    if (threadIdx.x < 64 && (mask >> lane & 1))
-        list[__popcll(mask & ((1ull << lane) - 1))] = lane;
-    __syncthreads();
-    const int rows = __popcll(mask);
-    if (rows <= 16)
-        lora_item<BF, RB, 1>(p, (char *)lds, list, rows, m0, a, rb, part);
-    else
-        lora_item<BF, RB, 2>(p, (char *)lds, list, rows, m0, a, rb, part);
+    for (int item = (int)wg;; item += p.items) {
+        const uint64_t mask = rows_of(id, item);
+        if (!mask)
+            return;
+        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(mask));
+        __syncthreads();                  // the item before is done with the list
+        if (threadIdx.x < 64 && (mask >> lane & 1))
+            list[__popcll(mask & ((1ull << lane) - 1))] = lane;
+        __syncthreads();
+        const int rows = __popcll(mask);
+        if (rows <= 16)
+            lora_item<BF, RB, 1>(p, (char *)lds, list, rows, m0, a, rb, part);
+        else
+            lora_item<BF, RB, 2>(p, (char *)lds, list, rows, m0, a, rb, part);
+    }
 }
 
 template <bool BF, int RB>
@@ -156,17 +164,38 @@ void launch_shrink(LoraArgs p, hipStream_t stream)
                        one > two ? one : two, stream, p);
 }
 
-// As many of an adapter's rows to a workgroup as there are, where the tiles alone fill
-// the compute units; else 16, for more workgroups.
-template <bool BF>
-void lora_shrink(LoraArgs p, hipStream_t stream)
+// How a tile of rows is shared.  Few tiles are a decode step, whose rows may all have
+// adapters of their own: a workgroup for each, K in as many pieces as fill the compute units.
+// Many are prompts, with one or two adapters to a tile and more rows of A to a workgroup, so
+// that X is read less often.  Measured, K = 8192, in us: 64 rows of 32 adapters of rank 16
+// in 4 pieces 8.8, in 2 10.4, in 8 14.0; of rank 64, 16 or 32 rows of A to a workgroup, 18.2
+// (2 pieces) and 15.4 (4); 2048 rows in runs of 256, rank 64, 16, 32 or 64 rows of A, 4 pieces,
+// 36, 26 and 18.8 (8 pieces: 44, 27 and 21.8).
+inline LoraArgs lora_shared(LoraArgs p)
 {
-    p.items = p.count < kLoraRows ? p.count : kLoraRows;
-    p.items = p.items < p.M ? p.items : p.M;
-    const bool many = cdiv(p.M, kLoraRows) * p.parts >= kCUs;
-    if (p.rank <= 16 || !many)
+    const int64_t tiles = cdiv(p.M, kLoraRows);
+    const int most = lora_parts(p.M, p.K);
+    int items = p.count < kLoraRows ? p.count : kLoraRows;
+    items = items < p.M ? items : p.M;
+    if (tiles < 8) {
+        const int64_t fill = kCUs / (tiles * items);
+        p.parts = (int)(fill < 1 ? 1 : fill < most ? fill : most);
+    } else {
+        p.parts = most;
+        const int64_t fill = tiles < 32 ? 8 : cdiv(2 * kCUs, tiles * most);
+        items = (int)(items < fill ? items : fill);
+    }
+    p.items = items;
+    return p;
+}
+
+template <bool BF>
+void lora_shrink(const LoraArgs &p, hipStream_t stream)
+{
+    const int64_t tiles = cdiv(p.M, kLoraRows);
+    if (p.rank <= 16 || p.M <= 16 || (p.rank <= 32 && tiles < 8))
         launch_shrink<BF, 1>(p, stream);
-    else if (p.rank <= 32)
+    else if (p.rank <= 32 || tiles < 32)
         launch_shrink<BF, 2>(p, stream);
     else
         launch_shrink<BF, 4>(p, stream);
@@ -215,14 +244,21 @@ struct LoraPlus {
             return 0.0f;
         const uint16_t *b = B + ((int64_t)a * N + n) * rank;
         float sum = 0.0f;
-        for (int j = 0; j < rank; j += 8) {
-            const u32x4 v = eight_of(b + j, rank - j);
+        auto piece = [&](u32x4 v, int j) G18_INLINE {
             const f32x4 x = *(const f32x4 *)(from + 4 + j), y = *(const f32x4 *)(from + 8 + j);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 sum = __builtin_fmaf(e < 4 ? x[e & 3] : y[e & 3],
                                      to_float<BF>((uint16_t)(v[e >> 1] >> (16 * (e & 1)))), sum);
+        };
+        int j = 0;
+        for (; j + 16 <= rank; j += 16) {        // two loads on their way together
+            const u32x4 v = *(const u32x4_any *)(b + j), w = *(const u32x4_any *)(b + j + 8);
+            piece(v, j);
+            piece(w, j + 8);
         }
+        for (; j < rank; j += 8)
+            piece(eight_of(b + j, rank - j), j);
         return sum;
     }
 };
@@ -259,117 +295,241 @@ void lora_fused(const LoraArgs &p, const W4Args &w, int group, hipStream_t strea
 
 // ---- the adapters' part alone --------------------------------------------
 
-constexpr int kExpandColumns = 512;
-
-// 64 rows of the adapters' part, kExpandColumns columns of it.  u, summed and rounded to the
+// 64 rows of the adapters' part, p.columns columns of it.  u, summed and rounded to the
 // 16-bit type (each row times a power of two that leaves its largest near 1, taken off
-// afterwards), is in LDS; for each adapter of the tile every row is multiplied with its B
-// and only the rows that have it are stored: what is infinite in one adapter stays out of
-// the others' rows.
-template <bool BF>
-__global__ void __launch_bounds__(256) lora_expand_kernel(LoraArgs p)
+// afterwards), is in LDS.  Each wave takes pairs of an adapter and 64 columns: the adapter's
+// rows of B, which come straight to registers, meet every 16 rows that hold one of its own,
+// and only its own are stored, so what is infinite in one adapter stays out of the others'
+// rows.  While one pair is multiplied, the next one's rows of B travel.  Results go through
+// the wave's own LDS 16 rows at a time, whole 128-byte lines of a row leave together.  Where
+// there are few tiles, p.split workgroups share one's adapters.  KS: pieces of 32 of the
+// rank.
+constexpr int kExpandLine = 64 * 2 + 16;         // bytes of a staged row
+
+template <bool BF, int KS>
+__global__ void __launch_bounds__(512, KS == 1 ? 4 : 2) lora_expand_kernel(LoraArgs p)
 {
     using x8 = typename Elem<BF>::x8;
+    constexpr int kLd = KS * 32 + 8;             // 16-bit elements of a row of u
     extern __shared__ f32x4 lds[];
     __shared__ float unscale[64];
-    const int columns = (p.N + kExpandColumns - 1) / kExpandColumns;
-    const uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
-    const int64_t m0 = (int64_t)(wg / columns) * 64;
+    __shared__ int adapter[64];
+    __shared__ uint64_t has[64];
+    const int blocks = (p.N + p.columns - 1) / p.columns;
+    uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
+    const int n0 = (int)(wg % blocks) * p.columns;
+    wg /= blocks;
+    const int share = (int)(wg % p.split);
+    const int64_t m0 = (int64_t)(wg / p.split) * 64;
     if (m0 >= p.M)
         return;
-    const int n0 = (int)(wg % columns) * kExpandColumns;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int id = adapter_of(p, m0 + lane);
-    const int ks = (p.rank + 31) / 32, ld = ks * 32 + 8;       // 16-bit elements of a row
     uint16_t *held = (uint16_t *)lds;
-    for (int m = wave; m < 64; m += 4) {
-        const bool in = __builtin_amdgcn_readlane(id, m) >= 0;
-        float v[LORA_MAX_RANK / 64], most = 0.0f;
+    char *stage = (char *)lds + 64 * kLd * 2 + wave * (16 * kExpandLine);
+    // this workgroup's adapters of the tile, by every wave alike
+    int count = 0;
+    for (uint64_t left = __ballot(id >= 0), i = 0; left; ++i) {
+        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        const uint64_t same = __ballot(id == a);
+        left &= ~same;
+        if (i % p.split != (uint32_t)share)
+            continue;
+        if (threadIdx.x == 0) {
+            adapter[count] = a;
+            has[count] = same;
+        }
+        ++count;
+    }
+    __syncthreads();
+    const int c = lane >> 4, col = lane & 15;
+    const int cols = (min(p.columns, p.N - n0) + 63) >> 6, pairs = count * cols;
+    using Rows = x8[4][KS];
+    // Unconditional buffer loads, rows past N and what is past the rank out of range: a
+    // branch around loads would wait for each.  A rank that is no multiple of 8 leaves
+    // elements of the next row behind the last, which are cleared; where it is odd the last
+    // element may be half of the range's last word, which reads as 0, and is loaded alone.
+    auto fetch = [&](Rows &w, int pair) G18_INLINE {
+        const int k = uniform(pair / cols), n = n0 + (pair - k * cols) * 64;
+        const int rows = min(64, p.N - n), a = uniform(adapter[k]);
+        const auto rs = range(p.B + ((int64_t)a * p.N + n) * p.rank,
+                              (uint32_t)(rows * p.rank) * 2u);
+        u32x4 v[4][KS];
+        uint32_t end[4];
 #pragma unroll
-        for (int i = 0; i < LORA_MAX_RANK / 64; ++i) {
-            const int j = lane + 64 * i;
-            v[i] = 0.0f;
-            if (in && j < p.rank)
-                for (int q = 0; q < p.parts; ++q)
-                    v[i] += p.u[((int64_t)q * p.M + m0 + m) * p.rank + j];
-            most = __builtin_fmaxf(most, __builtin_fabsf(v[i]));
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t row = (uint32_t)((col + 16 * i) * p.rank) * 2u;
+#pragma unroll
+            for (int q = 0; q < KS; ++q)
+                v[i][q] = load_b128(rs, 32 * q + 8 * c < p.rank ? row + (32 * q + 8 * c) * 2u
+                                                                : kOob);
+            if (p.rank & 1)
+                end[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                    rs, row + (p.rank - 1) * 2u, 0, 0);
+        }
+        if (p.rank & 7) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int q = 0; q < KS; ++q) {
+                    const int left = p.rank - 32 * q - 8 * c;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t keep = left > 2 * j + 1 ? 0xffffffffu
+                                              : left > 2 * j   ? 0xffffu
+                                                               : 0u;
+                        v[i][q][j] =
+                            left == 2 * j + 1 && (p.rank & 1) ? end[i] : v[i][q][j] & keep;
+                    }
+                }
         }
 #pragma unroll
-        for (int d = 32; d; d /= 2)
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < KS; ++q)
+                w[i][q] = __builtin_bit_cast(x8, v[i][q]);
+    };
+    Rows even, odd;
+    if (wave < pairs)
+        fetch(even, wave);
+    {
+        // eight lanes to a row
+        const int m = threadIdx.x >> 3, j0 = threadIdx.x & 7;
+        const bool in = __shfl(id, m) >= 0;
+        const float *u = p.u + (m0 + m) * p.rank;
+        float v[KS * 4], most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KS * 4; ++i)
+            v[i] = in && j0 + 8 * i < p.rank ? u[j0 + 8 * i] : 0.0f;
+        for (int q = 1; q < p.parts; ++q) {
+            u += (int64_t)p.M * p.rank;
+#pragma unroll
+            for (int i = 0; i < KS * 4; ++i)
+                v[i] += in && j0 + 8 * i < p.rank ? u[j0 + 8 * i] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < KS * 4; ++i)
+            most = __builtin_fmaxf(most, __builtin_fabsf(v[i]));
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2)
             most = __builtin_fmaxf(most, __shfl_xor(most, d));
         // 2^e <= most < 2^(e + 1); what is 0 or not finite stays as it is
         int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23) - 127;
         e = e == 128 || most == 0.0f ? 0 : e < -126 ? -126 : e;
-        if (lane == 0)
+        if (j0 == 0)
             unscale[m] = __builtin_ldexpf(1.0f, e);
 #pragma unroll
-        for (int i = 0; i < LORA_MAX_RANK / 64; ++i)
-            if (lane + 64 * i < ks * 32)
-                held[m * ld + lane + 64 * i] = from_float<BF>(__builtin_ldexpf(v[i], -e));
+        for (int i = 0; i < KS * 4; ++i)
+            held[m * kLd + j0 + 8 * i] = from_float<BF>(__builtin_ldexpf(v[i], -e));
     }
     __syncthreads();
-    const int c = lane >> 4, col = lane & 15;
-    const bool whole = p.N % 4 == 0 && ((uintptr_t)p.D & 7) == 0;
-    auto store = [&](int m, int n, const f32x4 &v) G18_INLINE {
+    const int vec = p.N % 4 != 0 || ((uintptr_t)p.D & 7) ? 0 : p.N % 8 || ((uintptr_t)p.D & 15)
+                                                                   ? 1 : 2;
+    auto packed = [&](const f32x4 &v) G18_INLINE {
+        return u32x2{from_float<BF>(v[0]) | (uint32_t)from_float<BF>(v[1]) << 16,
+                     from_float<BF>(v[2]) | (uint32_t)from_float<BF>(v[3]) << 16};
+    };
+    auto store = [&](int m, int n, u32x2 v) G18_INLINE {
         uint16_t *to = p.D + (m0 + m) * (int64_t)p.N + n;
-        if (whole) {
+        if (vec) {
             if (n < p.N)
-                *(u32x2 *)to = u32x2{from_float<BF>(v[0]) | (uint32_t)from_float<BF>(v[1]) << 16,
-                                     from_float<BF>(v[2]) | (uint32_t)from_float<BF>(v[3]) << 16};
+                *(u32x2 *)to = v;
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 if (n + r < p.N)
-                    to[r] = from_float<BF>(v[r]);
+                    to[r] = (uint16_t)(v[r >> 1] >> (16 * (r & 1)));
         }
     };
-    int row[4];                    // the adapters of this lane's rows; -2: past the end
+    auto consume = [&](const Rows &w, int pair) G18_INLINE {
+        const int k = pair / cols, n = n0 + (pair - k * cols) * 64;
+        const uint64_t rows = has[k];
+        const bool lines = vec == 2 && n + 64 <= p.N;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        row[b] = __shfl(id, 16 * b + col);
-        row[b] = m0 + 16 * b + col < p.M ? row[b] : -2;
-    }
-    uint64_t left = __ballot(id >= 0);
-    const bool bare = __ballot(id < 0 && m0 + lane < p.M) != 0;
-    for (int nb = wave * 16; nb < kExpandColumns && n0 + nb < p.N; nb += 64) {
-        const int n = n0 + nb;
-        if (bare) {
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t mine = uniform((int)(rows >> (16 * b)) & 0xffff);
+            if (!mine)
+                continue;
+            x8 a[KS];
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (row[b] == -1)
-                    store(16 * b + col, n + 4 * c, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-        }
-        for (uint64_t rest = left; rest;) {
-            const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(rest));
-            rest &= ~__ballot(id == a);
-            const uint16_t *B = p.B + ((int64_t)a * p.N + min(n + col, p.N - 1)) * p.rank;
-            f32x4 acc[4];
+            for (int q = 0; q < KS; ++q)
+                a[q] = *(const x8 *)(held + (16 * b + col) * kLd + q * 32 + 8 * c);
+            const float by = unscale[16 * b + col];
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            for (int k = 0; k < ks; ++k) {
-                const x8 w = __builtin_bit_cast(x8, eight_of(B + k * 32 + 8 * c,
-                                                            p.rank - k * 32 - 8 * c));
+            for (int i = 0; i < 4; ++i) {
+                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    acc[b] = mfma16<BF>(
-                        w, *(const x8 *)(held + (16 * b + col) * ld + k * 32 + 8 * c), acc[b]);
+                for (int q = 0; q < KS; ++q)
+                    acc = mfma16<BF>(w[i][q], a[q], acc);
+                const u32x2 v = packed(acc * by);
+                if (lines)
+                    *(u32x2 *)(stage + col * kExpandLine + i * 32 + c * 8) = v;
+                else if (mine >> col & 1)
+                    store(16 * b + col, n + 16 * i + 4 * c, v);
             }
+            if (!lines)
+                continue;
+            // the wave's own writes come before its reads, and those before its next writes
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int m = 8 * i + (lane >> 3);
+                const u32x4 v = *(const u32x4 *)(stage + m * kExpandLine + (lane & 7) * 16);
+                if (mine >> m & 1)
+                    *(u32x4 *)(p.D + (m0 + 16 * b + m) * (int64_t)p.N + n + (lane & 7) * 8) = v;
+            }
+            asm volatile("" ::: "memory");
+        }
+    };
+    for (int i = wave; i < pairs; i += 16) {
+        if (i + 8 < pairs)
+            fetch(odd, i + 8);
+        consume(even, i);
+        if (i + 16 < pairs)
+            fetch(even, i + 16);
+        if (i + 8 < pairs)
+            consume(odd, i + 8);
+    }
+    // rows without an adapter
+    const uint64_t bare = __ballot(id < 0 && m0 + lane < p.M);
+    if (bare && share == 0)
+        for (int i = wave; i < 4 * cols; i += 8)
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-                if (row[b] == a)
-                    store(16 * b + col, n + 4 * c, acc[b] * unscale[16 * b + col]);
-        }
-    }
+                if (bare >> (16 * b + col) & 1)
+                    store(16 * b + col, n0 + 16 * i + 4 * c, u32x2{0, 0});
 }
 
-template <bool BF>
-void lora_expand(const LoraArgs &p, hipStream_t stream)
+template <bool BF, int KS>
+void launch_expand(const LoraArgs &p, hipStream_t stream)
 {
-    const int lds = 64 * ((int)cdiv(p.rank, 32) * 32 + 8) * 2;
-    hipLaunchKernelGGL((lora_expand_kernel<BF>),
-                       tile_grid(cdiv(p.M, 64) * cdiv(p.N, kExpandColumns)), dim3(256), lds,
-                       stream, p);
+    hipLaunchKernelGGL((lora_expand_kernel<BF, KS>),
+                       tile_grid(cdiv(p.M, 64) * cdiv(p.N, p.columns) * p.split), dim3(512),
+                       64 * (KS * 32 + 8) * 2 + 8 * 16 * kExpandLine, stream, p);
+}
+
+// As many columns to a workgroup, 64 to 512, as leave each compute unit one; and where even
+// 64 are not few enough, several that share a tile's adapters, down to eight for each.
+// Measured, rank 16, in us: 64 x 16384, 32 adapters, 64 columns 13.3, 128 18, two sharing 14.7;
+// 64 x 8192 12.8 and 10.5; 2048 x 8192, 512 columns 10.6, 256 14.3.
+template <bool BF>
+void lora_expand(LoraArgs p, hipStream_t stream)
+{
+    const auto wgs = [&] { return cdiv(p.M, 64) * cdiv(p.N, p.columns); };
+    p.columns = 512;
+    while (p.columns > 64 && wgs() < kCUs)
+        p.columns /= 2;
+    const int64_t most = cdiv(p.count < 64 ? p.count : 64, 8), fill = kCUs / wgs();
+    p.split = (int)(fill < most ? fill : most);
+    p.split = p.split > 1 ? p.split : 1;
+    if (p.rank <= 32)
+        launch_expand<BF, 1>(p, stream);
+    else if (p.rank <= 64)
+        launch_expand<BF, 2>(p, stream);
+    else if (p.rank <= 128)
+        launch_expand<BF, 4>(p, stream);
+    else
+        launch_expand<BF, 8>(p, stream);
 }
 
 } // namespace

@@ -107,7 +107,9 @@ int gemm_nt_lora(const void *X, const void *W, const void *S, const void *Z,
     p.K = (int)K;
     p.rank = (int)a->rank;
     p.count = (int)a->count;
-    p.parts = lora_parts(M, K);
+    p.parts = 1;
+    if (p.count)
+        p = lora_shared(p);
     const bool bf = dtype == GEMM_T_BF16;
     const LoraLaunch go = bf ? gemm18_lora_bf16() : gemm18_lora_f16();
     const std::lock_guard<std::mutex> whole(launch_lock(workspace));
@@ -116,7 +118,7 @@ int gemm_nt_lora(const void *X, const void *W, const void *S, const void *Z,
     if (ldx == K && ldd == N && large(M, N, group)) {
         const void *weight = W;
         if (group) {
-            void *unpacked = (char *)workspace + up256(p.parts * M * a->rank * 4);
+            void *unpacked = (char *)workspace + up256(lora_parts(M, K) * M * a->rank * 4);
             const int rc =
                 gemm_w4_dequantize(W, S, Z, unpacked, N, K, K, group, dtype, stream);
             if (rc != GEMM_OK)

@@ -9,7 +9,8 @@ from __future__ import annotations
 import ctypes
 
 from . import binding
-from .w4 import W4Weight, check_out, dtype_code, launch, on_stream, row_stride, stream_of
+from .w4 import (W4Weight, check_out, dtype_code, launch, new_rows, on_stream, row_stride,
+                 stream_of)
 
 
 class LoraAdapters:
@@ -58,13 +59,13 @@ def gemm_nt_lora(X, w, adapters: LoraAdapters, ids, out=None, stream=None, works
     tensor of ``binding.gemm_nt_lora_ws_size`` bytes, allocated here if none is given."""
     import torch
     packed = isinstance(w, W4Weight)
-    device, K = adapters.device, adapters.K
-    if len(w.shape) != 2 or tuple(w.shape) != (adapters.N, K) or X.dim() != 2 \
-            or X.shape[1] != K:
-        raise ValueError(f"shapes {tuple(X.shape)}, {tuple(w.shape)} and adapters of "
-                         f"{adapters.N} x {K} are not [M, K], [N, K] and N x K")
-    if X.dtype != adapters.dtype or w.dtype != adapters.dtype:
-        raise TypeError(f"X is {X.dtype}, the weight {w.dtype}, the adapters {adapters.dtype}")
+    device, K, N, dtype = adapters.device, adapters.K, adapters.N, adapters.dtype
+    shape = X.shape
+    if w.shape != (N, K) or len(shape) != 2 or shape[1] != K:
+        raise ValueError(f"shapes {tuple(shape)}, {tuple(w.shape)} and adapters of {N} x {K} are "
+                         "not [M, K], [N, K] and N x K")
+    if X.dtype != dtype or w.dtype != dtype:
+        raise TypeError(f"X is {X.dtype}, the weight {w.dtype}, the adapters {dtype}")
     if X.device != device or w.device != device or ids.device != device:
         raise ValueError("X, the weight, the ids and the adapters must be on the same GPU")
     if packed:
@@ -73,23 +74,24 @@ def gemm_nt_lora(X, w, adapters: LoraAdapters, ids, out=None, stream=None, works
         pointers, group = (w.data_ptr(), None, None), 0
     else:
         raise ValueError("the weight must be contiguous")
-    M, N = X.shape[0], adapters.N
-    if ids.dtype != torch.int32 or tuple(ids.shape) != (M,) or not ids.is_contiguous():
+    M = shape[0]
+    if ids.dtype != torch.int32 or ids.shape != (M,) or not ids.is_contiguous():
         raise ValueError(f"ids must be a contiguous int32 tensor of {M} values")
-    ldx = row_stride(X, "X")
-    need = binding.lib().gemm_nt_lora_ws_size(M, N, K, adapters.rank, group)
-    with on_stream(stream):
-        if out is None:
-            out, ldd = X.new_empty((M, N)), N
-        else:
-            check_out(out, (M, N), X.dtype, device)
-            ldd = row_stride(out, "out")
-        if workspace is None:
+    ldx = K if X.is_contiguous() else row_stride(X, "X")
+    if out is None:
+        out, ldd = new_rows(X, M, N, stream), N
+    else:
+        check_out(out, (M, N), dtype, device)
+        ldd = row_stride(out, "out")
+    if workspace is None:
+        need = binding.lib().gemm_nt_lora_ws_size(M, N, K, adapters.rank, group)
+        with on_stream(stream):
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        elif workspace.device != device or not workspace.is_contiguous():
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous, on X's device")
+        need = workspace.numel() * workspace.element_size()
     launch("gemm_nt_lora", device,
            (X.data_ptr(), *pointers, adapters._ref, ids.data_ptr(), out.data_ptr(), M, N, K, ldx,
-            ldd, group, adapters.code, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), stream_of(device, stream)))
+            ldd, group, adapters.code, workspace.data_ptr(), need, stream_of(device, stream)))
     return out

@@ -67,7 +67,7 @@ def choose_experts(logits, topk: int, scoring: str = "softmax", bias=None, group
     T, E = logits.shape
     device = logits.device
     g = _gate(E, device, topk, scoring, bias, groups, topk_groups, group_top, scale)
-    ldl = row_stride(logits, "logits")
+    ldl = E if logits.is_contiguous() else row_stride(logits, "logits")
     with on_stream(stream):
         ids = torch.empty((T, topk), dtype=torch.int32, device=device)
         weights = torch.empty((T, topk), dtype=torch.float32, device=device)

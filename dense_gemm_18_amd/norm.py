@@ -7,7 +7,7 @@ stream of the tensors' device); tensors that it makes are that stream's.
 from __future__ import annotations
 
 from . import binding
-from .w4 import check_out, dtype_code, launch, on_stream, row_stride, stream_of
+from .w4 import check_out, dtype_code, launch, new_rows, on_stream, row_stride, stream_of
 
 _FORMATS = None
 
@@ -26,38 +26,42 @@ def _format(dtype) -> int:
 
 
 def _rows(x, weight, residual, residual_out, stream):
-    """Checked operands: (type code, T, H, ldx, residual address, its stride, weight address,
-    the tensor for s or None, its stride)."""
-    code = dtype_code(x.dtype)
-    if x.dim() != 2 or not x.shape[1]:
-        raise ValueError(f"shape {tuple(x.shape)} is not [T, H]")
+    """Checked operands: (type code, device, T, H, ldx, residual address, its stride, weight
+    address, the tensor for s or None, its address, its stride)."""
+    dtype, shape, device = x.dtype, x.shape, x.device
+    code = dtype_code(dtype)
+    if len(shape) != 2 or not shape[1]:
+        raise ValueError(f"shape {tuple(shape)} is not [T, H]")
     if not x.is_cuda:
         raise ValueError("x must be on a GPU")
-    T, H = x.shape
-    w = None
+    T, H = shape
+    w = r = s = None
     if weight is not None:
-        if weight.dtype != x.dtype:
-            raise TypeError(f"x is {x.dtype}, the weight {weight.dtype}")
-        if tuple(weight.shape) != (H,) or not weight.is_contiguous() \
-                or weight.device != x.device:
+        if weight.dtype != dtype:
+            raise TypeError(f"x is {dtype}, the weight {weight.dtype}")
+        if weight.shape != (H,) or not weight.is_contiguous() or weight.device != device:
             raise ValueError(f"the weight must be a contiguous tensor of {H} elements on x's GPU")
         w = weight.data_ptr()
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out without a residual")
-        return code, T, H, row_stride(x, "x"), None, 0, w, None, 0
-    if residual.dtype != x.dtype:
-        raise TypeError(f"x is {x.dtype}, the residual {residual.dtype}")
-    if residual.shape != x.shape or residual.device != x.device:
-        raise ValueError(f"the residual must be of shape {tuple(x.shape)}, on x's GPU")
-    if residual_out is None:
-        with on_stream(stream):
-            residual_out, lds = x.new_empty((T, H)), H
-    else:
-        check_out(residual_out, (T, H), x.dtype, x.device)
-        lds = row_stride(residual_out, "residual_out")
-    return (code, T, H, row_stride(x, "x"), residual.data_ptr(), row_stride(residual, "residual"),
-            w, residual_out, lds)
+    ldx = ldr = lds = H
+    if not x.is_contiguous():
+        ldx = row_stride(x, "x")
+    if residual is not None:
+        if residual.dtype != dtype:
+            raise TypeError(f"x is {dtype}, the residual {residual.dtype}")
+        if residual.shape != shape or residual.device != device:
+            raise ValueError(f"the residual must be of shape {tuple(shape)}, on x's GPU")
+        r = residual.data_ptr()
+        if not residual.is_contiguous():
+            ldr = row_stride(residual, "residual")
+        if residual_out is None:
+            residual_out = new_rows(x, T, H, stream)
+        else:
+            check_out(residual_out, shape, dtype, device)
+            lds = row_stride(residual_out, "residual_out")
+        s = residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    return code, device, T, H, ldx, r, ldr, w, residual_out, s, lds
 
 
 def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, out=None, residual_out=None,
@@ -68,17 +72,16 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, out=None, residua
 
     All may have a row stride.  ``out`` and ``residual_out`` (optional) take the results;
     each may be x or the residual itself."""
-    code, T, H, ldx, r, ldr, w, s, lds = _rows(x, weight, residual, residual_out, stream)
+    code, device, T, H, ldx, r, ldr, w, total, s, lds = _rows(x, weight, residual, residual_out,
+                                                              stream)
     if out is None:
-        with on_stream(stream):
-            out, ldy = x.new_empty((T, H)), H
+        out, ldy = new_rows(x, T, H, stream), H
     else:
-        check_out(out, (T, H), x.dtype, x.device)
+        check_out(out, (T, H), x.dtype, device)
         ldy = row_stride(out, "out")
-    launch("rms_norm", x.device,
-           (x.data_ptr(), r, w, out.data_ptr(), None if s is None else s.data_ptr(), T, H, ldx,
-            ldr, ldy, lds, eps, code, stream_of(x.device, stream)))
-    return out if s is None else (out, s)
+    launch("rms_norm", device, (x.data_ptr(), r, w, out.data_ptr(), s, T, H, ldx, ldr, ldy, lds,
+                                eps, code, stream_of(device, stream)))
+    return out if s is None else (out, total)
 
 
 def rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, dtype=None, scale=None,
@@ -92,17 +95,18 @@ def rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, dtype=None, s
     if dtype is None:
         dtype = torch.float8_e4m3fn
     fmt = _format(dtype)
-    code, T, H, ldx, r, ldr, w, s, lds = _rows(x, weight, residual, residual_out, stream)
+    code, device, T, H, ldx, r, ldr, w, total, s, lds = _rows(x, weight, residual, residual_out,
+                                                              stream)
     with on_stream(stream):
         if out is None:
-            out, ldq = torch.empty((T, H), dtype=dtype, device=x.device), H
+            out, ldq = torch.empty((T, H), dtype=dtype, device=device), H
         else:
-            check_out(out, (T, H), dtype, x.device)
+            check_out(out, (T, H), dtype, device)
             ldq = row_stride(out, "out")
-        scales = torch.empty((T,), dtype=torch.float32, device=x.device) if scale is None else None
-    launch("rms_norm_fp8", x.device,
-           (x.data_ptr(), r, w, out.data_ptr(), None if scales is None else scales.data_ptr(),
-            None if s is None else s.data_ptr(), T, H, ldx, ldr, ldq, lds, eps,
-            0.0 if scale is None else scale, fmt, code, stream_of(x.device, stream)))
+        scales = torch.empty((T,), dtype=torch.float32, device=device) if scale is None else None
+    launch("rms_norm_fp8", device,
+           (x.data_ptr(), r, w, out.data_ptr(), None if scales is None else scales.data_ptr(), s,
+            T, H, ldx, ldr, ldq, lds, eps, 0.0 if scale is None else scale, fmt, code,
+            stream_of(device, stream)))
     held = scale if scales is None else scales
-    return (out, held) if s is None else (out, held, s)
+    return (out, held) if s is None else (out, held, total)

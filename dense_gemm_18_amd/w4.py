@@ -54,12 +54,24 @@ def on_device(device):
 
 def launch(name: str, device, args) -> None:
     """The raw entry point ``name`` with ``args`` on ``device``."""
+    import torch
     fn = getattr(binding.lib(), name)
     # the library launches on the current device: make it the operands' one
-    with on_device(device):
+    if device.index == torch.cuda.current_device():
         rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
     if rc != GEMM_OK:
         raise GemmError(rc, name)
+
+
+def new_rows(x, rows: int, cols: int, stream):
+    """An uninitialised [rows, cols] tensor like ``x``, ``stream``'s."""
+    if stream is None:
+        return x.new_empty((rows, cols))
+    with on_stream(stream):
+        return x.new_empty((rows, cols))
 
 
 def row_stride(x, what: str) -> int:
