@@ -118,10 +118,9 @@ int64_t moe_nt_ws_size(int64_t T, const moe_nt_weights *w, int topk);
  *   w_j = scale * score[e_j], with MOE_RENORMALIZE over the sum of the chosen scores
  *
  * Without a bias and with group_top 1 the order of the choices is that of the
- * logits; otherwise scores, choices and the groups' values are formed in 64 bits,
+ * logits; otherwise it is that of scores, choices and groups' values in 64 bits,
  * so that which experts are chosen does not hang on a rounding.  Weights are
- * formed in 64 bits and rounded to fp32 once; a softmax's sum over all experts is
- * formed in fp32 where the choices are not.
+ * formed in fp32, in 64 bits where the chosen scores' sum is too small for that.
  *
  * A row with a NaN logit, and with softmax one whose largest logit is infinite,
  * gets NaN weights and topk distinct valid ids.  A NaN choice comes after every

@@ -1,9 +1,8 @@
 """GPU checks of the choice of experts from logits against plain 64-bit forms.
 
-Tolerances: ids are equal (logits are given, choices are formed in 64 bits).  Weights are
-formed in 64 bits and rounded to fp32, 2^-24; a softmax's sum over all experts, formed in
-fp32 where there is neither a bias nor a sum of two, adds the roundings of 16 terms and 6
-joins and an exponential's 2: 2^-24 * 32 in all.  In a layer the logits are fp32 sums: those
+Tolerances: ids are equal (logits are given, choices decided as in 64 bits).  Weights are formed
+in fp32: a softmax's sum over all experts takes 16 terms and 6 joins, exponentials 2 each, the
+chosen ones' sum 4 joins, quotients and products 4: 2^-24 * 32 in all.  In a layer the logits are fp32 sums: those
 of the layer's own tests.
 """
 from __future__ import annotations
@@ -247,3 +246,118 @@ def test_layer_replayed(T):
         assert all(torch.equal(a, b) for a, b in zip(logits, choose_experts(X[:, :32], 4)))
         X.mul_(-0.75)
         bias.mul_(0.5)
+
+
+def vectorised(logits, topk, scoring="softmax", bias=None, groups=1, topk_groups=None,
+               group_top=1, renormalize=True, scale=1.0):
+    """The reference for many rows."""
+    score = scores_of(logits, scoring)
+    T, E = score.shape
+    choice = score if bias is None else score + bias.double()
+    kept, n = groups if topk_groups is None else topk_groups, E // groups
+    value = torch.topk(choice.view(T, groups, n), group_top, dim=-1).values.sum(-1)
+    best = torch.sort(value, dim=-1, descending=True, stable=True).indices[:, :kept]
+    keep = torch.zeros((T, groups), dtype=torch.bool, device=device()).scatter_(1, best, True)
+    choice = choice.masked_fill(~keep.repeat_interleave(n, 1), -math.inf)
+    ids = torch.sort(choice, dim=-1, descending=True, stable=True).indices[:, :topk]
+    w = score.gather(1, ids)
+    if renormalize:
+        w = w / w.sum(-1, keepdim=True)
+    return ids.to(torch.int32), w * scale
+
+
+def settled(logits, scoring, bias, groups, topk_groups, group_top, **_):
+    """Rows whose groups 64 bits tell apart: of two sums of two choices that differ by less
+    than 2^-50 of themselves, four roundings of 2^-53 and an exponential's two, which is
+    larger hangs on those roundings (logits of a - d, a + d against a, a have sums that
+    differ by d^2, here 2^-47 of a 64th part of them)."""
+    score = scores_of(logits, scoring)
+    choice = score if bias is None else score + bias.double()
+    value = torch.topk(choice.view(len(choice), groups, -1), group_top, dim=-1).values.sum(-1)
+    value = torch.sort(value, dim=-1, descending=True).values
+    if topk_groups >= groups:
+        return torch.ones(len(choice), dtype=torch.bool, device=device())
+    a, b = value[:, topk_groups - 1], value[:, topk_groups]
+    return a - b > 2.0 ** -50 * a.abs()
+
+
+def check_many(logits, topk, **kw):
+    ids, weights = choose_experts(logits, topk, **kw)
+    want_ids, want = vectorised(logits, topk, **kw)
+    same = (ids == want_ids).all(-1)
+    if kw.get("group_top", 1) == 2:
+        same |= ~settled(logits, **kw)
+    assert bool(same.all())
+    weights, want = weights[(ids == want_ids).all(-1)], want[(ids == want_ids).all(-1)]
+    # below the smallest normal number an exponential, its correction, a quotient and a
+    # product are off by up to 2, 1/2, 1/2 and 1/2 steps, and the quotient and the scale
+    # make the ones before them up to 4 times larger here
+    tiny = 16 * 2.0 ** -149
+    assert bool(((weights.double() - want).abs() <= 2.0 ** -24 * 32 * want + tiny).all())
+    return ids, weights
+
+
+#       T    E   topk groups kept
+MANY = [(1024, 64, 6, 1, 1), (1025, 64, 8, 8, 3), (2047, 128, 1, 1, 1), (3001, 128, 8, 16, 5),
+        (1500, 256, 8, 8, 4), (4099, 256, 14, 1, 1), (1026, 256, 5, 2, 1), (1027, 256, 15, 4, 3),
+        (1100, 256, 8, 32, 7), (1100, 200, 8, 8, 2), (2000, 64, 14, 4, 1), (1111, 128, 4, 4, 2)]
+
+
+@pytest.mark.parametrize("T,E,topk,groups,kept", MANY)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_many_tokens(T, E, topk, groups, kept, dtype):
+    note(f"gate many T{T} E{E} k{topk} groups {kept} of {groups} {dtype}")
+    g = gen(T + E + topk)
+    wide = (torch.randn((T, E + 3), generator=g, device=device()) * 2).to(dtype)
+    bias = torch.randn((E,), generator=g, device=device()) * 0.1
+    for logits in (wide[:, :E].contiguous(), wide[:, 1:E + 1]):
+        for scoring in ("softmax", "sigmoid"):
+            for b in (None, bias, bias * 30):
+                for renorm, top in ((True, 1), (False, 2)):
+                    check_many(logits, topk, scoring=scoring, bias=b, groups=groups,
+                               topk_groups=kept, group_top=top, renormalize=renorm,
+                               scale=2.5 if renorm else 1.0)
+
+
+@pytest.mark.parametrize("E", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens_with_equal_and_close_choices(E, dtype):
+    note(f"gate many ties E{E} {dtype}")
+    g = gen(E)
+    few = torch.randint(-2, 3, (1200, E), generator=g, device=device()).to(dtype)
+    close = torch.randn((1200, 1), generator=g, device=device()) * torch.ones(E, device=device())
+    step = torch.randint(-3, 4, (1200, E), generator=g, device=device()).float()
+    close = (close + step * close.abs() * 2.0 ** -23).to(dtype)
+    flat = torch.full((1030, E), -3.0, dtype=dtype, device=device())
+    far = (torch.randn((1200, E), generator=g, device=device()) * 40).to(dtype)
+    for logits in (few, close, flat, far):
+        for b in (None, torch.full((E,), 0.3, device=device())):
+            for groups, kept, top in ((1, 1, 1), (8, 2, 2), (4, 2, 1)):
+                kw = dict(bias=b, groups=groups, topk_groups=kept, group_top=top)
+                # a sigmoid that rounds to 1 in 64 bits hides the order of its logits
+                if logits is not far:
+                    check_many(logits, 6, scoring="sigmoid", **kw)
+                check_many(logits, 6, scoring="softmax", **kw)
+
+
+def test_many_tokens_with_infinities_and_nans():
+    note("gate many infinities")
+    E = 128
+    logits = torch.randn((1300, E), generator=gen(11), device=device())
+    logits[::7, 40:90] = -math.inf
+    logits[5] = math.nan
+    logits[9, 3] = math.nan
+    logits[11] = -math.inf
+    rows = torch.ones(1300, dtype=torch.bool, device=device())
+    rows[[5, 9, 11]] = False
+    for b in (None, torch.linspace(0.1, 0.2, E, device=device())):
+        for scoring in ("softmax", "sigmoid"):
+            kw = dict(scoring=scoring, bias=b, groups=4, topk_groups=2, group_top=2)
+            ids, weights = choose_experts(logits, 8, **kw)
+            want_ids, want = vectorised(logits[rows], 8, **kw)
+            assert torch.equal(ids[rows], want_ids)
+            assert bool(((weights[rows].double() - want).abs() <= 2.0 ** -24 * 32 * want).all())
+            assert bool(weights[5].isnan().all()) and bool(weights[9].isnan().all())
+            for r in (5, 9, 11):
+                assert len(set(ids[r].tolist())) == 8 and int(ids[r].min()) >= 0
+                assert int(ids[r].max()) < E
