@@ -5,7 +5,6 @@
 namespace {
 
 constexpr int kGateWaves = 4;       // of a workgroup
-constexpr int kGateMany = 1024;     // tokens from which four share a wave
 
 // The order of logits as unsigned numbers: rising with the value, both zeros alike,
 // every NaN below everything, 0 left for what is absent or taken.
@@ -477,7 +476,7 @@ __global__ void __launch_bounds__(kGateWaves * 64) moe_gate_kernel(GateArgs p)
         gate_token<PER, WIDE, PLAIN>(p, t, choices + wave * p.E);
 }
 
-// ---- many tokens of 64, 128 or 256 experts -------------------------------
+// ---- 64, 128 or many tokens of 256 experts --------------------------------
 
 // Reductions over 16 lanes, a token's, the result in each of them.
 template <int CTRL>
@@ -530,9 +529,10 @@ __device__ __forceinline__ void sort_keys(uint32_t (&c)[PER])
 // the fixed point's range; NaN and infinite ones), the whole wave does the token again with
 // gate_token: one in ten thousand or so.  16-bit logits without WIDE have their order in the
 // upper 16 bits (fp16: 19) of their numbers in fp32: exact.
-// 16384 tokens of 256 experts in 8 groups, 8 chosen, a bias, took 26.8 us with a token to
-// a wave, 675 VALU instructions for each, which bound it.
-// SPAN: lanes of a group, a power of two; 0: one group.
+// 16384 tokens of 256 experts in 8 groups, 8 chosen, a bias: 14 us (its bytes take 3), 277 VALU
+// instructions to a token, which with the latency of four waves to a SIMD bound it; 26.8 us
+// and 675 instructions with a token to a wave, 28.7 in 64 bits throughout.
+// span: lanes of a group, a power of two; 0: one group.
 template <int PER, bool WIDE, int TYPE>
 __global__ void __launch_bounds__(kGateWaves * 64) moe_gate_many_kernel(GateArgs p, int span)
 {
@@ -759,11 +759,14 @@ void launch_many_typed(const GateArgs &a, int span, hipStream_t stream)
 }
 
 // Whether that kernel can take the call, and if so launches it: groups of whole lanes, a
-// power of two of them, and few enough chosen for the one after them to have a lane.
+// power of two of them, and few enough chosen for the two after them to have lanes.  In us,
+// a token to a wave / four, 8 chosen: 64 experts, 64 tokens 3.3 / 3.0, 16384 8.6 / 4.7; 128,
+// bias and 8 groups, 512 tokens 8.0 / 4.5, 16384 18.6 / 11.5; 256, 1024 tokens 4.1 / 4.6 and
+// with bias and groups 6.4 / 6.5, 2048 4.3 / 4.7 and 10.6 / 6.6, 16384 11.8 / 7.8 and 23.5 /
+// 12.2.
 bool launch_many_tokens(const GateArgs &a, hipStream_t stream)
 {
-    if ((a.E != 64 && a.E != 128 && a.E != 256) || a.parts != 1 || a.topk > 14 ||
-        a.T < kGateMany)
+    if ((a.E != 64 && a.E != 128 && (a.E != 256 || a.T < 2048)) || a.parts != 1 || a.topk > 14)
         return false;
     int span = 0;
     if (a.groups > 1) {

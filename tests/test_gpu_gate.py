@@ -300,7 +300,7 @@ def check_many(logits, topk, **kw):
 #       T    E   topk groups kept
 MANY = [(1024, 64, 6, 1, 1), (1025, 64, 8, 8, 3), (2047, 128, 1, 1, 1), (3001, 128, 8, 16, 5),
         (1500, 256, 8, 8, 4), (4099, 256, 14, 1, 1), (1026, 256, 5, 2, 1), (1027, 256, 15, 4, 3),
-        (1100, 256, 8, 32, 7), (1100, 200, 8, 8, 2), (2000, 64, 14, 4, 1), (1111, 128, 4, 4, 2)]
+        (2050, 256, 8, 8, 4), (2100, 256, 5, 2, 1), (2049, 256, 14, 16, 7), (1100, 256, 8, 32, 7), (1100, 200, 8, 8, 2), (2000, 64, 14, 4, 1), (1111, 128, 4, 4, 2)]
 
 
 @pytest.mark.parametrize("T,E,topk,groups,kept", MANY)
@@ -324,12 +324,13 @@ def test_many_tokens(T, E, topk, groups, kept, dtype):
 def test_many_tokens_with_equal_and_close_choices(E, dtype):
     note(f"gate many ties E{E} {dtype}")
     g = gen(E)
-    few = torch.randint(-2, 3, (1200, E), generator=g, device=device()).to(dtype)
-    close = torch.randn((1200, 1), generator=g, device=device()) * torch.ones(E, device=device())
-    step = torch.randint(-3, 4, (1200, E), generator=g, device=device()).float()
+    T = 2100 if E == 256 else 1200
+    few = torch.randint(-2, 3, (T, E), generator=g, device=device()).to(dtype)
+    close = torch.randn((T, 1), generator=g, device=device()) * torch.ones(E, device=device())
+    step = torch.randint(-3, 4, (T, E), generator=g, device=device()).float()
     close = (close + step * close.abs() * 2.0 ** -23).to(dtype)
-    flat = torch.full((1030, E), -3.0, dtype=dtype, device=device())
-    far = (torch.randn((1200, E), generator=g, device=device()) * 40).to(dtype)
+    flat = torch.full((T, E), -3.0, dtype=dtype, device=device())
+    far = (torch.randn((T, E), generator=g, device=device()) * 40).to(dtype)
     for logits in (few, close, flat, far):
         for b in (None, torch.full((E,), 0.3, device=device())):
             for groups, kept, top in ((1, 1, 1), (8, 2, 2), (4, 2, 1)):
