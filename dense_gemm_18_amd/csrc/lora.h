@@ -300,21 +300,23 @@ void lora_fused(const LoraArgs &p, const W4Args &w, int group, hipStream_t strea
 // afterwards), is in LDS.  Each wave takes pairs of an adapter and 64 columns: the adapter's
 // rows of B, which come straight to registers, meet every 16 rows that hold one of its own,
 // and only its own are stored, so what is infinite in one adapter stays out of the others'
-// rows.  While one pair is multiplied, the next one's rows of B travel.  Results go through
-// the wave's own LDS 16 rows at a time, whole 128-byte lines of a row leave together.  Where
+// rows.  The rows of B of several pairs travel at once, the first ones' while u is summed.
+// Results go through the wave's own LDS 16 rows at a time, whole 128-byte lines of a row leave together.  Where
 // there are few tiles, p.split workgroups share one's adapters.  KS: pieces of 32 of the
 // rank.
 constexpr int kExpandLine = 64 * 2 + 16;         // bytes of a staged row
 
-template <bool BF, int KS>
-__global__ void __launch_bounds__(512, KS == 1 ? 4 : 2) lora_expand_kernel(LoraArgs p)
+// TAIL: the rank is no multiple of 8.
+template <bool BF, int KS, bool TAIL>
+__global__ void __launch_bounds__(512, 2) lora_expand_kernel(LoraArgs p)
 {
     using x8 = typename Elem<BF>::x8;
     constexpr int kLd = KS * 32 + 8;             // 16-bit elements of a row of u
+    constexpr int kAhead = TAIL ? 1 : KS == 1 ? 4 : KS == 2 ? 2 : 1;   // pairs of a wave at once
     extern __shared__ f32x4 lds[];
     __shared__ float unscale[64];
     __shared__ int adapter[64];
-    __shared__ uint64_t has[64];
+    __shared__ uint64_t has[64], with[64];
     const int blocks = (p.N + p.columns - 1) / p.columns;
     uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
     const int n0 = (int)(wg % blocks) * p.columns;
@@ -327,19 +329,23 @@ __global__ void __launch_bounds__(512, KS == 1 ? 4 : 2) lora_expand_kernel(LoraA
     const int id = adapter_of(p, m0 + lane);
     uint16_t *held = (uint16_t *)lds;
     char *stage = (char *)lds + 64 * kLd * 2 + wave * (16 * kExpandLine);
-    // this workgroup's adapters of the tile, by every wave alike
-    int count = 0;
-    for (uint64_t left = __ballot(id >= 0), i = 0; left; ++i) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        const uint64_t same = __ballot(id == a);
-        left &= ~same;
-        if (i % p.split != (uint32_t)share)
-            continue;
-        if (threadIdx.x == 0) {
-            adapter[count] = a;
-            has[count] = same;
-        }
-        ++count;
+    // The tile's adapters by their first rows, eight rows to a wave, and of these the ones
+    // that are this workgroup's.
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int m = 8 * wave + i;
+        const uint64_t same = __ballot(id == __builtin_amdgcn_readlane(id, m));
+        if (lane == 0)
+            with[m] = same;
+    }
+    __syncthreads();
+    const uint64_t mine = with[lane];
+    const uint64_t firsts = __ballot(id >= 0 && __builtin_ctzll(mine) == lane);
+    const int total = __popcll(firsts), index = __popcll(firsts & ((1ull << lane) - 1));
+    const int count = (total - share + p.split - 1) / p.split;
+    if (wave == 0 && (firsts >> lane & 1) && index % p.split == share) {
+        adapter[index / p.split] = id;
+        has[index / p.split] = mine;
     }
     __syncthreads();
     const int c = lane >> 4, col = lane & 15;
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(512, KS == 1 ? 4 : 2) lora_expand_kernel(LoraA
         const auto rs = range(p.B + ((int64_t)a * p.N + n) * p.rank,
                               (uint32_t)(rows * p.rank) * 2u);
         u32x4 v[4][KS];
-        uint32_t end[4];
+        [[maybe_unused]] uint32_t end[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t row = (uint32_t)((col + 16 * i) * p.rank) * 2u;
@@ -363,11 +369,11 @@ __global__ void __launch_bounds__(512, KS == 1 ? 4 : 2) lora_expand_kernel(LoraA
             for (int q = 0; q < KS; ++q)
                 v[i][q] = load_b128(rs, 32 * q + 8 * c < p.rank ? row + (32 * q + 8 * c) * 2u
                                                                 : kOob);
-            if (p.rank & 1)
+            if (TAIL && (p.rank & 1))
                 end[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
                     rs, row + (p.rank - 1) * 2u, 0, 0);
         }
-        if (p.rank & 7) {
+        if constexpr (TAIL) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -389,9 +395,14 @@ __global__ void __launch_bounds__(512, KS == 1 ? 4 : 2) lora_expand_kernel(LoraA
             for (int q = 0; q < KS; ++q)
                 w[i][q] = __builtin_bit_cast(x8, v[i][q]);
     };
-    Rows even, odd;
-    if (wave < pairs)
-        fetch(even, wave);
+    Rows w[kAhead];
+    auto fetch_from = [&](int first) G18_INLINE {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (first + 8 * i < pairs)
+                fetch(w[i], first + 8 * i);
+    };
+    fetch_from(wave);
     {
         // eight lanes to a row
         const int m = threadIdx.x >> 3, j0 = threadIdx.x & 7;
@@ -481,14 +492,13 @@ __global__ void __launch_bounds__(512, KS == 1 ? 4 : 2) lora_expand_kernel(LoraA
             asm volatile("" ::: "memory");
         }
     };
-    for (int i = wave; i < pairs; i += 16) {
-        if (i + 8 < pairs)
-            fetch(odd, i + 8);
-        consume(even, i);
-        if (i + 16 < pairs)
-            fetch(even, i + 16);
-        if (i + 8 < pairs)
-            consume(odd, i + 8);
+    for (int first = wave; first < pairs; first += 8 * kAhead) {
+        if (first != wave)
+            fetch_from(first);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (first + 8 * i < pairs)
+                consume(w[i], first + 8 * i);
     }
     // rows without an adapter
     const uint64_t bare = __ballot(id < 0 && m0 + lane < p.M);
@@ -503,9 +513,15 @@ __global__ void __launch_bounds__(512, KS == 1 ? 4 : 2) lora_expand_kernel(LoraA
 template <bool BF, int KS>
 void launch_expand(const LoraArgs &p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((lora_expand_kernel<BF, KS>),
-                       tile_grid(cdiv(p.M, 64) * cdiv(p.N, p.columns) * p.split), dim3(512),
-                       64 * (KS * 32 + 8) * 2 + 8 * 16 * kExpandLine, stream, p);
+    const auto go = [&](auto tail) {
+        hipLaunchKernelGGL((lora_expand_kernel<BF, KS, decltype(tail)::value>),
+                           tile_grid(cdiv(p.M, 64) * cdiv(p.N, p.columns) * p.split), dim3(512),
+                           64 * (KS * 32 + 8) * 2 + 8 * 16 * kExpandLine, stream, p);
+    };
+    if (p.rank % 8)
+        go(std::true_type{});
+    else
+        go(std::false_type{});
 }
 
 // As many columns to a workgroup, 64 to 512, as leave each compute unit one; and where even
