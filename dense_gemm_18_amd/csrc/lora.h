@@ -5,8 +5,9 @@
 #include "lora_nt.h"
 #include "w4_product.h"
 
-// Rows of a tile of the first product.
+// Rows of a tile of the first product, and of one where there are many.
 constexpr int kLoraRows = 32;
+constexpr int kLoraMany = 64;
 // Values of u that a tile of the projection holds in LDS: its rows times the rank.
 constexpr int kLoraHeld = 4096;
 
@@ -22,13 +23,22 @@ struct LoraArgs {
     int columns, split;            // of a workgroup of the second product; who share adapters
 };
 
-// Pieces of K in the first product, and with them of u, at most: what the workspace has room
-// for.  Of 512 elements or more; the fewer the tiles of rows, the more of them.
-inline int lora_parts(int64_t M, int64_t K)
+// Whether the first product runs on the tiles of more rows, 64 of the rank to a workgroup.
+inline bool lora_many(int64_t M, int64_t rank) { return M > 512 && rank > 32; }
+
+// Tiles of the first product, with the blocks of the rank that take a workgroup each there.
+inline int64_t lora_tiles(int64_t M, int64_t rank)
 {
-    const int64_t tiles = cdiv(M, kLoraRows);
+    return lora_many(M, rank) ? cdiv(M, kLoraMany) * cdiv(rank, 64) : cdiv(M, kLoraRows);
+}
+
+// Pieces of K in the first product, and with them of u, at most: what the workspace has room
+// for.  Of 512 elements or more; the fewer the tiles, the more of them.
+inline int lora_parts(int64_t M, int64_t K, int64_t rank)
+{
+    const int64_t tiles = lora_tiles(M, rank), most = lora_many(M, rank) || tiles < 8 ? 8 : 4;
     int64_t p = tiles < 8 ? 8 : kCUs / tiles;
-    p = tiles >= 8 && p > 4 ? 4 : p < 1 ? 1 : p;
+    p = p > most ? most : p < 1 ? 1 : p;
     return (int)(p < cdiv(K, 512) ? p : cdiv(K, 512));
 }
 
@@ -88,52 +98,55 @@ __device__ __forceinline__ uint64_t rows_of(int id, int item)
 // core of skinny.h with A's rows as the weight: each workgroup looks for its items among the
 // tile's ids and gathers their rows, so an adapter is read once for the rows that have it
 // and no row is multiplied with another's.
-template <bool BF, int RB, int MB>
+template <bool BF, int RB, int MB, int NW>
 __device__ __forceinline__ void lora_item(const LoraArgs &p, char *lds, const int *list, int rows,
-                                          int64_t m0, int a, int rb, int part)
+                                          int64_t m0, int tile, int a, int rb, int part)
 {
+    constexpr int kEach = 16 * RB * NW;
     const int steps = (p.K + 127) >> 7;
     const int k0 = part * steps / p.parts * 128;
-    Skinny<BF, 0, RB, MB, 8, 1, true> c;
+    Skinny<BF, 0, RB, MB, 8 / NW, NW, true> c;
     c.W.w = p.A + k0;
-    c.row[0] = (int64_t)a * p.rank + rb * (16 * RB);
-    c.rows[0] = p.rank - rb * (16 * RB);
+    c.row[0] = (int64_t)a * p.rank + rb * kEach;
+    c.rows[0] = p.rank - rb * kEach;
     c.stride = p.K;
     c.K = min((part + 1) * steps / p.parts * 128, p.K) - k0;
     c.M = rows;
     c.begin(lds, p.X + m0 * p.ldx + k0,
-            (uint32_t)((min((int64_t)kLoraRows, p.M - m0) - 1) * p.ldx + c.K) * 2u);
+            (uint32_t)((min((int64_t)tile, p.M - m0) - 1) * p.ldx + c.K) * 2u);
     c.run([&](int m) { return (uint32_t)(list[m] * p.ldx) * 2u; });
     const float s = p.s ? p.s[a] : 1.0f;
-    float *u = p.u + ((int64_t)part * p.M + m0) * p.rank + rb * (16 * RB);
+    float *u = p.u + ((int64_t)part * p.M + m0) * p.rank;
     c.join([&](int m, int n, const float(&v)[RB]) {
+        const int j = rb * kEach + (n >> 4) * (16 * RB) + (n & 15);
 #pragma unroll
         for (int r = 0; r < RB; ++r)
-            if (rb * (16 * RB) + 16 * r + n < p.rank)
-                u[(int64_t)list[m] * p.rank + 16 * r + n] = v[r] * s;
+            if (j + 16 * r < p.rank)
+                u[(int64_t)list[m] * p.rank + j + 16 * r] = v[r] * s;
     });
 }
 
-template <bool BF, int RB>
+// RB * NW: blocks of 16 of the rank; TM: rows of a tile.
+template <bool BF, int RB, int NW, int TM>
 __global__ void __launch_bounds__(512, 2) lora_shrink_kernel(LoraArgs p)
 {
     extern __shared__ f32x4 lds[];
-    __shared__ int list[kLoraRows];
+    __shared__ int list[TM];
     // Items vary slowest: those that find no adapter are then the last workgroups.  (Between
     // the others, and dealt to the XCDs by turns, they left half of these idle: 34 us instead
     // of 19 for 2048 rows of 8192, rank 64, with a second item to each tile.)
     int64_t wg = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
-    const int64_t tiles = (p.M + (int64_t)kLoraRows - 1) / kLoraRows;
+    const int64_t tiles = (p.M + (int64_t)TM - 1) / TM;
     const int part = (int)(wg % p.parts);
     wg /= p.parts;
     const int rb = (int)(wg % p.rblocks);
     wg /= p.rblocks;
-    const int64_t m0 = wg % tiles * kLoraRows;
+    const int64_t m0 = wg % tiles * TM;
     wg /= tiles;
     if (wg >= p.items)
         return;
     const int lane = threadIdx.x & 63;
-    const int id = lane < kLoraRows ? adapter_of(p, m0 + lane) : -1;
+    const int id = lane < TM ? adapter_of(p, m0 + lane) : -1;
     for (int item = (int)wg;; item += p.items) {
         const uint64_t mask = rows_of(id, item);
         if (!mask)
@@ -145,44 +158,56 @@ __global__ void __launch_bounds__(512, 2) lora_shrink_kernel(LoraArgs p)
         __syncthreads();
         const int rows = __popcll(mask);
         if (rows <= 16)
-            lora_item<BF, RB, 1>(p, (char *)lds, list, rows, m0, a, rb, part);
-        else
-            lora_item<BF, RB, 2>(p, (char *)lds, list, rows, m0, a, rb, part);
+            lora_item<BF, RB, 1, NW>(p, (char *)lds, list, rows, m0, TM, a, rb, part);
+        else if (TM <= 32 || rows <= 32)
+            lora_item<BF, RB, 2, NW>(p, (char *)lds, list, rows, m0, TM, a, rb, part);
+        else if constexpr (TM > 32)
+            lora_item<BF, RB, 4, NW>(p, (char *)lds, list, rows, m0, TM, a, rb, part);
     }
 }
 
-template <bool BF, int RB>
+template <bool BF, int RB, int NW, int TM>
 void launch_shrink(LoraArgs p, hipStream_t stream)
 {
-    p.rblocks = (int)cdiv(p.rank, 16 * RB);
-    const int rows = p.M < kLoraRows ? p.M : kLoraRows;
+    p.rblocks = (int)cdiv(p.rank, 16 * RB * NW);
+    const int rows = p.M < TM ? p.M : TM;
     const int k = (int)cdiv(cdiv(p.K, 128), p.parts) * 128;
-    const int one = Skinny<BF, 0, RB, 1, 8, 1, true>::lds_bytes(rows < 16 ? rows : 16, k);
-    const int two = Skinny<BF, 0, RB, 2, 8, 1, true>::lds_bytes(rows, k);
-    hipLaunchKernelGGL((lora_shrink_kernel<BF, RB>),
-                       tile_grid(cdiv(p.M, kLoraRows) * p.items * p.rblocks * p.parts), dim3(512),
-                       one > two ? one : two, stream, p);
+    constexpr int KW = 8 / NW;
+    int lds = Skinny<BF, 0, RB, 1, KW, NW, true>::lds_bytes(rows < 16 ? rows : 16, k);
+    const int two = Skinny<BF, 0, RB, 2, KW, NW, true>::lds_bytes(rows < 32 ? rows : 32, k);
+    lds = lds > two ? lds : two;
+    if constexpr (TM > 32) {
+        const int four = Skinny<BF, 0, RB, 4, KW, NW, true>::lds_bytes(rows, k);
+        lds = lds > four ? lds : four;
+    }
+    hipLaunchKernelGGL((lora_shrink_kernel<BF, RB, NW, TM>),
+                       tile_grid(cdiv(p.M, TM) * p.items * p.rblocks * p.parts), dim3(512), lds,
+                       stream, p);
 }
 
 // How a tile of rows is shared.  Few tiles are a decode step, whose rows may all have
 // adapters of their own: a workgroup for each, K in as many pieces as fill the compute units.
-// Many are prompts, with one or two adapters to a tile and more rows of A to a workgroup, so
-// that X is read less often.  Measured, K = 8192, in us: 64 rows of 32 adapters of rank 16
-// in 4 pieces 8.8, in 2 10.4, in 8 14.0; of rank 64, 16 or 32 rows of A to a workgroup, 18.2
-// (2 pieces) and 15.4 (4); 2048 rows in runs of 256, rank 64, 16, 32 or 64 rows of A, 4 pieces,
-// 36, 26 and 18.8 (8 pieces: 44, 27 and 21.8).
+// Many are prompts, with one or two adapters to a tile.  A compute unit loads 25 bytes or so
+// in a ns, which bounds them: tiles of 64 rows and 64 of the rank read X and the adapters
+// least often.  Measured, K = 8192, in us: 64 rows of 32 adapters of rank 16 in 4 pieces 8.8,
+// in 2 10.4, in 8 14.0; 2048 rows in runs of 220, rank 64, tiles of 32 rows, in 4 pieces 28.8,
+// in 8 32.7, of 64 rows 32.6 and 20.4 (with a second workgroup for a tile's adapters 26.0);
+// 1024 rows 16.6 and 13.1.
 inline LoraArgs lora_shared(LoraArgs p)
 {
-    const int64_t tiles = cdiv(p.M, kLoraRows);
-    const int most = lora_parts(p.M, p.K);
-    int items = p.count < kLoraRows ? p.count : kLoraRows;
+    const bool many = lora_many(p.M, p.rank);
+    const int rows = many ? kLoraMany : kLoraRows;
+    const int64_t tiles = lora_tiles(p.M, p.rank);
+    const int most = lora_parts(p.M, p.K, p.rank);
+    int items = p.count < rows ? p.count : rows;
     items = items < p.M ? items : p.M;
-    if (tiles < 8) {
+    if (!many && tiles < 8) {
         const int64_t fill = kCUs / (tiles * items);
         p.parts = (int)(fill < 1 ? 1 : fill < most ? fill : most);
     } else {
         p.parts = most;
-        const int64_t fill = tiles < 32 ? 8 : cdiv(2 * kCUs, tiles * most);
+        const int64_t fill = many ? cdiv(kCUs, tiles * most)
+                             : tiles < 32 ? 8 : cdiv(2 * kCUs, tiles * most);
         items = (int)(items < fill ? items : fill);
     }
     p.items = items;
@@ -193,12 +218,12 @@ template <bool BF>
 void lora_shrink(const LoraArgs &p, hipStream_t stream)
 {
     const int64_t tiles = cdiv(p.M, kLoraRows);
-    if (p.rank <= 16 || p.M <= 16 || (p.rank <= 32 && tiles < 8))
-        launch_shrink<BF, 1>(p, stream);
-    else if (p.rank <= 32 || tiles < 32)
-        launch_shrink<BF, 2>(p, stream);
+    if (lora_many(p.M, p.rank))
+        launch_shrink<BF, 2, 2, kLoraMany>(p, stream);
+    else if (p.rank <= 16 || p.M <= 16 || (p.rank <= 32 && tiles < 8))
+        launch_shrink<BF, 1, 1, kLoraRows>(p, stream);
     else
-        launch_shrink<BF, 4>(p, stream);
+        launch_shrink<BF, 2, 1, kLoraRows>(p, stream);
 }
 
 // ---- beside the projection's tiles ---------------------------------------
@@ -524,7 +549,7 @@ void launch_expand(const LoraArgs &p, hipStream_t stream)
         go(std::false_type{});
 }
 
-// As many columns to a workgroup, 64 to 512, as leave each compute unit one; and where even
+// As many columns to a workgroup, 64 to 1024, as leave each compute unit one; and where even
 // 64 are not few enough, several that share a tile's adapters, down to eight for each.
 // Measured, rank 16, in us: 64 x 16384, 32 adapters, 64 columns 13.3, 128 18, two sharing 14.7;
 // 64 x 8192 12.8 and 10.5; 2048 x 8192, 512 columns 10.6, 256 14.3.
@@ -532,7 +557,7 @@ template <bool BF>
 void lora_expand(LoraArgs p, hipStream_t stream)
 {
     const auto wgs = [&] { return cdiv(p.M, 64) * cdiv(p.N, p.columns); };
-    p.columns = 512;
+    p.columns = 1024;
     while (p.columns > 64 && wgs() < kCUs)
         p.columns /= 2;
     const int64_t most = cdiv(p.count < 64 ? p.count : 64, 8), fill = kCUs / wgs();

@@ -46,7 +46,7 @@ int64_t gemm_nt_lora_ws_size(int64_t M, int64_t N, int64_t K, int64_t rank, int 
 {
     if (!sizes_ok_lora(M, N, K, rank, group) || M == 0 || N == 0 || K == 0)
         return 0;
-    int64_t bytes = up256(lora_parts(M, K) * M * rank * 4);
+    int64_t bytes = up256(lora_parts(M, K, rank) * M * rank * 4);
     if (group && large(M, N, group))
         bytes += up256(N * K * 2);
     return bytes;
@@ -118,7 +118,7 @@ int gemm_nt_lora(const void *X, const void *W, const void *S, const void *Z,
     if (ldx == K && ldd == N && large(M, N, group)) {
         const void *weight = W;
         if (group) {
-            void *unpacked = (char *)workspace + up256(lora_parts(M, K) * M * a->rank * 4);
+            void *unpacked = (char *)workspace + up256(lora_parts(M, K, a->rank) * M * a->rank * 4);
             const int rc =
                 gemm_w4_dequantize(W, S, Z, unpacked, N, K, K, group, dtype, stream);
             if (rc != GEMM_OK)
