@@ -128,9 +128,14 @@ __device__ __forceinline__ float wider(float most, float v)
 __device__ __forceinline__ float plus(float a, float b) { return a + b; }
 __device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
 
-// Rows whose sum of squares passes fp32's range are multiplied by this first: 2^22 squares
-// of 2^128 times it are in range, and eps no longer counts.
-constexpr float kShrink = 0x1p-80f;
+// What a row is multiplied by first, and eps by its square, where the sum of squares leaves
+// fp32's range: 2^22 squares of 2^128 times 2^-80 are in it, and so are, times 2^80, those of
+// the smallest numbers there are.  Where the mean and eps are above 2^-120, squares that vanish,
+// 2^-150 each, do not count.
+__device__ __forceinline__ float range_of(float sum, int H, float eps)
+{
+    return sum == __builtin_inff() ? 0x1p-80f : sum / (float)H + eps < 0x1p-120f ? 0x1p80f : 1.0f;
+}
 // What s is multiplied by.
 __device__ __forceinline__ float inverse(float sum, int H, float eps)
 {
@@ -171,8 +176,8 @@ __device__ __forceinline__ u32x2 scaled_bits(const float (&y)[8], const Scale &s
     return eight_bits<FP8>(q);
 }
 
-// A row in the registers of W waves, V times 8 elements to a lane: one pass over memory.
-// FP8: the format, or -1 for 16-bit rows.
+// A row in the registers of W waves, V times 8 elements to a lane: one pass over memory, which
+// bounds it.  FP8: the format, or -1 for 16-bit rows.
 template <bool BF, int FP8, int W, int V>
 __global__ void __launch_bounds__(W == 1 ? 256 : W * 64) rms_norm_kernel(NormArgs p)
 {
@@ -206,14 +211,15 @@ __global__ void __launch_bounds__(W == 1 ? 256 : W * 64) rms_norm_kernel(NormArg
     }
     sum = over_row<W>(sum, red[0], plus);
     float eps = p.eps;
-    if (sum == __builtin_inff()) {
+    const float range = range_of(sum, p.H, eps);
+    if (range != 1.0f) {
         sum = 0.0f;
-        eps = 0.0f;
+        eps = eps * range * range;
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                s[i][e] *= kShrink;
+                s[i][e] *= range;
                 sum = __builtin_fmaf(s[i][e], s[i][e], sum);
             }
         sum = over_row<W>(sum, red[1], plus);
@@ -255,7 +261,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : W * 64) rms_norm_kernel(NormArg
 }
 
 // Rows of any length, by 16 waves: over the squares, over |y| where scales are wanted,
-// and to write, each pass reading the row again.
+// and to write, each pass reading the row again (out of the caches: 4096 rows of 40960 take
+// 343 us, 3.4 TB/s).
 template <bool BF, int FP8>
 __global__ void __launch_bounds__(1024) rms_norm_long_kernel(NormArgs p)
 {
@@ -274,29 +281,29 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(NormArgs p)
                 s[e] += element<BF>(r, e);
         }
     };
-    auto squares = [&](float shrink) G18_INLINE {
+    auto squares = [&](float range) G18_INLINE {
         float sum = 0.0f, s[8];
         for (int k = at; k < p.H; k += 8192) {
             row(k, s);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                sum = __builtin_fmaf(s[e] * shrink, s[e] * shrink, sum);
+                sum = __builtin_fmaf(s[e] * range, s[e] * range, sum);
         }
         return sum;
     };
-    float shrink = 1.0f, eps = p.eps;
+    float eps = p.eps;
     float sum = over_row<16>(squares(1.0f), red[0], plus);
-    if (sum == __builtin_inff()) {
-        shrink = kShrink;
-        eps = 0.0f;
-        sum = over_row<16>(squares(kShrink), red[1], plus);
+    const float range = range_of(sum, p.H, eps);
+    if (range != 1.0f) {
+        eps = eps * range * range;
+        sum = over_row<16>(squares(range), red[1], plus);
     }
     const float by = inverse(sum, p.H, eps);
     auto normed = [&](int k, const float(&s)[8], float(&y)[8]) G18_INLINE {
         const u32x4 w = p.W ? load_eight(p.W + k, p.H - k) : u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            y[e] = s[e] * shrink * by;
+            y[e] = s[e] * range * by;
             if (p.W)
                 y[e] *= element<BF>(w, e);
         }
@@ -348,8 +355,16 @@ void launch_rows(const NormArgs &p, hipStream_t stream)
                        dim3(W == 1 ? 256 : W * 64), 0, stream, p);
 }
 
-// Waves to a row: the fewest whose registers hold it, or, where the rows are not even one
-// for each compute unit, as many as leave a lane 8 elements.
+// Waves to a row: with few rows a lane has few elements, with many a row few waves, as little
+// waits for the others then.  In us (residual, weights, E4M3 rows with scales; waves x eights of
+// a lane):
+//   row                 1024              2048              4096              8192
+//   256 rows    4x1 3.8 1x2 4.2   4x1 4.0 1x4 6.0   4x2 5.1 16x1 5.9   16x1 7.4 4x4 7.8
+//   512         4x1 4.3 1x2 4.4   4x1 4.8 1x4 6.2   4x2 6.8 16x1 9.1  16x1 11.3 4x4 10.9
+//   2048        4x1 8.8 1x2 6.6  4x1 10.8 1x4 10.9  4x2 15.1 4x4 19.6 16x1 30.8 4x4 27.5
+//   16384      4x1 40.3 1x2 24.8 4x1 46.3 1x4 45.4  4x2 81.5 4x4 91.4  16x1 196 4x4 163
+// one row of 16384 16x2 5.6, three passes 7.3; 2048 rows of 32768 16x4 112, three passes 144.
+// 16384 rows of 8192 move 939 MB, 5.8 TB/s: more than a copy of 1 GiB (5.1).
 template <bool BF, int FP8>
 void launch_norm(const NormArgs &p, hipStream_t stream)
 {
@@ -358,11 +373,9 @@ void launch_norm(const NormArgs &p, hipStream_t stream)
         launch_rows<BF, FP8, 1, 1>(p, stream);
     else if (p.H <= 1024 && !few)
         launch_rows<BF, FP8, 1, 2>(p, stream);
-    else if (p.H <= 2048 && !few)
-        launch_rows<BF, FP8, 1, 4>(p, stream);
     else if (p.H <= 2048)
         launch_rows<BF, FP8, 4, 1>(p, stream);
-    else if (p.H <= 4096 && !few)
+    else if (p.H <= 4096)
         launch_rows<BF, FP8, 4, 2>(p, stream);
     else if (p.H <= 8192 && !few)
         launch_rows<BF, FP8, 4, 4>(p, stream);

@@ -215,3 +215,22 @@ def test_replayed_and_on_another_stream():
             assert torch.equal(q.view(torch.uint8), got[0].view(torch.uint8))
             assert torch.equal(scales, got[1]) and torch.equal(bits(s), bits(got[2]))
         x.mul_(-0.5)
+
+
+@pytest.mark.parametrize("H", [1, 100, 1000, 4097, 9000, 40000])
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -140, 2.0 ** -125, 2.0 ** -119, 2.0 ** -80])
+def test_squares_below_the_range(H, eps):
+    """bfloat16 rows whose squares vanish in fp32; powers of two are exact, so the tolerance is
+    that of any row; what vanishes beside a mean and eps above 2^-120, 2^-30 of
+    it, is far below its 32 * 2^-24."""
+    note(f"norm tiny H{H} eps {eps}")
+    x = torch.randn((5, H), generator=gen(H), device=device()).abs() + 0.5
+    for k, e in enumerate((-132, -100, -70, -62, -55)):
+        x[k] *= 2.0 ** e
+    x = x.bfloat16()
+    for rows in (x, x.repeat(60, 1)):
+        want = reference(rows, None, None, eps)
+        check_y(rms_norm(rows, None, eps), want, torch.bfloat16)
+        q, scales = rms_norm_fp8(rows, None, eps)
+        live = want.abs().amax(-1) > 2.0 ** -90      # scales in fp32's range
+        check_q(q[live], scales[live], want[live], torch.float8_e4m3fn)
