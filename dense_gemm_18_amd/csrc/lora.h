@@ -296,6 +296,11 @@ void launch_lora_dense(const W4Args &w, const LoraPlus &plus, hipStream_t stream
                                  plus);
 }
 
+// Tiles of 16-bit weights, rank 16, 32 adapters, in us: one row of 16384 x 4096 in tiles of
+// 16 x 32 24.4, of 16 x 16 26.0, 5120 x 2048 8.3 and 9.2, but 12288 x 8192 45.5 and 35.7, 8192 x
+// 6144 21.7 and 20.6, 4096 x 4096 11.7 and 9.9; 64 rows of 2048 x 4096 in tiles of 32 x 16 17.5,
+// of 32 x 32 19.5, 128 rows 23.2 and 19.9.  A weight of 268 MB, 16384 x 8192, goes by at 5.8
+// TB/s.
 template <bool BF>
 void lora_fused(const LoraArgs &p, const W4Args &w, int group, hipStream_t stream)
 {
@@ -307,7 +312,7 @@ void lora_fused(const LoraArgs &p, const W4Args &w, int group, hipStream_t strea
         return;
     }
     if (p.M <= 16 || most < 32) {
-        if (p.N <= 16 * kCUs)
+        if (p.N <= 16 * kCUs || p.K > 4096)
             launch_lora_dense<BF, 1, 1, 8, 1>(w, plus, stream);
         else
             launch_lora_dense<BF, 1, 1, 4, 2>(w, plus, stream);
@@ -326,8 +331,9 @@ void lora_fused(const LoraArgs &p, const W4Args &w, int group, hipStream_t strea
 // rows of B, which come straight to registers, meet every 16 rows that hold one of its own,
 // and only its own are stored, so what is infinite in one adapter stays out of the others'
 // rows.  The rows of B of several pairs travel at once, the first ones' while u is summed.
-// Results go through the wave's own LDS 16 rows at a time, whole 128-byte lines of a row leave together.  Where
-// there are few tiles, p.split workgroups share one's adapters.  KS: pieces of 32 of the
+// Results go through the wave's own LDS 16 rows at a time, whole
+// 128-byte lines of a row leave together.  Where there are few tiles, p.split workgroups share
+// one's adapters.  KS: pieces of 32 of the
 // rank.
 constexpr int kExpandLine = 64 * 2 + 16;         // bytes of a staged row
 
@@ -551,8 +557,10 @@ void launch_expand(const LoraArgs &p, hipStream_t stream)
 
 // As many columns to a workgroup, 64 to 1024, as leave each compute unit one; and where even
 // 64 are not few enough, several that share a tile's adapters, down to eight for each.
-// Measured, rank 16, in us: 64 x 16384, 32 adapters, 64 columns 13.3, 128 18, two sharing 14.7;
-// 64 x 8192 12.8 and 10.5; 2048 x 8192, 512 columns 10.6, 256 14.3.
+// Measured, in us: 64 x 16384, 32 adapters of rank 16, 64 columns 13.3, 128 18, two sharing
+// 14.7; 64 x 8192 12.8 and, two sharing, 10.5; 2048 x 8192, rank 16, 512 columns 10.6, 256 14.3;
+// rank 64 in 8 parts of u 512 columns 27.8, 1024 23.1 (34 MB at 1.5 TB/s: u's parts and the
+// adapters' rows come first, then all is written at once).
 template <bool BF>
 void lora_expand(LoraArgs p, hipStream_t stream)
 {

@@ -21,13 +21,34 @@ uint64_t span_bytes(int64_t rows, int64_t cols, int64_t ld)
 int64_t up256(int64_t n) { return cdiv(n, 256) * 256; }
 
 // Whether a call with dense rows goes through the large tiles of the dense products: u, then
-// the adapters' part into D, then the product added to it.  16-bit weights: where the tiles
-// for few rows are not the better ones; packed weights: where they are unpacked anyway.
-bool large(int64_t M, int64_t N, int group)
+// the adapters' part into D, then the product added to it.  Packed weights: where they are
+// unpacked anyway.  16-bit weights: where the tiles for few rows are not the better ones,
+// which take one pass and one launch, but read the activations once for every 16 or 32
+// columns.  Measured with 32 adapters of rank 16, tiles for few rows / large, in us:
+//   columns                     2048          4096          8192         16384
+//   K 4096   1 row         8.0 / 16.5    9.9 / 17.3   15.0 / 19.0   24.5 / 31.4
+//            8             9.2 / 16.7   11.1 / 17.5   16.1 / 19.2   26.6 / 32.0
+//           16            11.1 / 16.9   13.6 / 17.6   20.0 / 19.6   36.5 / 33.2
+//           32            17.4 / 18.2   20.4 / 19.3   27.1 / 21.7   45.5 / 36.1
+//           64            17.5 / 20.3   23.0 / 22.5   42.5 / 25.9   82.1 / 39.4
+//          128            19.9 / 25.9   30.8 / 29.3   81.6 / 35.7  145.8 / 63.9
+//   K 2048  32 rows                                   17.0 / 16.3   24.8 / 24.1
+//   K 1024  32 rows                                    9.8 / 13.2   15.0 / 17.2
+//   K 8192   1 row        11.8 / 25.3   15.3 / 25.9   24.8 / 30.3   46.0 / 53.9
+//            8            15.2 / 25.5   20.4 / 26.2   33.2 / 30.7   58.7 / 55.4
+//           16            19.5 / 25.7   27.2 / 26.5   39.7 / 31.2   65.6 / 57.3
+//           32            30.2 / 27.8   36.1 / 28.5   48.9 / 33.3   76.5 / 61.2
+//           64            30.8 / 33.2   38.6 / 34.2   72.1 / 40.6  135.8 / 64.2
+// Up to 16 rows it is whether LDS holds the activations whole that tells them apart.
+bool large(int64_t M, int64_t N, int64_t K, int group)
 {
     if (group)
         return M > GEMM_W4_DIRECT_M;
-    return M > 16 && cdiv(M, 32) * cdiv(N, 16) > kCUs;
+    if (M <= 16)
+        return N > 16 * kCUs && M * (cdiv(K, 128) * 256 + 16) > kActBytes;
+    if (M <= 32 && K <= 2048)
+        return false;
+    return N > 8 * kCUs || cdiv(M, 32) * cdiv(N, 32) > kCUs;
 }
 
 // D = +0 (K == 0).
@@ -47,7 +68,7 @@ int64_t gemm_nt_lora_ws_size(int64_t M, int64_t N, int64_t K, int64_t rank, int 
     if (!sizes_ok_lora(M, N, K, rank, group) || M == 0 || N == 0 || K == 0)
         return 0;
     int64_t bytes = up256(lora_parts(M, K, rank) * M * rank * 4);
-    if (group && large(M, N, group))
+    if (group && large(M, N, K, group))
         bytes += up256(N * K * 2);
     return bytes;
 }
@@ -115,7 +136,7 @@ int gemm_nt_lora(const void *X, const void *W, const void *S, const void *Z,
     const std::lock_guard<std::mutex> whole(launch_lock(workspace));
     if (p.count)
         go.shrink(p, stream);
-    if (ldx == K && ldd == N && large(M, N, group)) {
+    if (ldx == K && ldd == N && large(M, N, K, group)) {
         const void *weight = W;
         if (group) {
             void *unpacked = (char *)workspace + up256(lora_parts(M, K, a->rank) * M * a->rank * 4);

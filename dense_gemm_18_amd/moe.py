@@ -193,7 +193,8 @@ class MoeLayer:
         gate = () if self._gate is None else (self._gate,)
         launch("moe_nt_layer_gated" if gate else "moe_nt_layer", self.device,
                (self._ref, *gate, X.data_ptr(), out.data_ptr(), ids.data_ptr(),
-                weights.data_ptr(), X.shape[0], ldx, ldd, self.topk, self._flags, ws.data_ptr(), ws_bytes, handle))
+                weights.data_ptr(), X.shape[0], ldx, ldd, self.topk, self._flags, ws.data_ptr(),
+                ws_bytes, handle))
         return out, ids, weights
 
     def route(self, X, stream=None):
@@ -204,7 +205,7 @@ class MoeLayer:
         gate = () if self._gate is None else (self._gate,)
         launch("moe_nt_route_gated" if gate else "moe_nt_route", self.device,
                (self._ref, *gate, X.data_ptr(), ids.data_ptr(), weights.data_ptr(), X.shape[0],
-                ldx,                self.topk, self._flags, ws.data_ptr(), ws_bytes, handle))
+                ldx, self.topk, self._flags, ws.data_ptr(), ws_bytes, handle))
         return ids, weights
 
     def experts(self, X, ids, weights, out=None, stream=None):

@@ -16,8 +16,7 @@ import math
 import pytest
 import torch
 
-from dense_gemm_18_amd import (LoraAdapters, MoeLayer, W4Weight, binding, gemm_nt, gemm_nt_lora,
-                               gemm_nt_w4, quantize_w4, rms_norm)
+from dense_gemm_18_amd import LoraAdapters, W4Weight, binding, gemm_nt_lora, rms_norm
 from tests import w4_ref
 from tests.gpu_util import device, note
 from tests.test_gpu_w4 import bits, check_guard, gen, strided
@@ -26,9 +25,13 @@ from tests.w4_ref import TYPES, half_step, rel
 pytestmark = pytest.mark.gpu
 
 
-def large(M, N, group):
+def large(M, N, K, group):
     """Whether a dense call goes through the large tiles."""
-    return M > 384 if group else M > 16 and -(-M // 32) * -(-N // 16) > 256
+    if group:
+        return M > 384
+    if M <= 16:
+        return N > 4096 and M * (-(-K // 128) * 256 + 16) > 66 * 1024
+    return (M > 32 or K > 2048) and (N > 2048 or -(-M // 32) * -(-N // 32) > 256)
 
 
 class Case:
@@ -71,7 +74,7 @@ class Case:
         u, tiny = half_step(self.dtype), torch.finfo(self.dtype).smallest_normal
         bound = u * ref.abs() + 2.0 ** -15 * C + tiny
         most = u
-        if dense and large(*ref.shape, self.group):
+        if dense and large(*ref.shape, self.X.shape[1], self.group):
             bound += 2 * u * E + u * part.abs() + (u * C if self.group else 0)
             most = (2 if self.group else 1.5) * u
         assert D.dtype == self.dtype and D.shape == ref.shape
@@ -86,7 +89,9 @@ class Case:
 #          M    N     K   rank count group zeros
 CASES = [(1, 1, 1, 1, 1, 0, False), (1, 64, 128, 8, 1, 0, False), (1, 4100, 1000, 16, 3, 0, False),
          (2, 300, 2050, 12, 5, 0, False), (7, 130, 4099, 33, 2, 0, False),
-         (16, 5000, 640, 64, 20, 0, False), (16, 100, 300, 256, 4, 0, False),
+         (16, 5000, 640, 64, 20, 0, False), (16, 4100, 2100, 16, 20, 0, False),
+         (3, 9000, 11300, 16, 2, 0, False), (250, 1000, 1100, 30, 6, 0, False),
+         (20, 9000, 1030, 16, 20, 0, False), (32, 4100, 2056, 24, 9, 0, False), (16, 100, 300, 256, 4, 0, False),
          (17, 64, 130, 100, 3, 0, False), (31, 2000, 1024, 16, 40, 0, False),
          (33, 777, 515, 5, 7, 0, False), (64, 1000, 2048, 16, 32, 0, False),
          (64, 5000, 512, 16, 70, 0, False), (65, 4096, 264, 64, 9, 0, False),
