@@ -8,6 +8,8 @@
 // Rows of a tile of the first product, and of one where there are many.
 constexpr int kLoraRows = 32;
 constexpr int kLoraMany = 64;
+// Pieces of u at most.
+constexpr int kLoraParts = 8;
 // Values of u that a tile of the projection holds in LDS: its rows times the rank.
 constexpr int kLoraHeld = 4096;
 
@@ -36,8 +38,9 @@ inline int64_t lora_tiles(int64_t M, int64_t rank)
 // for.  Of 512 elements or more; the fewer the tiles, the more of them.
 inline int lora_parts(int64_t M, int64_t K, int64_t rank)
 {
-    const int64_t tiles = lora_tiles(M, rank), most = lora_many(M, rank) || tiles < 8 ? 8 : 4;
-    int64_t p = tiles < 8 ? 8 : kCUs / tiles;
+    const int64_t tiles = lora_tiles(M, rank);
+    const int64_t most = lora_many(M, rank) || tiles < 8 ? kLoraParts : 4;
+    int64_t p = tiles < 8 ? kLoraParts : kCUs / tiles;
     p = p > most ? most : p < 1 ? 1 : p;
     return (int)(p < cdiv(K, 512) ? p : cdiv(K, 512));
 }
@@ -112,10 +115,10 @@ __device__ __forceinline__ void lora_item(const LoraArgs &p, char *lds, const in
     c.stride = p.K;
     c.K = min((part + 1) * steps / p.parts * 128, p.K) - k0;
     c.M = rows;
+    const float s = p.s ? p.s[a] : 1.0f;       // on its way before the rest
     c.begin(lds, p.X + m0 * p.ldx + k0,
             (uint32_t)((min((int64_t)tile, p.M - m0) - 1) * p.ldx + c.K) * 2u);
     c.run([&](int m) { return (uint32_t)(list[m] * p.ldx) * 2u; });
-    const float s = p.s ? p.s[a] : 1.0f;
     float *u = p.u + ((int64_t)part * p.M + m0) * p.rank;
     c.join([&](int m, int n, const float(&v)[RB]) {
         const int j = rb * kEach + (n >> 4) * (16 * RB) + (n & 15);
@@ -229,7 +232,10 @@ void lora_shrink(const LoraArgs &p, hipStream_t stream)
 // ---- beside the projection's tiles ---------------------------------------
 
 // The addend of a tile: u of its rows and their adapters wait in LDS, an output reads its
-// row of B.
+// row of B.  A thread's first value of u is on its way before the weights are: its pieces by
+// unconditional loads, together, with nothing that waits for the row's adapter: one row of 4096 x
+// 4096 with 8 pieces 10.1 us, 10.4 with rank 64, the product alone 9.4; with a loop over the
+// pieces after the product 10.5 and 11.8.
 struct LoraPlus {
     static constexpr bool kNone = false;
     const float *u;
@@ -238,25 +244,54 @@ struct LoraPlus {
     int M, N, rank, count, parts;
     int lds_at;
 
+    struct Value {
+        int id;
+        float x[kLoraParts];
+    };
+
     __host__ __device__ int stride() const { return (rank + 7) & ~7; }
     int bytes(int rows) const { return rows * (stride() + 4) * 4; }
 
-    // Row m's adapter is the word before its u.
-    __device__ __forceinline__ void stage(char *lds, int m0, int rows) const
+    // What value i of the tile is made of.
+    __device__ __forceinline__ Value load(int i, int m0, int rows) const
     {
-        const int ld = stride() + 4;
+        const int ld = stride() + 4, m = i / ld, j = i - m * ld - 4;
+        const auto at = range(u + (int64_t)m0 * rank,
+                              (uint32_t)(((int64_t)(parts - 1) * M + rows) * rank * 4));
+        const uint32_t off = m < rows && (uint32_t)j < (uint32_t)rank
+                                 ? (uint32_t)(m * rank + j) * 4u : kOob;
+        Value v;
+        v.id = __builtin_amdgcn_raw_buffer_load_b32(range(ids + m0, (uint32_t)rows * 4u),
+                                                    (uint32_t)m * 4u, 0, 0);
+#pragma unroll
+        for (int q = 0; q < kLoraParts; ++q)
+            v.x[q] = __builtin_bit_cast(
+                float, __builtin_amdgcn_raw_buffer_load_b32(
+                           at, q < parts ? off + (uint32_t)q * (uint32_t)M * (uint32_t)rank * 4u : kOob,
+                           0, 0));
+        return v;
+    }
+
+    __device__ __forceinline__ Value first(int m0, int rows) const
+    {
+        return load(threadIdx.x, m0, rows);
+    }
+
+    // Row m's adapter is the word before its u.
+    __device__ __forceinline__ void stage(char *lds, int m0, int rows, Value v) const
+    {
+        const int ld = stride() + 4, all = rows * ld;
         float *to = (float *)(lds + lds_at);
-        for (int i = threadIdx.x; i < rows * ld; i += blockDim.x) {
-            const int m = i / ld, j = i - m * ld - 4;
-            const int id = ids[m0 + m];
-            const bool in = (uint32_t)id < (uint32_t)count;
-            float v = 0.0f;
-            if (j < 0)
-                v = __builtin_bit_cast(float, in ? id : -1);
-            else if (in && j < rank)
-                for (int q = 0; q < parts; ++q)
-                    v += u[((int64_t)q * M + m0 + m) * rank + j];
-            to[i] = v;
+        for (int i = threadIdx.x; i < all;) {
+            const bool in = (uint32_t)v.id < (uint32_t)count;
+            float sum = v.x[0];
+#pragma unroll
+            for (int q = 1; q < kLoraParts; ++q)
+                sum += v.x[q];
+            to[i] = i % ld < 4 ? __builtin_bit_cast(float, in ? v.id : -1) : in ? sum : 0.0f;
+            i += blockDim.x;
+            if (i < all)
+                v = load(i, m0, rows);
         }
     }
 
@@ -349,13 +384,17 @@ __global__ void __launch_bounds__(512, 2) lora_expand_kernel(LoraArgs p)
     __shared__ int adapter[64];
     __shared__ uint64_t has[64], with[64];
     const int blocks = (p.N + p.columns - 1) / p.columns;
-    uint32_t wg = blockIdx.x + blockIdx.y * gridDim.x;
+    // Workgroups are dealt to the eight XCDs by turns: each gets tiles that follow one
+    // another, so that what it reads of u and B passes its L2 once.
+    const uint32_t all = ((uint32_t)p.M + 63u) / 64u * p.split * blocks;
+    const uint32_t dealt = blockIdx.x + blockIdx.y * gridDim.x;
+    if (dealt >= all)
+        return;
+    uint32_t wg = dealt % 8 * (all / 8) + min(dealt % 8, all % 8) + dealt / 8;
     const int n0 = (int)(wg % blocks) * p.columns;
     wg /= blocks;
     const int share = (int)(wg % p.split);
     const int64_t m0 = (int64_t)(wg / p.split) * 64;
-    if (m0 >= p.M)
-        return;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int id = adapter_of(p, m0 + lane);
     uint16_t *held = (uint16_t *)lds;
@@ -438,16 +477,34 @@ __global__ void __launch_bounds__(512, 2) lora_expand_kernel(LoraArgs p)
         // eight lanes to a row
         const int m = threadIdx.x >> 3, j0 = threadIdx.x & 7;
         const bool in = __shfl(id, m) >= 0;
-        const float *u = p.u + (m0 + m) * p.rank;
+        // pieces of u as many at a time as registers take, unconditionally
+        constexpr int kAtOnce = KS <= 2 ? 4 : KS == 4 ? 2 : 1;
+        const auto at = range(p.u + m0 * p.rank,
+                              (uint32_t)(((int64_t)(p.parts - 1) * p.M +
+                                          min((int64_t)64, p.M - m0)) * p.rank * 4));
         float v[KS * 4], most = 0.0f;
 #pragma unroll
         for (int i = 0; i < KS * 4; ++i)
-            v[i] = in && j0 + 8 * i < p.rank ? u[j0 + 8 * i] : 0.0f;
-        for (int q = 1; q < p.parts; ++q) {
-            u += (int64_t)p.M * p.rank;
+            v[i] = 0.0f;
+        for (int q = 0; q < p.parts; q += kAtOnce) {
+            float x[kAtOnce][KS * 4];
 #pragma unroll
-            for (int i = 0; i < KS * 4; ++i)
-                v[i] += in && j0 + 8 * i < p.rank ? u[j0 + 8 * i] : 0.0f;
+            for (int k = 0; k < kAtOnce; ++k) {
+                const bool piece = in && q + k < p.parts;
+                const uint32_t row =
+                    ((uint32_t)(q + k) * (uint32_t)p.M + (uint32_t)m) * (uint32_t)p.rank;
+#pragma unroll
+                for (int i = 0; i < KS * 4; ++i)
+                    x[k][i] = __builtin_bit_cast(
+                        float, __builtin_amdgcn_raw_buffer_load_b32(
+                                   at, piece && j0 + 8 * i < p.rank ? (row + j0 + 8 * i) * 4u
+                                                                    : kOob, 0, 0));
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+                for (int i = 0; i < KS * 4; ++i)
+                    v[i] += x[k][i];
         }
 #pragma unroll
         for (int i = 0; i < KS * 4; ++i)
@@ -559,8 +616,9 @@ void launch_expand(const LoraArgs &p, hipStream_t stream)
 // 64 are not few enough, several that share a tile's adapters, down to eight for each.
 // Measured, in us: 64 x 16384, 32 adapters of rank 16, 64 columns 13.3, 128 18, two sharing
 // 14.7; 64 x 8192 12.8 and, two sharing, 10.5; 2048 x 8192, rank 16, 512 columns 10.6, 256 14.3;
-// rank 64 in 8 parts of u 512 columns 27.8, 1024 23.1 (34 MB at 1.5 TB/s: u's parts and the
-// adapters' rows come first, then all is written at once).
+// rank 64 in 8 parts of u 512 columns 27.8, 1024 23.1.  (Since then u's parts travel together
+// and an XCD's tiles follow one another: 64 x 16384 12.5 to 11.2, 2048 x 8192, rank 64, 28.1 to
+// 26.1 in a trace: 34 MB written at 1.3 TB/s, after u's parts and the adapters' rows.)
 template <bool BF>
 void lora_expand(LoraArgs p, hipStream_t stream)
 {

@@ -25,11 +25,13 @@ __attribute__((visibility("hidden"))) void gemm18_w4_bf16(const W4Args &a, int g
 namespace {
 
 // What a kernel adds to a tile's sums before they are rounded: nothing.  Others have
-// `lds_at`, where their part of the LDS begins, bytes(rows) of it, stage(), which every
-// thread calls, and at(), the addend of the tile's row m in column n.
+// `lds_at`, where their part of the LDS begins, bytes(rows) of it, first(), what a thread
+// loads before the product, stage(), which every thread calls with that after it, and at(),
+// the addend of the tile's row m in column n.
 struct NoPlus {
     static constexpr bool kNone = true;
     int bytes(int) const { return 0; }
+    __device__ __forceinline__ NoPlus first(int, int) const { return {}; }
 };
 
 // One workgroup's tile of D, 16 * MB rows and as many columns as Core has
@@ -54,11 +56,12 @@ __global__ void __launch_bounds__(Core::kThreads, 2) gemm_w4_kernel(W4Args p, Pl
     c.rows[0] = p.N - n0;
     c.K = p.K;
     c.M = min(16 * MB, p.M - m0);
+    const auto held = plus.first(m0, c.M);
     c.begin((char *)lds, p.A + (int64_t)m0 * p.lda,
             (uint32_t)((c.M - 1) * p.lda + p.K) * 2u);
     c.run([&](int m) { return (uint32_t)(m * p.lda) * 2u; });
     if constexpr (!Plus::kNone)
-        plus.stage((char *)lds, m0, c.M);
+        plus.stage((char *)lds, m0, c.M, held);
     uint16_t *D = p.D + (int64_t)m0 * p.ldd + n0;
     c.join([&](int m, int n, const auto &v) {
         constexpr int RB = sizeof(v) / sizeof(v[0]);
