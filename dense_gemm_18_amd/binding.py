@@ -436,6 +436,7 @@ def rms_norm_fp8(X: int, R: int, W: int, Q: int, scales: int, S: int, T: int, H:
 # ---- tensor-level convenience ----------------------------------------------
 
 _FP8 = {}
+_HERE = nullcontext()
 
 
 def _scale_of(x, n, what, device):
@@ -491,8 +492,8 @@ def gemm_nt(A, B, out=None, stream=None, scale: float = 1.0, b_scale=None, a_sca
     N = B.shape[0]
     if out is None:
         # the tensor is the call's stream's
-        with nullcontext() if stream is None else torch.cuda.stream(stream):
-            out = torch.empty((M, N), dtype=out_dtype, device=device)
+        with _HERE if stream is None else torch.cuda.stream(stream):
+            out = torch.empty(M, N, dtype=out_dtype, device=device)
     elif (out.dtype != out_dtype or tuple(out.shape) != (M, N) or not out.is_contiguous()
           or out.device != device):
         raise ValueError(f"out must be a contiguous {out_dtype} [M, N] tensor on A's device")
@@ -502,7 +503,7 @@ def gemm_nt(A, B, out=None, stream=None, scale: float = 1.0, b_scale=None, a_sca
     pa, pb, pd = A.data_ptr(), B.data_ptr(), out.data_ptr()
     b_ptr = None if b_scale is None else _scale_of(b_scale, N, "b_scale", device)
     # the library launches on the current device: make it the operands' one
-    with (nullcontext() if device.index == torch.cuda.current_device()
+    with (_HERE if device.index == torch._C._cuda_getDevice()
           else torch.cuda.device(device)):
         if fp8 and (a_scale is not None or dtype is not None):
             name = "gemm_nt_fp8_rs"

@@ -7,6 +7,7 @@ the tensors' device); tensors that it makes are that stream's.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import binding
 from .w4 import (W4Weight, check_out, dtype_code, launch, new_rows, on_stream, row_stride,
@@ -50,6 +51,11 @@ class LoraAdapters:
         self._ref = ctypes.byref(self._held)
 
 
+@functools.lru_cache(maxsize=4096)
+def _ws_size(M, N, K, rank, group):
+    return binding.lib().gemm_nt_lora_ws_size(M, N, K, rank, group)
+
+
 def gemm_nt_lora(X, w, adapters: LoraAdapters, ids, out=None, stream=None, workspace=None):
     """D = X @ w.T and, in each row, the part of its own adapter: row m has the adapter
     ids[m] (int32, [M]), or none where that is outside [0, count), -1 say.
@@ -84,7 +90,7 @@ def gemm_nt_lora(X, w, adapters: LoraAdapters, ids, out=None, stream=None, works
         check_out(out, (M, N), dtype, device)
         ldd = row_stride(out, "out")
     if workspace is None:
-        need = binding.lib().gemm_nt_lora_ws_size(M, N, K, adapters.rank, group)
+        need = _ws_size(M, N, K, adapters.rank, group)
         with on_stream(stream):
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:

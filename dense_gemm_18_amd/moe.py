@@ -69,8 +69,8 @@ def choose_experts(logits, topk: int, scoring: str = "softmax", bias=None, group
     g = _gate(E, device, topk, scoring, bias, groups, topk_groups, group_top, scale)
     ldl = E if logits.is_contiguous() else row_stride(logits, "logits")
     with on_stream(stream):
-        ids = torch.empty((T, topk), dtype=torch.int32, device=device)
-        weights = torch.empty((T, topk), dtype=torch.float32, device=device)
+        ids = torch.empty(T, topk, dtype=torch.int32, device=device)
+        weights = torch.empty(T, topk, dtype=torch.float32, device=device)
     launch("moe_nt_choose", device,
            (ctypes.byref(g), logits.data_ptr(), ids.data_ptr(), weights.data_ptr(), T, E, ldl,
             topk, binding.MOE_RENORMALIZE if renormalize else 0, code,

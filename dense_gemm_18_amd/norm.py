@@ -99,11 +99,11 @@ def rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, dtype=None, s
                                                               stream)
     with on_stream(stream):
         if out is None:
-            out, ldq = torch.empty((T, H), dtype=dtype, device=device), H
+            out, ldq = torch.empty(T, H, dtype=dtype, device=device), H
         else:
             check_out(out, (T, H), dtype, device)
             ldq = row_stride(out, "out")
-        scales = torch.empty((T,), dtype=torch.float32, device=device) if scale is None else None
+        scales = torch.empty(T, dtype=torch.float32, device=device) if scale is None else None
     launch("rms_norm_fp8", device,
            (x.data_ptr(), r, w, out.data_ptr(), None if scales is None else scales.data_ptr(), s,
             T, H, ldx, ldr, ldq, lds, eps, 0.0 if scale is None else scale, fmt, code,

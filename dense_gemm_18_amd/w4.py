@@ -57,7 +57,7 @@ def launch(name: str, device, args) -> None:
     import torch
     fn = getattr(binding.lib(), name)
     # the library launches on the current device: make it the operands' one
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():       # initialised: there are tensors
         rc = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -68,10 +68,11 @@ def launch(name: str, device, args) -> None:
 
 def new_rows(x, rows: int, cols: int, stream):
     """An uninitialised [rows, cols] tensor like ``x``, ``stream``'s."""
+    # sizes as arguments, not as a tuple: 1.2 us instead of 1.4
     if stream is None:
-        return x.new_empty((rows, cols))
+        return x.new_empty(rows, cols)
     with on_stream(stream):
-        return x.new_empty((rows, cols))
+        return x.new_empty(rows, cols)
 
 
 def row_stride(x, what: str) -> int:

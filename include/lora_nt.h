@@ -42,11 +42,15 @@ typedef struct lora_nt_adapters {
  * group == 0: W is N x K of the type `dtype` and S and Z are NULL.  group 32, 64 or 128:
  * W, S and Z are a packed weight's Q, S and Z.
  *
- * Sums are held in fp32, u too, and D is rounded once, up to 64 rows (16-bit weights)
- * or GEMM_W4_DIRECT_M rows (packed ones).  With more rows u and the adapters' part of D
- * are rounded to the 16-bit type (u times a power of two, so that it is in range)
- * before the weight's sum is added in fp32 and D is rounded, and a packed weight is
- * unpacked to 16 bits first; rows that are not dense (ldx > K or ldd > N) are not.
+ * Sums are held in fp32, u too, and D is rounded once, where the tiles for few rows
+ * serve the call.  Where the large ones do, u and the adapters' part of D are rounded to
+ * the 16-bit type (u times a power of two, so that it is in range) before the weight's
+ * sum is added in fp32 and D is rounded, and a packed weight is unpacked to 16 bits
+ * first.  They serve dense rows (ldx == K and ldd == N) of packed weights past
+ * GEMM_W4_DIRECT_M rows, and of 16-bit ones
+ *   up to 16 rows   with N > 4096 and M * (K rounded up to 128, + 8) * 2 > 66 KB,
+ *   from 17 on      with N > 2048 or ceil(M / 32) * ceil(N / 32) > 256, but not up to 32
+ *                   rows with K <= 2048.
  * An infinite or NaN value of one adapter, or of a row, changes no other's rows.
  *
  * workspace: device memory of gemm_nt_lora_ws_size bytes or more, 256-byte aligned, any
