@@ -529,9 +529,9 @@ __device__ __forceinline__ void sort_keys(uint32_t (&c)[PER])
 // the fixed point's range; NaN and infinite ones), the whole wave does the token again with
 // gate_token: one in ten thousand or so.  16-bit logits without WIDE have their order in the
 // upper 16 bits (fp16: 19) of their numbers in fp32: exact.
-// 16384 tokens of 256 experts in 8 groups, 8 chosen, a bias: 14 us (its bytes take 3), 277 VALU
-// instructions to a token, which with the latency of four waves to a SIMD bound it; 26.8 us
-// and 675 instructions with a token to a wave, 28.7 in 64 bits throughout.
+// 16384 tokens of 256 experts in 8 groups, 8 chosen, a bias: 13 to 18 us (its bytes take 3),
+// 277 VALU instructions to a token, 65 % of the issue slots; 26.8 us and 675 instructions with
+// a token to a wave, 28.7 in 64 bits throughout.
 // span: lanes of a group, a power of two; 0: one group.
 template <int PER, bool WIDE, int TYPE>
 __global__ void __launch_bounds__(kGateWaves * 64) moe_gate_many_kernel(GateArgs p, int span)
