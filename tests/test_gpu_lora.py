@@ -12,6 +12,7 @@ with a packed weight and 1.5 u without.
 from __future__ import annotations
 
 import math
+import threading
 
 import pytest
 import torch
@@ -167,11 +168,13 @@ def test_rows_without_an_adapter(M, group, dtype):
     c.check(D)
 
 
-@pytest.mark.parametrize("M,N", [(20, 300), (40, 5000), (500, 300)])
+@pytest.mark.parametrize("M,N,K,rank", [(20, 300, 300, 16), (40, 5000, 300, 16),
+                                        (500, 300, 300, 16), (600, 2300, 300, 64),
+                                        (16, 4200, 2200, 16)])
 @pytest.mark.parametrize("group", [0, 128])
-def test_infinities_and_nans_stay_where_they_are(M, N, group):
+def test_infinities_and_nans_stay_where_they_are(M, N, K, rank, group):
     note(f"lora NaN M{M} N{N} group {group}")
-    c = Case(6, M, N, 300, 16, 4, torch.bfloat16, group)
+    c = Case(6, M, N, K, rank, 4, torch.bfloat16, group)
     c.ids[:8] = torch.tensor([0, 1, 2, 3, -1, 0, 1, 2], device=device())
     want = c.run()
     c.A[1, 3, 7] = math.nan
@@ -255,6 +258,31 @@ def test_replayed_and_on_another_stream(M, group):
             assert torch.equal(bits(got), bits(eager))
         c.X.mul_(-0.5)
         c.ids.copy_(c.ids.roll(1))
+
+
+@pytest.mark.parametrize("M,group", [(64, 0), (400, 64), (5, 32)])
+def test_threads_that_share_a_stream_and_a_workspace(M, group):
+    """Each call's launches are enqueued side by side, so another's u never comes between."""
+    note(f"lora threads M{M} group {group}")
+    cases = [Case(20 + k, M, 2500, 520, 16, 5, torch.bfloat16, group) for k in range(2)]
+    want = [c.run() for c in cases]
+    ws = torch.empty(binding.gemm_nt_lora_ws_size(M, 2500, 520, 16, group), dtype=torch.uint8,
+                     device=device())
+    got = [[torch.empty_like(want[k]) for _ in range(30)] for k in range(2)]
+    stream = torch.cuda.current_stream()
+
+    def calls(k):
+        with torch.cuda.stream(stream):
+            for out in got[k]:
+                cases[k].run(out=out, workspace=ws)
+    threads = [threading.Thread(target=calls, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(bits(out), bits(want[k])) for out in got[k])
 
 
 @pytest.mark.parametrize("T", [1, 6, 70])
