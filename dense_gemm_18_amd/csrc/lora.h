@@ -62,20 +62,6 @@ namespace {
 // 16 bytes at any 2-byte alignment (one global load).
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
-// The first `count` of the 8 elements at p, zero for the others; nothing past them is
-// accessed.
-__device__ __forceinline__ u32x4 eight_of(const uint16_t *p, int count)
-{
-    if (count >= 8)
-        return *(const u32x4_any *)p;
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < count)
-            v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-    return v;
-}
-
 __device__ __forceinline__ int adapter_of(const LoraArgs &p, int64_t m)
 {
     const int id = m < p.M ? p.ids[m] : -1;
@@ -235,7 +221,8 @@ void lora_shrink(const LoraArgs &p, hipStream_t stream)
 // row of B.  A thread's first value of u is on its way before the weights are: its pieces by
 // unconditional loads, together, with nothing that waits for the row's adapter: one row of 4096 x
 // 4096 with 8 pieces 10.1 us, 10.4 with rank 64, the product alone 9.4; with a loop over the
-// pieces after the product 10.5 and 11.8.
+// pieces after the product 10.5 and 11.8.  Rank 12 takes what 16 does; 0.35 us more with its last
+// four loaded one by one.
 struct LoraPlus {
     static constexpr bool kNone = false;
     const float *u;
@@ -304,21 +291,41 @@ struct LoraPlus {
             return 0.0f;
         const uint16_t *b = B + ((int64_t)a * N + n) * rank;
         float sum = 0.0f;
-        auto piece = [&](u32x4 v, int j) G18_INLINE {
-            const f32x4 x = *(const f32x4 *)(from + 4 + j), y = *(const f32x4 *)(from + 8 + j);
+        // the last `count` of eight of B and of u, from j on
+        auto piece = [&](u32x4 v, int j, int count) G18_INLINE {
+            const float *x = from + 4 + j;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                sum = __builtin_fmaf(e < 4 ? x[e & 3] : y[e & 3],
-                                     to_float<BF>((uint16_t)(v[e >> 1] >> (16 * (e & 1)))), sum);
+                sum = __builtin_fmaf(
+                    e >= 8 - count ? x[e] : 0.0f,
+                    e >= 8 - count ? to_float<BF>((uint16_t)(v[e >> 1] >> (16 * (e & 1)))) : 0.0f,
+                    sum);
         };
+        auto eight = [&](int j) G18_INLINE { return *(const u32x4_any *)(b + j); };
         int j = 0;
         for (; j + 16 <= rank; j += 16) {        // two loads on their way together
-            const u32x4 v = *(const u32x4_any *)(b + j), w = *(const u32x4_any *)(b + j + 8);
-            piece(v, j);
-            piece(w, j + 8);
+            const u32x4 v = eight(j), w = eight(j + 8);
+            piece(v, j, 8);
+            piece(w, j + 8, 8);
         }
-        for (; j < rank; j += 8)
-            piece(eight_of(b + j, rank - j), j);
+        // What is left, fewer than 16, ends with the row's last eight: no branch around a load.
+        const int left = rank - j;
+        if (left > 8) {
+            const u32x4 v = eight(j), w = eight(rank - 8);
+            piece(v, j, 8);
+            piece(w, rank - 8, left - 8);
+        } else if (left && rank >= 8) {
+            piece(eight(rank - 8), rank - 8, left);
+        } else if (left) {
+            uint16_t v[8];
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                v[e] = b[e < rank ? e : rank - 1];
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                sum = __builtin_fmaf(e < rank ? from[4 + e] : 0.0f,
+                                     e < rank ? to_float<BF>(v[e]) : 0.0f, sum);
+        }
         return sum;
     }
 };
@@ -372,7 +379,7 @@ void lora_fused(const LoraArgs &p, const W4Args &w, int group, hipStream_t strea
 // rank.
 constexpr int kExpandLine = 64 * 2 + 16;         // bytes of a staged row
 
-// TAIL: the rank is no multiple of 8.
+// TAIL: the rank is no multiple of 8.  (Past 128 that form spills 33 registers of a lane.)
 template <bool BF, int KS, bool TAIL>
 __global__ void __launch_bounds__(512, 2) lora_expand_kernel(LoraArgs p)
 {
