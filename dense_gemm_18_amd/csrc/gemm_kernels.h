@@ -775,9 +775,12 @@ constexpr int kSpinLimit = 1 << 24;
 // bit 0 loads A, bit 1 loads B with the non-temporal cache policy, set when
 // that operand is read exactly once per call (a single column or row of
 // tiles), so that streaming it does not allocate in the caches.  H16: the
-// running sum is fp16 (mma_acc16), one update per K-step and block.
+// running sum is fp16 (mma_acc16), one update per K-step and block.  ADD: D += A * B^T, one
+// rounding: the sums start from D, read while the first steps load, and the epilogue is the
+// plain one.  (2048 x 8192 x 8192 bf16 in a trace 205 us, 189 at least; as EPI's C, which is read
+// after the last step, 209 and 201; a call with low-rank adapters 237 and 249.)
 template <class C, bool KTAIL, bool SK, bool EPI, bool BF, int F8 = 0, int UB = 2, int NT = 0,
-          bool H16 = false>
+          bool H16 = false, bool ADD = false>
 __global__ void __launch_bounds__(C::THREADS, 1)
 gemm_nt_dma_kernel(const typename Elem<BF>::T *__restrict__ A,
                    const typename Elem<BF>::T *__restrict__ B, typename Elem<BF>::T *__restrict__ D,
@@ -1405,6 +1408,34 @@ gemm_nt_dma_kernel(const typename Elem<BF>::T *__restrict__ A,
 #pragma unroll
         for (int j = 0; j < C::TN; ++j)
             acc[i][j] = AccT{};
+    // ADD: what D holds, on its way before the operands; the sums begin with it (below).
+    using H4 = typename Vec4<typename Elem<BF>::T>::type;
+    constexpr int HG = C::MF == 32 ? 4 : 1;         // groups of four in a block's registers
+    [[maybe_unused]] H4 held[ADD ? C::TM : 1][C::TN][HG];
+    if constexpr (ADD) {
+        static_assert(!SK && !EPI && F8 == 0 && !H16, "one tile, 16-bit operands, fp32 sums");
+        auto fetch = [&](auto all) G18_INLINE {
+#pragma unroll
+            for (int i = 0; i < C::TM; ++i) {
+                const int m = m0 + wm * C::WTM + C::MF * i + lane % C::MF;
+                const auto *row = D + (int64_t)m * N;
+#pragma unroll
+                for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+                    for (int g = 0; g < HG; ++g) {
+                        const int at = n0 + wn * C::WTN + C::MF * j + 8 * g + 4 * (lane / C::MF);
+                        if constexpr (decltype(all)::value)
+                            held[i][j][g] = *(const H4 *)(row + at);
+                        else
+                            held[i][j][g] = m < M ? load4h(row, at, N, vec_store) : H4{};
+                    }
+            }
+        };
+        if (vec_store && m0 + C::BM <= M && n0 + C::BN <= N)
+            fetch(std::true_type{});
+        else
+            fetch(std::false_type{});
+    }
 
     // Prologue: steps 0 .. NSTAGE-2 and, with split loads, the first half of
     // step NSTAGE-1 (its second half is issued by step 0's first slice, like
@@ -1483,6 +1514,15 @@ gemm_nt_dma_kernel(const typename Elem<BF>::T *__restrict__ A,
         }
     }
     lds_barrier();
+    }
+    if constexpr (ADD) {
+#pragma unroll
+        for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4 * HG; ++e)
+                    acc[i][j][e] = (float)held[i][j][e / 4][e % 4];
     }
     static_for<0, NR>([&](auto qc) G18_INLINE { read_one(Z_{}, Z_{}, Z_{}, qc); });
 
@@ -1765,7 +1805,7 @@ EpiArg<EPI> epi_arg(const Epi &e)
         return NoEpi{};
 }
 
-template <class C, bool SK, bool EPI, bool BF>
+template <class C, bool SK, bool EPI, bool BF, bool ADD = false>
 void launch_dma(const void *A, const void *B, void *D, int M, int N, int K, int vec, hipStream_t s,
                 const SkPlan &sk, int grid, const Epi &epi)
 {
@@ -1774,7 +1814,7 @@ void launch_dma(const void *A, const void *B, void *D, int M, int N, int K, int 
     const dim3 g = SK ? dim3((unsigned)grid) : tile_grid((int64_t)tm * tn);
     auto go = [&](auto ktail, auto ntc) {
         hipLaunchKernelGGL((gemm_nt_dma_kernel<C, decltype(ktail)::value, SK, EPI, BF, 0, 2,
-                                               decltype(ntc)::value>),
+                                               decltype(ntc)::value, false, ADD>),
                            g, dim3(C::THREADS), 0, s, (const T *)A,
                            (const T *)B, (T *)D, M, N, K, tm, tn, vec, sk, epi_arg<EPI>(epi));
     };
@@ -1838,41 +1878,41 @@ inline int load_bytes(const void *A, const void *B, int64_t M, int64_t N, int64_
 // bias must then also be 8-byte aligned for vector accesses.  CDma: the
 // direct-to-LDS pipeline (K % 8 == 0, A and B 16-byte aligned); CReg: the
 // same pipeline with register-staged 16-byte chunks (everything else).
-template <class CDma, class CReg, bool EPI = false, bool BF = false>
+template <class CDma, class CReg, bool EPI = false, bool BF = false, bool ADD = false>
 void launch_tile(const void *A, const void *B, void *D, int M, int N, int K, hipStream_t s,
                  const Epi &epi = Epi{})
 {
     const int vec = store_mode(D, N, (uintptr_t)epi.C | (uintptr_t)epi.bias);
     const SkPlan none{};
     if (load_bytes(A, B, M, N, K) == 16)
-        launch_dma<CDma, false, EPI, BF>(A, B, D, M, N, K, vec, s, none, 0, epi);
+        launch_dma<CDma, false, EPI, BF, ADD>(A, B, D, M, N, K, vec, s, none, 0, epi);
     else
-        launch_dma<CReg, false, EPI, BF>(A, B, D, M, N, K, vec, s, none, 0, epi);
+        launch_dma<CReg, false, EPI, BF, ADD>(A, B, D, M, N, K, vec, s, none, 0, epi);
 }
 
 // The tile `t` with direct-to-LDS loads when they apply, else register
 // staging (the 64 x 64 kernel serves the 64 x 32 and 32 x 64 tiles then).
-template <bool EPI = false, bool BF = false>
+template <bool EPI = false, bool BF = false, bool ADD = false>
 void launch_plain(Tile t, const void *A, const void *B, void *D, int M, int N, int K,
                   hipStream_t s, const Epi &epi = Epi{})
 {
     switch (t) {
     case Tile::kBig:
         if (K % 512 != 0)
-            launch_tile<BigDma3, BigReg, EPI, BF>(A, B, D, M, N, K, s, epi);
+            launch_tile<BigDma3, BigReg, EPI, BF, ADD>(A, B, D, M, N, K, s, epi);
         else
-            launch_tile<BigDma, BigReg, EPI, BF>(A, B, D, M, N, K, s, epi);
+            launch_tile<BigDma, BigReg, EPI, BF, ADD>(A, B, D, M, N, K, s, epi);
         break;
     case Tile::kMid:
         if (cdiv(M, 128) * cdiv(N, 128) > kCUs)
-            launch_tile<Mid2Dma, MidReg, EPI, BF>(A, B, D, M, N, K, s, epi);
+            launch_tile<Mid2Dma, MidReg, EPI, BF, ADD>(A, B, D, M, N, K, s, epi);
         else
-            launch_tile<MidDma, MidReg, EPI, BF>(A, B, D, M, N, K, s, epi);
+            launch_tile<MidDma, MidReg, EPI, BF, ADD>(A, B, D, M, N, K, s, epi);
         break;
-    case Tile::kRect: launch_tile<RectDma, MidReg, EPI, BF>(A, B, D, M, N, K, s, epi); break;
-    case Tile::kThinN: launch_tile<ThinNDma, ThinReg, EPI, BF>(A, B, D, M, N, K, s, epi); break;
-    case Tile::kThinM: launch_tile<ThinMDma, ThinReg, EPI, BF>(A, B, D, M, N, K, s, epi); break;
-    default: launch_tile<ThinDma, ThinReg, EPI, BF>(A, B, D, M, N, K, s, epi); break;
+    case Tile::kRect: launch_tile<RectDma, MidReg, EPI, BF, ADD>(A, B, D, M, N, K, s, epi); break;
+    case Tile::kThinN: launch_tile<ThinNDma, ThinReg, EPI, BF, ADD>(A, B, D, M, N, K, s, epi); break;
+    case Tile::kThinM: launch_tile<ThinMDma, ThinReg, EPI, BF, ADD>(A, B, D, M, N, K, s, epi); break;
+    default: launch_tile<ThinDma, ThinReg, EPI, BF, ADD>(A, B, D, M, N, K, s, epi); break;
     }
 }
 

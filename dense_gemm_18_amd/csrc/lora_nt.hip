@@ -147,13 +147,7 @@ int gemm_nt_lora(const void *X, const void *W, const void *S, const void *Z,
             weight = unpacked;
         }
         go.expand(p, stream);
-        if (bf) {
-            gemm18_add_bf16(X, weight, D, p.M, p.N, p.K, stream);
-        } else {
-            const int rc = gemm_nt_f16_ex(X, weight, D, nullptr, D, M, N, K, 1.0f, 1.0f, stream);
-            if (rc != GEMM_OK)
-                return rc;
-        }
+        (bf ? gemm18_add_bf16 : gemm18_add_f16)(X, weight, D, p.M, p.N, p.K, stream);
     } else {
         W4Args w{};
         w.A = (const uint16_t *)X;

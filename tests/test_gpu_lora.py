@@ -99,6 +99,8 @@ CASES = [(1, 1, 1, 1, 1, 0, False), (1, 64, 128, 8, 1, 0, False), (1, 4100, 1000
          (70, 3001, 1030, 20, 3, 0, False), (300, 1500, 520, 256, 6, 0, False),
          (500, 700, 2000, 129, 100, 0, False), (1025, 1030, 777, 17, 3, 0, False),
          (1500, 700, 1300, 64, 9, 0, False), (2100, 520, 520, 250, 5, 0, False),
+         (600, 2501, 6, 8, 3, 0, False), (2000, 3001, 1100, 16, 5, 0, False),
+         (2049, 4100, 520, 24, 4, 0, False), (2048, 4096, 512, 16, 4, 0, False),
          (1300, 2049, 600, 40, 4, 0, False), (700, 1030, 1024, 48, 3, 64, True),
          (1, 64, 128, 8, 1, 128, False), (1, 4100, 1000, 16, 3, 32, True),
          (5, 18500, 384, 16, 3, 64, True), (13, 5000, 2050, 12, 5, 32, True),
