@@ -17,8 +17,9 @@ SOURCES = [CSRC / "gemm_nt_f16.hip", CSRC / "gemm_nt_f16_ex.hip", CSRC / "gemm_n
            CSRC / "gemm_nt_f16_noalloc.hip", CSRC / "gemm_nt_f16_acc16.hip",
            CSRC / "gemm_nt_w4.hip", CSRC / "gemm_nt_w4_f16.hip", CSRC / "gemm_nt_w4_bf16.hip",
            CSRC / "moe_nt.hip", CSRC / "moe_nt_f16.hip", CSRC / "moe_nt_bf16.hip",
-           CSRC / "moe_gate.hip", CSRC / "rms_norm.hip", CSRC / "gemm_nt_f16_add.hip", CSRC / "gemm_nt_bf16_add.hip",
-           CSRC / "lora_nt.hip", CSRC / "lora_nt_f16.hip", CSRC / "lora_nt_bf16.hip"]
+           CSRC / "moe_gate.hip", CSRC / "rms_norm.hip", CSRC / "gemm_nt_f16_add.hip",
+           CSRC / "gemm_nt_bf16_add.hip", CSRC / "lora_nt.hip", CSRC / "lora_nt_f16.hip",
+           CSRC / "lora_nt_bf16.hip"]
 HEADERS = [*CSRC.glob("*.h"), *(ROOT / "include").glob("*.h")]
 LIB = PKG / "libgemm18.so"
 
